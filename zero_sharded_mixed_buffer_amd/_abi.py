@@ -21,6 +21,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libzs.so")
 
 ZS_BF16, ZS_FP16, ZS_FP32 = 0, 1, 2
+ZS_E4M3, ZS_INT8 = 0, 1
 STATUS = {0: "ZS_OK", -1: "ZS_EINVAL", -2: "ZS_EHIP", -3: "ZS_ENOMEM", -4: "ZS_EUNSUPPORTED"}
 
 
@@ -51,6 +52,11 @@ class StateHost(ctypes.Structure):
 
     def as_dict(self):
         return {k: getattr(self, k) for k, _ in self._fields_ if k != "reserved"}
+
+
+class ActArrays(ctypes.Structure):
+    """zs_act: a checkpoint's arrays and code."""
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("code", c_int32), ("reserved", c_int32)]
 
 
 _lib = None
@@ -88,6 +94,18 @@ _SIGS = {
     "zs_probe_copy": [c_void_p, c_void_p, c_int64, c_void_p],
     "zs_probe_read": [c_void_p, c_int64, c_void_p, c_void_p],
     "zs_probe_write": [c_void_p, c_int64, c_void_p],
+    "zs_act_size": [c_int64, c_int64, c_void_p, c_void_p],
+    "zs_act_pack": [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p],
+    "zs_act_unpack": [c_void_p, c_int64, c_int64, c_void_p, c_int32, c_int64, c_void_p],
+    "zs_rmsnorm": [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32, c_int64, c_int64, c_double, c_void_p,
+                   c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p],
+    "zs_rmsnorm_workspace": [c_int64, c_int64, c_void_p],
+    "zs_rmsnorm_backward": [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
+                            c_int32, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_void_p,
+                            c_int64, c_void_p],
+    "zs_act_wgrad_workspace": [c_int64, c_int64, c_int64, c_void_p],
+    "zs_act_wgrad": [c_void_p, c_int64, c_int64, c_void_p, c_int32, c_int64, c_int64, c_void_p, c_int32, c_int64,
+                     c_int32, c_void_p, c_void_p, c_int64, c_void_p],
     "zs_offload_adamw_step": [c_void_p, c_void_p, c_int32, c_void_p, POINTER(AdamwHParams), c_void_p, c_void_p,
                               c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p],
 }
@@ -418,3 +436,71 @@ def zs_probe_read(src, nbytes, sink, stream=None):
 def zs_probe_write(dst, nbytes, stream=None):
     w = "zs_probe_write"
     _check(lib().zs_probe_write(_dptr(dst, "dst", w), int(nbytes), _stream(stream)), w)
+
+
+# ---------------------------------------------------------------------------- activation operators
+# (include/zs_act.h; a checkpoint argument is an ActArrays, or None)
+
+def _act(a):
+    return None if a is None else ctypes.addressof(a)
+
+
+def zs_act_size(rows, cols):
+    """Returns (codes_bytes, scales_bytes) of a rows x cols checkpoint."""
+    a, b = c_int64(), c_int64()
+    _check(lib().zs_act_size(rows, cols, ctypes.addressof(a), ctypes.addressof(b)), "zs_act_size")
+    return a.value, b.value
+
+
+def zs_act_pack(src, src_dtype, src_stride, rows, cols, act, stream=None):
+    w = "zs_act_pack"
+    _check(lib().zs_act_pack(_dptr(src, "src", w), dtype_code(src_dtype), src_stride, rows, cols, _act(act),
+                             _stream(stream)), w)
+
+
+def zs_act_unpack(act, rows, cols, dst, dst_dtype, dst_stride, stream=None):
+    w = "zs_act_unpack"
+    _check(lib().zs_act_unpack(_act(act), rows, cols, _dptr(dst, "dst", w), dtype_code(dst_dtype), dst_stride,
+                               _stream(stream)), w)
+
+
+def zs_rmsnorm(x, x_stride, residual, residual_stride, weight, dtype, rows, cols, eps, h=None, h_stride=0, y=None,
+               y_stride=0, y8=None, h8=None, rstd=None, stream=None):
+    w = "zs_rmsnorm"
+    _check(lib().zs_rmsnorm(_dptr(x, "x", w), x_stride, _dptr(residual, "residual", w), residual_stride,
+                            _dptr(weight, "weight", w), dtype_code(dtype), rows, cols, eps, _dptr(h, "h", w), h_stride,
+                            _dptr(y, "y", w), y_stride, _act(y8), _act(h8), _dptr(rstd, "rstd", w), _stream(stream)), w)
+
+
+def zs_rmsnorm_workspace(rows, cols):
+    """Bytes of zs_rmsnorm_backward's workspace."""
+    n = c_int64()
+    _check(lib().zs_rmsnorm_workspace(rows, cols, ctypes.addressof(n)), "zs_rmsnorm_workspace")
+    return n.value
+
+
+def zs_rmsnorm_backward(dy, dy_stride, dh, dh_stride, h, h_stride, h8, weight, rstd, dtype, rows, cols, dx, dx_stride,
+                        dweight=None, dweight_dtype=ZS_FP32, base=None, workspace=None, workspace_bytes=0,
+                        stream=None):
+    w = "zs_rmsnorm_backward"
+    _check(lib().zs_rmsnorm_backward(_dptr(dy, "dy", w), dy_stride, _dptr(dh, "dh", w), dh_stride, _dptr(h, "h", w),
+                                     h_stride, _act(h8), _dptr(weight, "weight", w), _dptr(rstd, "rstd", w),
+                                     dtype_code(dtype), rows, cols, _dptr(dx, "dx", w), dx_stride,
+                                     _dptr(dweight, "dweight", w), dtype_code(dweight_dtype), _dptr(base, "base", w),
+                                     _dptr(workspace, "workspace", w), workspace_bytes, _stream(stream)), w)
+
+
+def zs_act_wgrad_workspace(rows, cols, outs):
+    """Bytes of zs_act_wgrad's workspace."""
+    n = c_int64()
+    _check(lib().zs_act_wgrad_workspace(rows, cols, outs, ctypes.addressof(n)), "zs_act_wgrad_workspace")
+    return n.value
+
+
+def zs_act_wgrad(x8, rows, cols, dy, dy_dtype, dy_stride, outs, dw, dw_dtype, dw_stride, in_major=False, base=None,
+                 workspace=None, workspace_bytes=0, stream=None):
+    w = "zs_act_wgrad"
+    _check(lib().zs_act_wgrad(_act(x8), rows, cols, _dptr(dy, "dy", w), dtype_code(dy_dtype), dy_stride, outs,
+                              _dptr(dw, "dw", w), dtype_code(dw_dtype), dw_stride, int(bool(in_major)),
+                              _dptr(base, "base", w), _dptr(workspace, "workspace", w), workspace_bytes,
+                              _stream(stream)), w)

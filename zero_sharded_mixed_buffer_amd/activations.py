@@ -1,0 +1,380 @@
+"""Tensor-level calls of the activation operators (include/zs_act.h) and their autograd form.
+
+What a training program keeps between forward and backward, at 1.03 bytes per element, and the
+gradients that backward then writes into the optimizer's gradient buffer:
+
+    Act8                         an 8-bit checkpoint of a rows x cols matrix
+    act_pack, act_unpack         write a checkpoint, read it back
+    rmsnorm, rmsnorm_backward    the norm with the residual's addition; it writes checkpoints of
+                                 its output and of its input in the same pass
+    act_wgrad                    a linear layer's weight gradient from its input's checkpoint
+    norm, linear                 the same under autograd
+
+The functions work on the current stream of their tensors' device, write into the tensors they
+are given, allocate nothing but a workspace that was not passed in, and never wait for the GPU.
+A wrong type, shape, stride or device is a ValueError before anything is enqueued.
+"""
+
+from __future__ import annotations
+
+import contextlib
+from collections import namedtuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _abi as A
+
+GROUP = 32
+CODES = {"e4m3": A.ZS_E4M3, "int8": A.ZS_INT8}
+HALF = (torch.bfloat16, torch.float16)
+_DTYPES = {torch.bfloat16: A.ZS_BF16, torch.float16: A.ZS_FP16, torch.float32: A.ZS_FP32}
+
+
+class Act8:
+    """An 8-bit checkpoint: `codes`, uint8 [rows, cols rounded up to a multiple of 32], and
+    `scales`, uint8 [rows, groups of 32], both contiguous on one GPU; `code` is "e4m3" or
+    "int8".  The arrays are the caller's, or Act8.empty's."""
+
+    __slots__ = ("codes", "scales", "rows", "cols", "code", "device", "arrays")
+
+    def __init__(self, codes, scales, cols, code="e4m3"):
+        if code not in CODES:
+            raise ValueError(f"code is 'e4m3' or 'int8', not {code!r}")
+        cols = int(cols)
+        if cols < 1:
+            raise ValueError("cols must be positive")
+        groups = -(-cols // GROUP)
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise ValueError("codes and scales must be uint8")
+        rows = codes.shape[0] if codes.dim() else -1
+        if codes.shape != (rows, groups * GROUP) or scales.shape != (rows, groups):
+            raise ValueError(f"a checkpoint of {cols} columns holds codes [rows, {groups * GROUP}] and scales "
+                             f"[rows, {groups}], got {tuple(codes.shape)} and {tuple(scales.shape)}")
+        if not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes and scales must be contiguous")
+        if codes.device != scales.device:
+            raise ValueError(f"codes are on {codes.device}, scales on {scales.device}")
+        if codes.data_ptr() % 16:
+            raise ValueError("codes must be 16-byte aligned")
+        self.codes, self.scales, self.rows, self.cols, self.code = codes, scales, rows, cols, code
+        self.device = codes.device
+        self.arrays = A.ActArrays(codes.data_ptr(), scales.data_ptr(), CODES[code], 0)
+
+    @classmethod
+    def empty(cls, rows, cols, code="e4m3", device="cuda"):
+        """A checkpoint with newly allocated, unwritten arrays."""
+        groups = -(-int(cols) // GROUP)
+        return cls(torch.empty(int(rows), groups * GROUP, dtype=torch.uint8, device=device),
+                   torch.empty(int(rows), groups, dtype=torch.uint8, device=device), cols, code)
+
+    @classmethod
+    def of(cls, x, code="e4m3"):
+        """The checkpoint of a matrix (bf16, fp16 or fp32)."""
+        act = cls.empty(x.shape[0], x.shape[1], code, x.device)
+        act_pack(x, act)
+        return act
+
+    def unpack(self, dtype=torch.bfloat16):
+        """The matrix it stands for, in a new tensor."""
+        out = torch.empty(self.rows, self.cols, dtype=dtype, device=self.device)
+        act_unpack(self, out)
+        return out
+
+    @property
+    def nbytes(self):
+        return self.codes.numel() + self.scales.numel()
+
+
+def _need_gpu(device):
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must live on a GPU, not on {device}")
+
+
+def _on(device):
+    """The device as the current one (a no-op when it is already)."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _matrix(t, what, dtype, rows, cols, device):
+    """Check a matrix argument; returns its row stride."""
+    if t.dtype != dtype:
+        raise ValueError(f"{what} is {t.dtype}, not {dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    if t.device != device:
+        raise ValueError(f"{what} lives on {t.device}, not on {device}")
+    row, col = t.stride()
+    if cols > 1 and col != 1:
+        raise ValueError(f"{what}: the columns must be consecutive (its stride is {t.stride()})")
+    return row
+
+
+def _vector(t, what, dtypes, n, device):
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} is {t.dtype}, not one of {dtypes}")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous vector of {n} elements")
+    if t.device != device:
+        raise ValueError(f"{what} lives on {t.device}, not on {device}")
+    return t
+
+
+def _checkpoint(act, what, rows, cols, device):
+    if (act.rows, act.cols) != (rows, cols):
+        raise ValueError(f"{what} is a checkpoint of {act.rows} x {act.cols}, not of {rows} x {cols}")
+    if act.device != device:
+        raise ValueError(f"{what} lives on {act.device}, not on {device}")
+    return act.arrays
+
+
+def _input(t, what, dtypes):
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{what} must be a matrix with at least one column, got shape {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} is {t.dtype}, not one of {dtypes}")
+    _need_gpu(t.device)
+    return t.shape[0], t.shape[1], t.device
+
+
+def _workspace(workspace, need, device):
+    """The caller's workspace (any contiguous tensor), or a new one: allocated on the current
+    stream, so the caching allocator hands it out again only after this call's kernels."""
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    have = workspace.numel() * workspace.element_size()
+    if have < need:
+        raise ValueError(f"workspace holds {have} bytes, {need} are needed")
+    return workspace, have
+
+
+def act_pack(x, act):
+    """Write the checkpoint of matrix x (bf16, fp16 or fp32; any row stride) into `act`."""
+    rows, cols, dev = _input(x, "x", _DTYPES)
+    stride = _matrix(x, "x", x.dtype, rows, cols, dev)
+    arrays = _checkpoint(act, "act", rows, cols, dev)
+    with _on(dev):
+        A.zs_act_pack(x, _DTYPES[x.dtype], stride, rows, cols, arrays, _stream(dev))
+
+
+def act_unpack(act, out):
+    """Read a checkpoint back into matrix `out` (bf16, fp16 or fp32; any row stride)."""
+    rows, cols, dev = _input(out, "out", _DTYPES)
+    stride = _matrix(out, "out", out.dtype, rows, cols, dev)
+    arrays = _checkpoint(act, "act", rows, cols, dev)
+    with _on(dev):
+        A.zs_act_unpack(arrays, rows, cols, out, _DTYPES[out.dtype], stride, _stream(dev))
+
+
+def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, y8=None, h8=None, rstd=None):
+    """h = x + residual, rstd = (mean(h^2) + eps)^-1/2 per row, y = h * rstd * weight, in one
+    pass; every output that is given is written: h, y (matrices of x's dtype), y8, h8
+    (checkpoints of y and h), rstd (fp32 vector).  h may be x or residual itself."""
+    rows, cols, dev = _input(x, "x", HALF)
+    dt = x.dtype
+    xs = _matrix(x, "x", dt, rows, cols, dev)
+    _vector(weight, "weight", (dt,), cols, dev)
+    rs = _matrix(residual, "residual", dt, rows, cols, dev) if residual is not None else 0
+    hs = _matrix(h, "h", dt, rows, cols, dev) if h is not None else 0
+    ys = _matrix(y, "y", dt, rows, cols, dev) if y is not None else 0
+    if h is not None and y is not None and rows and h.data_ptr() == y.data_ptr():
+        raise ValueError("h and y are the same memory")
+    if rstd is not None:
+        _vector(rstd, "rstd", (torch.float32,), rows, dev)
+    ya = _checkpoint(y8, "y8", rows, cols, dev) if y8 is not None else None
+    ha = _checkpoint(h8, "h8", rows, cols, dev) if h8 is not None else None
+    with _on(dev):
+        A.zs_rmsnorm(x, xs, residual, rs, weight, _DTYPES[dt], rows, cols, eps, h, hs, y, ys, ya, ha, rstd,
+                     _stream(dev))
+
+
+def rmsnorm_backward(dy, saved, weight, rstd, dx, dh=None, dweight=None, base=None, workspace=None):
+    """Backward of rmsnorm: dx = the gradient of x (and of the residual) from dy and, if it is
+    given, dh, the gradient that reaches h by other ways; dweight (bf16, fp16 or fp32) = base +
+    the weight's gradient.  `saved` is h or its Act8.  base may be dweight itself: the gradient
+    is then added to what is there.  dx may be dy or dh."""
+    rows, cols, dev = _input(dy, "dy", HALF)
+    dt = dy.dtype
+    dys = _matrix(dy, "dy", dt, rows, cols, dev)
+    dxs = _matrix(dx, "dx", dt, rows, cols, dev)
+    dhs = _matrix(dh, "dh", dt, rows, cols, dev) if dh is not None else 0
+    _vector(weight, "weight", (dt,), cols, dev)
+    _vector(rstd, "rstd", (torch.float32,), rows, dev)
+    h, hs, h8 = None, 0, None
+    if isinstance(saved, Act8):
+        h8 = _checkpoint(saved, "saved", rows, cols, dev)
+    else:
+        h, hs = saved, _matrix(saved, "saved", dt, rows, cols, dev)
+    size = 0
+    if dweight is not None:
+        _vector(dweight, "dweight", tuple(_DTYPES), cols, dev)
+        if base is not None:
+            _vector(base, "base", (dweight.dtype,), cols, dev)
+        workspace, size = _workspace(workspace, A.zs_rmsnorm_workspace(rows, cols), dev)
+    elif base is not None:
+        raise ValueError("base without dweight")
+    with _on(dev):
+        A.zs_rmsnorm_backward(dy, dys, dh, dhs, h, hs, h8, weight, rstd, _DTYPES[dt], rows, cols, dx, dxs, dweight,
+                              _DTYPES[dweight.dtype] if dweight is not None else A.ZS_FP32, base, workspace, size,
+                              _stream(dev))
+
+
+def act_wgrad(x8, dy, dw, base=None, in_major=False, workspace=None):
+    """dw = base + dy^T x: the weight gradient of y = x W^T from the checkpoint of x and the
+    gradient dy [rows, outs] of y.  dw is [outs, cols], or [cols, outs] with in_major (weights
+    kept as (in, out)), in dy's dtype or fp32; base has dw's dtype, shape and stride and may be
+    dw itself: the gradient is then added to what is there."""
+    rows, outs, dev = _input(dy, "dy", HALF)
+    dys = _matrix(dy, "dy", dy.dtype, rows, outs, dev)
+    arrays = _checkpoint(x8, "x8", rows, x8.cols, dev)
+    shape = (x8.cols, outs) if in_major else (outs, x8.cols)
+    if dw.dtype not in (dy.dtype, torch.float32):
+        raise ValueError(f"dw is {dw.dtype}, not {dy.dtype} or torch.float32")
+    dws = _matrix(dw, "dw", dw.dtype, *shape, dev)
+    if base is not None and _matrix(base, "base", dw.dtype, *shape, dev) != dws and shape[0] > 1:
+        raise ValueError("base and dw must have the same strides")
+    workspace, size = _workspace(workspace, A.zs_act_wgrad_workspace(rows, x8.cols, outs), dev)
+    with _on(dev):
+        A.zs_act_wgrad(arrays, rows, x8.cols, dy, _DTYPES[dy.dtype], dys, outs, dw, _DTYPES[dw.dtype], dws, in_major,
+                       base, workspace, size, _stream(dev))
+
+
+# ------------------------------------------------------------------------------ autograd
+
+NormOutput = namedtuple("NormOutput", ["y", "h", "y8"])
+
+
+def _rows(t):
+    """A tensor's last dimension as matrix columns, copied only if that takes it."""
+    m = t.reshape(-1, t.shape[-1])
+    return m if m.shape[1] == 1 or m.stride(1) == 1 else m.contiguous()
+
+
+def _check_grad_into(grad_into, weight):
+    if grad_into is None:
+        return
+    if grad_into.shape != weight.shape or not grad_into.is_contiguous() or grad_into.device != weight.device:
+        raise ValueError(f"grad_into must be contiguous with the weight's shape {tuple(weight.shape)} on its device")
+    if grad_into.dtype not in (weight.dtype, torch.float32):
+        raise ValueError("grad_into has the weight's dtype or fp32")
+    if grad_into.requires_grad:
+        raise ValueError("grad_into is a plain buffer, without requires_grad")
+
+
+class _Norm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, save, y8, grad_into):
+        ctx.set_materialize_grads(False)
+        x2 = _rows(x)
+        rows, cols = x2.shape
+        y = torch.empty(rows, cols, dtype=x.dtype, device=x.device)
+        h = torch.empty_like(y) if residual is not None else None
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        h8 = Act8.empty(rows, cols, save, x.device) if save is not None else None
+        rmsnorm(x2, weight, eps, residual=_rows(residual) if residual is not None else None, h=h, y=y, y8=y8, h8=h8,
+                rstd=rstd)
+        ctx.save, ctx.cols, ctx.grad_into, ctx.two = save, cols, grad_into, residual is not None
+        out = y.view(x.shape)
+        sum_ = h.view(x.shape) if h is not None else None
+        if h8 is not None:
+            ctx.save_for_backward(weight, rstd, h8.codes, h8.scales)
+        else:
+            ctx.save_for_backward(weight, rstd, sum_ if sum_ is not None else x)
+        return (out, sum_) if ctx.two else out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        weight, rstd, *kept = ctx.saved_tensors
+        if dy is None:
+            return dh, dh if ctx.two else None, None, None, None, None, None
+        saved = Act8(kept[0], kept[1], ctx.cols, ctx.save) if ctx.save is not None else _rows(kept[0])
+        dy2 = _rows(dy)
+        dx = torch.empty(dy2.shape, dtype=dy.dtype, device=dy.device)
+        into, dweight = ctx.grad_into, None
+        if ctx.needs_input_grad[2]:
+            dweight = torch.empty_like(weight) if into is None else into
+        rmsnorm_backward(dy2, saved, weight, rstd, dx, dh=_rows(dh) if dh is not None else None, dweight=dweight,
+                         base=into if dweight is not None else None)
+        dx = dx.view(dy.shape)
+        return (dx, dx if ctx.two else None, dweight if into is None else None, None, None, None, None)
+
+
+def norm(x, weight, eps=1e-6, residual=None, save="e4m3", y8=None, grad_into=None):
+    """rmsnorm under autograd, for x [..., cols]: returns NormOutput(y, h, y8).
+
+    h is x + residual (x itself without one) and carries gradients like y.  save: what backward
+    keeps of h: its checkpoint ("e4m3" or "int8"), or None for h in 16 bits.  y8: "e4m3" or
+    "int8" writes the checkpoint of y in the same pass, for the linear layers that read y.
+    grad_into: a buffer of the weight's shape (its dtype or fp32; with flat_views the weight's
+    .grad) that backward adds the weight's gradient to; the weight then receives none from
+    autograd.
+
+    To capture forward and backward into a graph, let no eager graph of the same leaves be
+    alive: autograd would join their streams in the capture."""
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+        raise ValueError("residual must have x's shape and dtype")
+    if x.dim() < 1 or x.dtype not in HALF:
+        raise ValueError("x must be a bf16 or fp16 tensor")
+    _need_gpu(x.device)
+    _check_grad_into(grad_into, weight)
+    if save is not None and save not in CODES:
+        raise ValueError(f"save is 'e4m3', 'int8' or None, not {save!r}")
+    cols = x.shape[-1]
+    act = Act8.empty(x.numel() // max(cols, 1), cols, y8, x.device) if y8 is not None else None
+    out = _Norm.apply(x, residual, weight, eps, save, act, grad_into)
+    y, h = out if residual is not None else (out, x)
+    return NormOutput(y, h, act)
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, x8, grad_into):
+        ctx.save_for_backward(weight, x8.codes, x8.scales)
+        ctx.code, ctx.cols, ctx.grad_into = x8.code, x8.cols, grad_into
+        return torch.nn.functional.linear(x, weight)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        weight, codes, scales = ctx.saved_tensors
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = torch.matmul(dy.contiguous(), weight)
+        if ctx.needs_input_grad[1]:
+            into = ctx.grad_into
+            target = torch.empty_like(weight) if into is None else into
+            act_wgrad(Act8(codes, scales, ctx.cols, ctx.code), _rows(dy), target, base=into)
+            dw = target if into is None else None
+        return dx, dw, None, None
+
+
+def linear(x, weight, x8=None, code="e4m3", grad_into=None):
+    """y = x W^T under autograd, for x [..., cols] and weight [outs, cols], keeping an 8-bit
+    checkpoint of x for the weight's gradient instead of x.
+
+    x8: the checkpoint of x if there is one already (norm's y8: several layers that read one
+    tensor share it); otherwise it is taken here, with `code`.  grad_into: as for norm."""
+    if x.dim() < 1 or x.dtype not in HALF or weight.dtype != x.dtype or weight.dim() != 2:
+        raise ValueError("x and a weight of two dimensions must have one dtype, bf16 or fp16")
+    if x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"x has {x.shape[-1]} columns, the weight {weight.shape[1]}")
+    if not weight.is_contiguous():
+        raise ValueError("the weight must be contiguous")
+    _need_gpu(x.device)
+    if weight.device != x.device:
+        raise ValueError(f"the weight lives on {weight.device}, not on {x.device}")
+    _check_grad_into(grad_into, weight)
+    if x8 is None:
+        x8 = Act8.of(_rows(x.detach()), code)
+    else:
+        _checkpoint(x8, "x8", x.numel() // x.shape[-1], x.shape[-1], x.device)
+    return _Linear.apply(x, weight, x8, grad_into)

@@ -15,9 +15,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libzs.so")
 
-SOURCES = ["zs_abi.cpp", "zs_kernels.hip", "zs_probe.hip"]
+SOURCES = ["zs_abi.cpp", "zs_kernels.hip", "zs_probe.hip", "zs_act.hip", "zs_wgrad.hip"]
 HOST_SOURCES = ["zs_host.cpp", "zs_plan.cpp"]  # plain C++ (host step, planner), built by the host compiler
-HEADERS = ["zs_internal.h", "zs_host.h", "zs_plan.h"]
+HEADERS = ["zs_internal.h", "zs_host.h", "zs_plan.h", "zs_act_dev.h"]
 
 # Packed fp32 vector ops are disabled for all device code; fp contraction is left to the
 # sources, which switch it off where an fp64 expression must round like its plain form.

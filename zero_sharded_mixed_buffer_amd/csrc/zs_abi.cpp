@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "zs.h"
+#include "zs_act.h"
 #include "zs_host.h"
 #include "zs_probe.h"
 #include "zs_internal.h"
@@ -908,4 +909,262 @@ extern "C" zs_status zs_probe_write(void* dst, int64_t bytes, void* stream) {
   if (st != ZS_OK) return st;
   hipError_t e = zs::launch_probe_write(dst, bytes, as_stream(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "launching the write probe");
+}
+
+// ---------------------------------------------------------------------------- activation operators
+
+namespace {
+
+// Sizes are bounded so that no byte offset of any array leaves 63 bits.
+constexpr int64_t kMaxExtent = int64_t(1) << 40;
+constexpr int64_t kMaxBytes = int64_t(1) << 62;
+
+zs_status check_sizes(int64_t rows, int64_t cols) {
+  if (rows < 0) return fail(ZS_EINVAL, "rows is negative");
+  if (cols < 1) return fail(ZS_EINVAL, "cols must be positive");
+  if (rows > kMaxExtent || cols > kMaxExtent || (rows > 0 && cols + zs::kActPad > kMaxBytes / rows))
+    return fail(ZS_EINVAL, "rows x cols is too large");
+  return ok();
+}
+
+// A matrix argument: pointer, row stride, element alignment.  `what` names it.
+zs_status check_matrix(const void* p, int64_t stride, int dt, int64_t rows, int64_t cols, const char* what) {
+  if (p == nullptr && rows > 0) return fail(ZS_EINVAL, "%s is NULL", what);
+  if (rows > 1 && stride < cols) return fail(ZS_EINVAL, "%s: the row stride is smaller than a row", what);
+  if (rows > 1 && stride > kMaxBytes / 4 / rows) return fail(ZS_EINVAL, "%s: the row stride is too large", what);
+  if (!grad_aligned(p, dt)) return fail(ZS_EINVAL, "%s must be aligned to its elements", what);
+  return ok();
+}
+
+zs_status check_act(const zs_act* a, int64_t rows, const char* what) {
+  if (a == nullptr) return fail(ZS_EINVAL, "%s is NULL", what);
+  if (a->code != ZS_E4M3 && a->code != ZS_INT8) return fail(ZS_EINVAL, "%s: unknown code %d", what, a->code);
+  if (rows > 0 && (a->codes == nullptr || a->scales == nullptr))
+    return fail(ZS_EINVAL, "%s: codes or scales is NULL", what);
+  if (!aligned16(a->codes)) return fail(ZS_EINVAL, "%s: codes must be 16-byte aligned", what);
+  return ok();
+}
+
+zs::Act as_act(const zs_act* a) {
+  if (a == nullptr) return {nullptr, nullptr, 0};
+  return {static_cast<uint8_t*>(a->codes), static_cast<uint8_t*>(a->scales), a->code};
+}
+
+zs_status check_workspace(const void* p, int64_t have, int64_t need) {
+  if (p == nullptr) return fail(ZS_EINVAL, "workspace is NULL");
+  if (!aligned16(p)) return fail(ZS_EINVAL, "workspace must be 16-byte aligned");
+  if (have < need)
+    return fail(ZS_EINVAL, "workspace holds %lld bytes, %lld are needed", static_cast<long long>(have),
+                static_cast<long long>(need));
+  return ok();
+}
+
+// rows x cols as one launch of the pack and unpack kernels.
+zs_status check_chunks(int64_t rows, int64_t cols) {
+  if (rows > 0 && zs::act_padded(cols) / 8 > zs::kActMaxChunks / rows)
+    return fail(ZS_EINVAL, "rows x cols exceeds one launch");
+  if (zs::act_padded(cols) / 8 > (int64_t(1) << 31)) return fail(ZS_EINVAL, "cols exceeds one launch");
+  return ok();
+}
+
+zs_status check_norm_sizes(int64_t rows, int64_t cols) {
+  zs_status st = check_sizes(rows, cols);
+  if (st != ZS_OK) return st;
+  if (cols > zs::kNormMaxCols)
+    return fail(ZS_EINVAL, "the norm takes rows of at most %lld columns", static_cast<long long>(zs::kNormMaxCols));
+  if (rows > zs::rmsnorm_max_rows(cols))
+    return fail(ZS_EINVAL, "rows exceeds one launch");
+  return ok();
+}
+
+int64_t norm_workspace(int64_t rows, int64_t cols) {
+  return std::max<int64_t>(16, zs::rmsnorm_partials(rows, cols) * round_up(cols, 8) * int64_t(sizeof(float)));
+}
+
+}  // namespace
+
+extern "C" zs_status zs_act_size(int64_t rows, int64_t cols, int64_t* codes_bytes, int64_t* scales_bytes) {
+  if (codes_bytes == nullptr || scales_bytes == nullptr) return fail(ZS_EINVAL, "an output is NULL");
+  zs_status st = check_sizes(rows, cols);
+  if (st != ZS_OK) return st;
+  *codes_bytes = rows * zs::act_padded(cols);
+  *scales_bytes = *codes_bytes / zs::kActPad;
+  return ok();
+}
+
+extern "C" zs_status zs_act_pack(const void* src, zs_dtype src_dtype, int64_t src_stride, int64_t rows, int64_t cols,
+                                 const zs_act* act, void* stream) {
+  const TraceRange trace("zs_act_pack");
+  if (!is_grad_dtype(src_dtype)) return fail(ZS_EINVAL, "src_dtype must be bf16, fp16 or fp32");
+  zs_status st = check_sizes(rows, cols);
+  if (st == ZS_OK) st = check_chunks(rows, cols);
+  if (st == ZS_OK) st = check_matrix(src, src_stride, src_dtype, rows, cols, "src");
+  if (st == ZS_OK) st = check_act(act, rows, "act");
+  if (st != ZS_OK) return st;
+  hipError_t e = zs::launch_act_pack(src, src_dtype, src_stride, rows, cols, as_act(act), as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the checkpoint pack");
+}
+
+extern "C" zs_status zs_act_unpack(const zs_act* act, int64_t rows, int64_t cols, void* dst, zs_dtype dst_dtype,
+                                   int64_t dst_stride, void* stream) {
+  const TraceRange trace("zs_act_unpack");
+  if (!is_grad_dtype(dst_dtype)) return fail(ZS_EINVAL, "dst_dtype must be bf16, fp16 or fp32");
+  zs_status st = check_sizes(rows, cols);
+  if (st == ZS_OK) st = check_chunks(rows, cols);
+  if (st == ZS_OK) st = check_matrix(dst, dst_stride, dst_dtype, rows, cols, "dst");
+  if (st == ZS_OK) st = check_act(act, rows, "act");
+  if (st != ZS_OK) return st;
+  hipError_t e = zs::launch_act_unpack(as_act(act), rows, cols, dst, dst_dtype, dst_stride, as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the checkpoint unpack");
+}
+
+extern "C" zs_status zs_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                const void* weight, zs_dtype dtype, int64_t rows, int64_t cols, double eps, void* h,
+                                int64_t h_stride, void* y, int64_t y_stride, const zs_act* y8, const zs_act* h8,
+                                float* rstd, void* stream) {
+  const TraceRange trace("zs_rmsnorm");
+  if (!is_half_dtype(dtype)) return fail(ZS_EINVAL, "dtype must be bf16 or fp16");
+  zs_status st = check_norm_sizes(rows, cols);
+  if (st == ZS_OK) st = check_matrix(x, x_stride, dtype, rows, cols, "x");
+  if (st == ZS_OK && residual != nullptr) st = check_matrix(residual, residual_stride, dtype, rows, cols, "residual");
+  if (st == ZS_OK && h != nullptr) st = check_matrix(h, h_stride, dtype, rows, cols, "h");
+  if (st == ZS_OK && y != nullptr) st = check_matrix(y, y_stride, dtype, rows, cols, "y");
+  if (st == ZS_OK && y8 != nullptr) st = check_act(y8, rows, "y8");
+  if (st == ZS_OK && h8 != nullptr) st = check_act(h8, rows, "h8");
+  if (st != ZS_OK) return st;
+  if (weight == nullptr) return fail(ZS_EINVAL, "weight is NULL");
+  if (!grad_aligned(weight, dtype)) return fail(ZS_EINVAL, "weight must be aligned to its elements");
+  if (!grad_aligned(rstd, ZS_FP32)) return fail(ZS_EINVAL, "rstd must be aligned to its elements");
+  if (h == nullptr && y == nullptr && y8 == nullptr && h8 == nullptr && rstd == nullptr)
+    return fail(ZS_EINVAL, "no output: h, y, y8, h8 and rstd are all NULL");
+  if (!(eps >= 1.17549435e-38) || !(eps <= 3.4e38)) return fail(ZS_EINVAL, "eps must be a normal fp32 number above 0");
+  zs::NormArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.weight = static_cast<const uint16_t*>(weight);
+  a.h = static_cast<uint16_t*>(h);
+  a.y = static_cast<uint16_t*>(y);
+  a.rstd = rstd;
+  a.x_stride = x_stride;
+  a.residual_stride = residual_stride;
+  a.h_stride = h_stride;
+  a.y_stride = y_stride;
+  a.y8 = as_act(y8);
+  a.h8 = as_act(h8);
+  a.rows = rows;
+  a.cols = static_cast<int32_t>(cols);
+  a.eps = eps;
+  hipError_t e = zs::launch_rmsnorm(a, dtype, as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the norm");
+}
+
+extern "C" zs_status zs_rmsnorm_workspace(int64_t rows, int64_t cols, int64_t* bytes) {
+  if (bytes == nullptr) return fail(ZS_EINVAL, "bytes is NULL");
+  zs_status st = check_norm_sizes(rows, cols);
+  if (st != ZS_OK) return st;
+  *bytes = norm_workspace(rows, cols);
+  return ok();
+}
+
+extern "C" zs_status zs_rmsnorm_backward(const void* dy, int64_t dy_stride, const void* dh, int64_t dh_stride,
+                                         const void* h, int64_t h_stride, const zs_act* h8, const void* weight,
+                                         const float* rstd, zs_dtype dtype, int64_t rows, int64_t cols, void* dx,
+                                         int64_t dx_stride, void* dweight, zs_dtype dweight_dtype, const void* base,
+                                         void* workspace, int64_t workspace_bytes, void* stream) {
+  const TraceRange trace("zs_rmsnorm_backward");
+  if (!is_half_dtype(dtype)) return fail(ZS_EINVAL, "dtype must be bf16 or fp16");
+  zs_status st = check_norm_sizes(rows, cols);
+  if (st == ZS_OK) st = check_matrix(dy, dy_stride, dtype, rows, cols, "dy");
+  if (st == ZS_OK && dh != nullptr) st = check_matrix(dh, dh_stride, dtype, rows, cols, "dh");
+  if (st == ZS_OK) st = check_matrix(dx, dx_stride, dtype, rows, cols, "dx");
+  if (st == ZS_OK && h != nullptr) st = check_matrix(h, h_stride, dtype, rows, cols, "h");
+  if (st == ZS_OK && h8 != nullptr) st = check_act(h8, rows, "h8");
+  if (st != ZS_OK) return st;
+  if ((h == nullptr) == (h8 == nullptr) && (rows > 0 || h != nullptr))
+    return fail(ZS_EINVAL, "exactly one of h and h8 must be given");
+  if (weight == nullptr || (rstd == nullptr && rows > 0)) return fail(ZS_EINVAL, "weight and rstd must not be NULL");
+  if (!grad_aligned(weight, dtype)) return fail(ZS_EINVAL, "weight must be aligned to its elements");
+  if (!grad_aligned(rstd, ZS_FP32)) return fail(ZS_EINVAL, "rstd must be aligned to its elements");
+  if (dweight == nullptr && base != nullptr) return fail(ZS_EINVAL, "base without dweight");
+  if (dweight != nullptr) {
+    if (!is_grad_dtype(dweight_dtype)) return fail(ZS_EINVAL, "dweight_dtype must be bf16, fp16 or fp32");
+    if (!grad_aligned(dweight, dweight_dtype) || !grad_aligned(base, dweight_dtype))
+      return fail(ZS_EINVAL, "dweight and base must be aligned to their elements");
+    st = check_workspace(workspace, workspace_bytes, norm_workspace(rows, cols));
+    if (st != ZS_OK) return st;
+  }
+  zs::NormBackwardArgs a{};
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.dh = static_cast<const uint16_t*>(dh);
+  a.h = static_cast<const uint16_t*>(h);
+  a.h8 = as_act(h8);
+  a.weight = static_cast<const uint16_t*>(weight);
+  a.rstd = rstd;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.dy_stride = dy_stride;
+  a.dh_stride = dh_stride;
+  a.h_stride = h_stride;
+  a.dx_stride = dx_stride;
+  a.rows = rows;
+  a.cols = static_cast<int32_t>(cols);
+  a.dweight = dweight;
+  a.base = base;
+  a.dweight_dt = dweight_dtype;
+  a.partials = static_cast<float*>(workspace);
+  hipError_t e = zs::launch_rmsnorm_backward(a, dtype, as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the norm's backward pass");
+}
+
+namespace {
+
+zs_status check_wgrad_sizes(int64_t rows, int64_t cols, int64_t outs, int64_t* need) {
+  zs_status st = check_sizes(rows, cols);
+  if (st == ZS_OK) st = check_sizes(rows, outs);
+  if (st == ZS_OK) st = check_sizes(outs, cols);
+  if (st != ZS_OK) return st;
+  *need = zs::wgrad_workspace(rows, cols, outs);
+  if (*need < 0) return fail(ZS_EINVAL, "outs x cols exceeds one launch");
+  return ok();
+}
+
+}  // namespace
+
+extern "C" zs_status zs_act_wgrad_workspace(int64_t rows, int64_t cols, int64_t outs, int64_t* bytes) {
+  if (bytes == nullptr) return fail(ZS_EINVAL, "bytes is NULL");
+  return check_wgrad_sizes(rows, cols, outs, bytes);
+}
+
+extern "C" zs_status zs_act_wgrad(const zs_act* x8, int64_t rows, int64_t cols, const void* dy, zs_dtype dy_dtype,
+                                  int64_t dy_stride, int64_t outs, void* dw, zs_dtype dw_dtype, int64_t dw_stride,
+                                  int32_t in_major, const void* base, void* workspace, int64_t workspace_bytes,
+                                  void* stream) {
+  const TraceRange trace("zs_act_wgrad");
+  if (!is_half_dtype(dy_dtype)) return fail(ZS_EINVAL, "dy_dtype must be bf16 or fp16");
+  if (!is_grad_dtype(dw_dtype)) return fail(ZS_EINVAL, "dw_dtype must be bf16, fp16 or fp32");
+  if (dw_dtype != dy_dtype && dw_dtype != ZS_FP32) return fail(ZS_EUNSUPPORTED, "dw_dtype must be dy's or fp32");
+  int64_t need = 0;
+  zs_status st = check_wgrad_sizes(rows, cols, outs, &need);
+  if (st == ZS_OK) st = check_act(x8, rows, "x8");
+  if (st == ZS_OK) st = check_matrix(dy, dy_stride, dy_dtype, rows, outs, "dy");
+  const int64_t dw_rows = in_major ? cols : outs, dw_cols = in_major ? outs : cols;
+  if (st == ZS_OK) st = check_matrix(dw, dw_stride, dw_dtype, dw_rows, dw_cols, "dw");
+  if (st == ZS_OK && base != nullptr) st = check_matrix(base, dw_stride, dw_dtype, dw_rows, dw_cols, "base");
+  if (st == ZS_OK) st = check_workspace(workspace, workspace_bytes, need);
+  if (st != ZS_OK) return st;
+  zs::WgradArgs a{};
+  a.x8 = as_act(x8);
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.dw = dw;
+  a.base = base;
+  a.partials = static_cast<float*>(workspace);
+  a.rows = rows;
+  a.cols = cols;
+  a.outs = outs;
+  a.dy_stride = dy_stride;
+  a.dw_stride = dw_stride;
+  a.dy_dt = dy_dtype;
+  a.dw_dt = dw_dtype;
+  a.in_major = in_major != 0;
+  hipError_t e = zs::launch_wgrad(a, as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the weight gradient");
 }

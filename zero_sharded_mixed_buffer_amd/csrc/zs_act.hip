@@ -1,0 +1,522 @@
+// gfx950 kernels of the 8-bit activation checkpoints and of the root-mean-square norm with
+// its backward pass (zs_act.h).
+//
+// All of them stream HBM.  A lane owns chunks of eight consecutive columns (one 16-byte
+// access of 2-byte data, one 8-byte access of codes), so four neighbouring lanes hold a group
+// of 32 that shares a scale, and its largest magnitude is two quad permutes away.  A row of
+// the norm stays in the registers of the lanes that own it between the statistics and the
+// outputs: every input is read once.
+
+#include "zs_act_dev.h"
+
+namespace zs {
+namespace {
+
+using namespace act;
+
+// ------------------------------------------------------------------ pack, unpack
+
+constexpr int kChunksPerThread = 4;
+constexpr int kChunksPerBlock = kThreads * kChunksPerThread;
+
+// Row and chunk of task `first + k` (k < kChunksPerBlock), chunks_per_row to a row: one 64-bit
+// division per workgroup, a 32-bit one per chunk.
+struct ChunkAt {
+  int64_t row;
+  uint32_t chunk;
+};
+__device__ __forceinline__ ChunkAt chunk_at(int64_t row0, uint32_t rem0, uint32_t k, uint32_t chunks_per_row) {
+  const uint32_t r = rem0 + k;
+  const uint32_t d = r / chunks_per_row;
+  return {row0 + d, r - d * chunks_per_row};
+}
+
+__device__ __forceinline__ int clamp_count(int64_t left) { return left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0; }
+
+// Reads 2 (or 4) bytes and writes 1.03 per element.
+template <int DT, int CODE>
+__global__ __launch_bounds__(kThreads) void k_act_pack(const void* __restrict__ src, int64_t stride, int64_t cols,
+                                                       uint32_t chunks_per_row, int64_t ntasks,
+                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const int64_t first = int64_t(blockIdx.x) * kChunksPerBlock;
+  const int64_t row0 = first / chunks_per_row;
+  const uint32_t rem0 = static_cast<uint32_t>(first - row0 * chunks_per_row);
+  float f[kChunksPerThread][8];
+#pragma unroll
+  for (int u = 0; u < kChunksPerThread; ++u) {
+    const uint32_t k = u * kThreads + threadIdx.x;
+    const ChunkAt at = chunk_at(row0, rem0, k, chunks_per_row);
+    const int cnt = first + k < ntasks ? clamp_count(cols - int64_t(at.chunk) * 8) : 0;
+    const int64_t e = at.row * stride + int64_t(at.chunk) * 8;
+    if constexpr (DT == ZS_FP32) {
+      const float* p = static_cast<const float*>(src) + e;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[u][j] = 0.0f;
+      if (cnt == 8) {
+        const v4u a = *reinterpret_cast<const v4u_a4*>(p);
+        const v4u b = *reinterpret_cast<const v4u_a4*>(p + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[u][j] = bits_f(a[j]);
+          f[u][4 + j] = bits_f(b[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+          if (j < cnt) f[u][j] = p[j];
+      }
+    } else {
+      widen8<DT>(load8h_nt(static_cast<const uint16_t*>(src) + e, cnt), f[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kChunksPerThread; ++u) {
+    const int64_t t = first + u * kThreads + threadIdx.x;
+    if (t < ntasks) encode_store<CODE>(f[u], codes, scales, t);
+  }
+}
+
+template <int DT, int CODE>
+__global__ __launch_bounds__(kThreads) void k_act_unpack(const uint8_t* __restrict__ codes,
+                                                         const uint8_t* __restrict__ scales, int64_t cols,
+                                                         uint32_t chunks_per_row, int64_t ntasks,
+                                                         void* __restrict__ dst, int64_t stride) {
+  const int64_t first = int64_t(blockIdx.x) * kChunksPerBlock;
+  const int64_t row0 = first / chunks_per_row;
+  const uint32_t rem0 = static_cast<uint32_t>(first - row0 * chunks_per_row);
+  v2u c[kChunksPerThread];
+  int b[kChunksPerThread];
+#pragma unroll
+  for (int u = 0; u < kChunksPerThread; ++u) {
+    const int64_t t = first + u * kThreads + threadIdx.x;
+    c[u] = v2u{0u, 0u};
+    b[u] = 0;
+    if (t < ntasks) {
+      c[u] = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(codes) + t);
+      b[u] = scales[t >> 2];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kChunksPerThread; ++u) {
+    const uint32_t k = u * kThreads + threadIdx.x;
+    const ChunkAt at = chunk_at(row0, rem0, k, chunks_per_row);
+    const int cnt = first + k < ntasks ? clamp_count(cols - int64_t(at.chunk) * 8) : 0;
+    if (cnt == 0) continue;
+    const int64_t e = at.row * stride + int64_t(at.chunk) * 8;
+    float f[8];
+    decode8<CODE>(c[u], scale_value(b[u]), f);
+    if constexpr (DT == ZS_FP32) {
+      float* p = static_cast<float*>(dst) + e;
+      if (cnt == 8) {
+        v4u lo, hi;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          lo[j] = f_bits(f[j]);
+          hi[j] = f_bits(f[4 + j]);
+        }
+        __builtin_nontemporal_store(lo, reinterpret_cast<v4u_a4*>(p));
+        __builtin_nontemporal_store(hi, reinterpret_cast<v4u_a4*>(p + 4));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+          if (j < cnt) p[j] = f[j];
+      }
+    } else {
+      clamp8<DT>(f);
+      store8h(static_cast<uint16_t*>(dst) + e, narrow8<DT>(f), cnt);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ norm
+
+// Sum over the LPR lanes of a row, the same in every lane: butterflies inside a wave, then
+// the waves' sums in index order through LDS.  `slot` is LDS of LPR / 64 values that no
+// earlier sum still reads.
+template <int LPR, typename T>
+__device__ __forceinline__ T row_sum(T x, T* slot) {
+  constexpr int kLanes = LPR < 64 ? LPR : 64;
+#pragma unroll
+  for (int off = kLanes / 2; off >= 1; off >>= 1) x += __shfl_xor(x, off, 64);
+  if constexpr (LPR > 64) {
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = slot[0];
+#pragma unroll
+    for (int i = 1; i < LPR / 64; ++i) x += slot[i];
+  }
+  return x;
+}
+
+template <int LPR>
+constexpr int norm_block() {
+  return LPR > kThreads ? LPR : kThreads;
+}
+
+// LPR lanes share a row, V chunks each (LPR * V * 8 >= cols).  The sum of squares is taken in
+// fp64: it neither overflows for any finite fp16 or bf16 row nor depends on the row's length,
+// and costs 16 half-rate operations per 16 bytes of the row, behind the memory's time.
+template <int DT, int LPR, int V>
+__global__ __launch_bounds__(norm_block<LPR>()) void k_rmsnorm(NormArgs a) {
+  constexpr int kBlock = norm_block<LPR>();
+  __shared__ double slot[LPR > 64 ? LPR / 64 : 1];
+  const int64_t row = int64_t(blockIdx.x) * (kBlock / LPR) + threadIdx.x / LPR;
+  const int lane = threadIdx.x % LPR;
+  const bool live = row < a.rows;
+  v4u hb[V];
+  int cnt[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int col = (v * LPR + lane) * 8;
+    cnt[v] = live ? clamp_count(a.cols - col) : 0;
+    hb[v] = load8h_nt(a.x + row * a.x_stride + col, cnt[v]);
+  }
+  if (a.residual != nullptr) {
+    v4u rb[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) rb[v] = load8h_nt(a.residual + row * a.residual_stride + (v * LPR + lane) * 8, cnt[v]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        hb[v][j] = pair_bits<DT>(lo_f<DT>(hb[v][j]) + lo_f<DT>(rb[v][j]), hi_f<DT>(hb[v][j]) + hi_f<DT>(rb[v][j]));
+    }
+  }
+  double sum = 0.0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float f[8];
+    widen8<DT>(hb[v], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += static_cast<double>(f[j]) * static_cast<double>(f[j]);
+  }
+  sum = row_sum<LPR>(sum, slot);
+  const float rstd = static_cast<float>(1.0 / sqrt(sum / a.cols + a.eps));
+  if (!live) return;
+  if (a.rstd != nullptr && lane == 0) a.rstd[row] = rstd;
+  const int64_t chunks = act_padded(a.cols) / 8;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int chunk = v * LPR + lane;
+    const int col = chunk * 8;
+    if (chunk >= chunks) continue;  // whole groups of four lanes leave together
+    float f[8];
+    widen8<DT>(hb[v], f);
+    if (a.h != nullptr) store8h(a.h + row * a.h_stride + col, hb[v], cnt[v]);
+    if (a.h8.codes != nullptr) {
+      if (a.h8.code == ZS_E4M3)
+        encode_store<ZS_E4M3>(f, a.h8.codes, a.h8.scales, row * chunks + chunk);
+      else
+        encode_store<ZS_INT8>(f, a.h8.codes, a.h8.scales, row * chunks + chunk);
+    }
+    if (a.y == nullptr && a.y8.codes == nullptr) continue;
+    float w[8];
+    widen8<DT>(load8h(a.weight + col, cnt[v]), w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j < cnt[v] ? f[j] * rstd * w[j] : 0.0f;
+    if (a.y != nullptr) store8h(a.y + row * a.y_stride + col, narrow8<DT>(f), cnt[v]);
+    if (a.y8.codes != nullptr) {
+      if (a.y8.code == ZS_E4M3)
+        encode_store<ZS_E4M3>(f, a.y8.codes, a.y8.scales, row * chunks + chunk);
+      else
+        encode_store<ZS_INT8>(f, a.y8.codes, a.y8.scales, row * chunks + chunk);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ norm, backward
+
+__device__ __forceinline__ float load_any(const void* p, int dt, int64_t i) {
+  if (dt == ZS_FP32) return static_cast<const float*>(p)[i];
+  const uint32_t b = static_cast<const uint16_t*>(p)[i];
+  return dt == ZS_BF16 ? lo_f<ZS_BF16>(b) : lo_f<ZS_FP16>(b);
+}
+__device__ __forceinline__ void store_any(void* p, int dt, int64_t i, float x) {
+  if (dt == ZS_FP32)
+    static_cast<float*>(p)[i] = x;
+  else
+    static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(dt == ZS_BF16 ? half_bits<ZS_BF16>(x) : half_bits<ZS_FP16>(x));
+}
+
+// What the norm's backward reads as h: 16-bit values, or a checkpoint of either code.
+enum Saved : int { kSaved16 = 0, kSavedE4m3 = 1, kSavedInt8 = 2 };
+
+// Workgroup b takes rows b * RPB + sub, then every (gridDim.x * RPB)-th, and keeps the sums
+// of dy * xh of its columns in registers over all of them; they leave as one row of
+// `partials`, which k_dweight adds up in row order.
+template <int DT, int SAVED, int LPR, int V>
+__global__ __launch_bounds__(norm_block<LPR>()) void k_rmsnorm_backward(NormBackwardArgs a) {
+  constexpr int kBlock = norm_block<LPR>();
+  constexpr int kRows = kBlock / LPR;
+  __shared__ float slot[2][LPR > 64 ? LPR / 64 : 1];
+  __shared__ float fold[kRows > 1 ? kRows : 1][kRows > 1 ? LPR * V * 8 : 1];
+  const int sub = threadIdx.x / LPR;
+  const int lane = threadIdx.x % LPR;
+  const int64_t chunks = act_padded(a.cols) / 8;
+  v4u w[V];
+  int width[V];
+  float acc[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int col = (v * LPR + lane) * 8;
+    width[v] = clamp_count(a.cols - col);
+    w[v] = load8h(a.weight + col, width[v]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[v][j] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t row0 = int64_t(blockIdx.x) * kRows; row0 < a.rows; row0 += int64_t(gridDim.x) * kRows, turn ^= 1) {
+    const int64_t row = row0 + sub;
+    const bool live = row < a.rows;
+    v4u dy[V], h[V], dh[V];
+    float s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int chunk = v * LPR + lane;
+      const int cnt = live ? width[v] : 0;
+      dy[v] = load8h_nt(a.dy + row * a.dy_stride + chunk * 8, cnt);
+      if constexpr (SAVED == kSaved16) {
+        h[v] = load8h_nt(a.h + row * a.h_stride + chunk * 8, cnt);
+      } else {
+        h[v] = v4u{0u, 0u, 0u, 0u};
+        int b = 0;
+        if (cnt > 0) {
+          const v2u c = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(a.h8.codes) + row * chunks + chunk);
+          h[v][0] = c[0];
+          h[v][1] = c[1];
+          b = a.h8.scales[(row * chunks + chunk) >> 2];
+        }
+        s[v] = scale_value(b);
+      }
+      dh[v] = a.dh != nullptr ? load8h_nt(a.dh + row * a.dh_stride + chunk * 8, cnt) : v4u{0u, 0u, 0u, 0u};
+    }
+    const float rstd = live ? a.rstd[row] : 0.0f;
+    float dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float xh[8], d[8], g[8];
+      if constexpr (SAVED == kSaved16)
+        widen8<DT>(h[v], xh);
+      else
+        decode8<SAVED == kSavedE4m3 ? ZS_E4M3 : ZS_INT8>(v2u{h[v][0], h[v][1]}, s[v], xh);
+      widen8<DT>(dy[v], d);
+      widen8<DT>(w[v], g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // columns past the end hold zeros everywhere, but a checkpoint's NaN scale covers them too
+        const float x = (SAVED == kSaved16 || j < width[v]) ? xh[j] * rstd : 0.0f;
+        dot += d[j] * g[j] * x;
+        acc[v][j] += d[j] * x;
+      }
+    }
+    dot = row_sum<LPR>(dot, slot[turn]);
+    const float mean = dot / static_cast<float>(a.cols);
+    if (!live) continue;
+    // The row waits for its mean in packed form: without this the compiler keeps the widened
+    // values over the reduction, at two to three times the registers.
+#pragma unroll
+    for (int v = 0; v < V; ++v) asm volatile("" : "+v"(dy[v]), "+v"(h[v]), "+v"(w[v]));
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (width[v] == 0) continue;
+      float xh[8], d[8], g[8], r[8];
+      if constexpr (SAVED == kSaved16)
+        widen8<DT>(h[v], xh);
+      else
+        decode8<SAVED == kSavedE4m3 ? ZS_E4M3 : ZS_INT8>(v2u{h[v][0], h[v][1]}, s[v], xh);
+      widen8<DT>(dy[v], d);
+      widen8<DT>(w[v], g);
+      widen8<DT>(dh[v], r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] += rstd * (d[j] * g[j] - xh[j] * rstd * mean);
+      store8h(a.dx + row * a.dx_stride + (v * LPR + lane) * 8, narrow8<DT>(r), width[v]);
+    }
+  }
+  if (a.dweight == nullptr) return;
+  const int64_t pitch = (int64_t(a.cols) + 7) / 8 * 8;
+  if constexpr (kRows > 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) fold[sub][(v * LPR + lane) * 8 + j] = acc[v][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += kBlock) {
+      float t = fold[0][c];
+#pragma unroll
+      for (int i = 1; i < kRows; ++i) t += fold[i][c];
+      if (gridDim.x == 1)
+        store_any(a.dweight, a.dweight_dt, c, t + (a.base != nullptr ? load_any(a.base, a.dweight_dt, c) : 0.0f));
+      else
+        a.partials[int64_t(blockIdx.x) * pitch + c] = t;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int col = (v * LPR + lane) * 8;
+      if (width[v] == 0) continue;
+      if (gridDim.x == 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < width[v])
+            store_any(a.dweight, a.dweight_dt, col + j,
+                      acc[v][j] + (a.base != nullptr ? load_any(a.base, a.dweight_dt, col + j) : 0.0f));
+      } else {
+        v4u lo, hi;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          lo[j] = f_bits(acc[v][j]);
+          hi[j] = f_bits(acc[v][4 + j]);
+        }
+        v4u* p = reinterpret_cast<v4u*>(a.partials + int64_t(blockIdx.x) * pitch + col);
+        p[0] = lo;
+        p[1] = hi;
+      }
+    }
+  }
+}
+
+// dweight = base + the sum of `count` partial rows, in a fixed order: eight threads share a
+// column, each adding every eighth row, then the eight sums in index order, in fp64.
+constexpr int kFoldCols = 32;
+__global__ __launch_bounds__(kThreads) void k_dweight(const float* __restrict__ partials, int64_t count, int64_t pitch,
+                                                      int32_t cols, void* dweight, int dt, const void* base) {
+  constexpr int kSlices = kThreads / kFoldCols;
+  __shared__ double part[kSlices][kFoldCols];
+  const int c = threadIdx.x % kFoldCols, slice = threadIdx.x / kFoldCols;
+  const int64_t col = int64_t(blockIdx.x) * kFoldCols + c;
+  double t = 0.0;
+  if (col < cols) {
+#pragma unroll 8
+    for (int64_t i = slice; i < count; i += kSlices) t += static_cast<double>(partials[i * pitch + col]);
+  }
+  part[slice][c] = t;
+  __syncthreads();
+  if (slice == 0 && col < cols) {
+#pragma unroll
+    for (int i = 1; i < kSlices; ++i) t += part[i][c];
+    if (base != nullptr) t += static_cast<double>(load_any(base, dt, col));
+    store_any(dweight, dt, col, static_cast<float>(t));
+  }
+}
+
+// ------------------------------------------------------------------ launch choices
+
+template <int DT>
+hipError_t pack_code(const void* src, int64_t stride, int64_t cols, uint32_t cpr, int64_t n, const Act& act,
+                     hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((n + kChunksPerBlock - 1) / kChunksPerBlock));
+  if (act.code == ZS_E4M3)
+    hipLaunchKernelGGL((k_act_pack<DT, ZS_E4M3>), grid, dim3(kThreads), 0, s, src, stride, cols, cpr, n, act.codes,
+                       act.scales);
+  else
+    hipLaunchKernelGGL((k_act_pack<DT, ZS_INT8>), grid, dim3(kThreads), 0, s, src, stride, cols, cpr, n, act.codes,
+                       act.scales);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t unpack_code(const Act& act, int64_t cols, uint32_t cpr, int64_t n, void* dst, int64_t stride, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((n + kChunksPerBlock - 1) / kChunksPerBlock));
+  if (act.code == ZS_E4M3)
+    hipLaunchKernelGGL((k_act_unpack<DT, ZS_E4M3>), grid, dim3(kThreads), 0, s, act.codes, act.scales, cols, cpr, n,
+                       dst, stride);
+  else
+    hipLaunchKernelGGL((k_act_unpack<DT, ZS_INT8>), grid, dim3(kThreads), 0, s, act.codes, act.scales, cols, cpr, n,
+                       dst, stride);
+  return hipGetLastError();
+}
+
+template <int DT, int LPR, int V>
+hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
+  constexpr int kBlock = norm_block<LPR>();
+  constexpr int kRows = kBlock / LPR;
+  hipLaunchKernelGGL((k_rmsnorm<DT, LPR, V>), dim3(static_cast<unsigned>((a.rows + kRows - 1) / kRows)), dim3(kBlock), 0,
+                     s, a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t norm_cols(const NormArgs& a, hipStream_t s) {
+  if (a.cols <= 128) return norm_launch<DT, 16, 1>(a, s);
+  if (a.cols <= 512) return norm_launch<DT, 64, 1>(a, s);
+  if (a.cols <= 2048) return norm_launch<DT, 256, 1>(a, s);
+  if (a.cols <= 4096) return norm_launch<DT, 256, 2>(a, s);
+  if (a.cols <= 8192) return norm_launch<DT, 256, 4>(a, s);
+  return norm_launch<DT, 1024, 2>(a, s);
+}
+
+int norm_rows_per_block(int64_t cols) { return cols <= 128 ? 16 : cols <= 512 ? 4 : 1; }
+
+template <int DT, int SAVED, int LPR, int V>
+hipError_t backward_launch(const NormBackwardArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_rmsnorm_backward<DT, SAVED, LPR, V>), dim3(static_cast<unsigned>(rmsnorm_partials(a.rows, a.cols))),
+                     dim3(norm_block<LPR>()), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT, int SAVED>
+hipError_t backward_cols(const NormBackwardArgs& a, hipStream_t s) {
+  if (a.cols <= 128) return backward_launch<DT, SAVED, 16, 1>(a, s);
+  if (a.cols <= 512) return backward_launch<DT, SAVED, 64, 1>(a, s);
+  if (a.cols <= 2048) return backward_launch<DT, SAVED, 256, 1>(a, s);
+  if (a.cols <= 4096) return backward_launch<DT, SAVED, 256, 2>(a, s);
+  if (a.cols <= 8192) return backward_launch<DT, SAVED, 256, 4>(a, s);
+  return backward_launch<DT, SAVED, 1024, 2>(a, s);
+}
+
+template <int DT>
+hipError_t backward_saved(const NormBackwardArgs& a, hipStream_t s) {
+  if (a.h != nullptr) return backward_cols<DT, kSaved16>(a, s);
+  if (a.h8.code == ZS_E4M3) return backward_cols<DT, kSavedE4m3>(a, s);
+  return backward_cols<DT, kSavedInt8>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_act_pack(const void* src, int dt, int64_t stride, int64_t rows, int64_t cols, const Act& act,
+                           hipStream_t s) {
+  const uint32_t cpr = static_cast<uint32_t>(act_padded(cols) / 8);
+  const int64_t n = rows * cpr;
+  if (n == 0) return hipSuccess;
+  if (dt == ZS_BF16) return pack_code<ZS_BF16>(src, stride, cols, cpr, n, act, s);
+  if (dt == ZS_FP16) return pack_code<ZS_FP16>(src, stride, cols, cpr, n, act, s);
+  return pack_code<ZS_FP32>(src, stride, cols, cpr, n, act, s);
+}
+
+hipError_t launch_act_unpack(const Act& act, int64_t rows, int64_t cols, void* dst, int dt, int64_t stride,
+                             hipStream_t s) {
+  const uint32_t cpr = static_cast<uint32_t>(act_padded(cols) / 8);
+  const int64_t n = rows * cpr;
+  if (n == 0) return hipSuccess;
+  if (dt == ZS_BF16) return unpack_code<ZS_BF16>(act, cols, cpr, n, dst, stride, s);
+  if (dt == ZS_FP16) return unpack_code<ZS_FP16>(act, cols, cpr, n, dst, stride, s);
+  return unpack_code<ZS_FP32>(act, cols, cpr, n, dst, stride, s);
+}
+
+hipError_t launch_rmsnorm(const NormArgs& a, int dt, hipStream_t s) {
+  if (a.rows == 0) return hipSuccess;
+  return dt == ZS_BF16 ? norm_cols<ZS_BF16>(a, s) : norm_cols<ZS_FP16>(a, s);
+}
+
+int64_t rmsnorm_max_rows(int64_t cols) {
+  return ((int64_t(1) << (cols <= 8192 ? 24 : 22)) - 1) * norm_rows_per_block(cols);
+}
+
+int64_t rmsnorm_partials(int64_t rows, int64_t cols) {
+  const int per = norm_rows_per_block(cols);
+  const int64_t steps = (rows + per - 1) / per;
+  if (steps <= 8) return 1;
+  return steps < 512 ? steps : 512;
+}
+
+hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, int dt, hipStream_t s) {
+  hipError_t e = dt == ZS_BF16 ? backward_saved<ZS_BF16>(a, s) : backward_saved<ZS_FP16>(a, s);
+  const int64_t parts = rmsnorm_partials(a.rows, a.cols);
+  if (e != hipSuccess || a.dweight == nullptr || parts == 1) return e;
+  const int64_t pitch = (int64_t(a.cols) + 7) / 8 * 8;
+  hipLaunchKernelGGL(k_dweight, dim3(static_cast<unsigned>((a.cols + kFoldCols - 1) / kFoldCols)), dim3(kThreads), 0, s,
+                     a.partials, parts, pitch, a.cols, a.dweight, a.dweight_dt, a.base);
+  return hipGetLastError();
+}
+
+}  // namespace zs

@@ -123,4 +123,72 @@ hipError_t launch_probe_copy(const void* src, void* dst, int64_t bytes, hipStrea
 hipError_t launch_probe_read(const void* src, int64_t bytes, uint32_t* sink, hipStream_t s);
 hipError_t launch_probe_write(void* dst, int64_t bytes, hipStream_t s);
 
+// Activation operators (zs_act.hip, zs_wgrad.hip); every argument already checked.  A matrix
+// is a base pointer and a row stride in elements.
+struct Act {  // checkpoint arrays; code is a zs_code
+  uint8_t* codes;
+  uint8_t* scales;
+  int code;
+};
+constexpr int64_t kActPad = 32;           // codes per row are a multiple of this
+constexpr int64_t kNormMaxCols = 16384;   // 1024 threads with two chunks of eight columns each
+__host__ __device__ inline int64_t act_padded(int64_t cols) { return (cols + kActPad - 1) / kActPad * kActPad; }
+// Rows of one launch of the norm (its workgroups hold fewer than 2^32 threads).
+int64_t rmsnorm_max_rows(int64_t cols);
+// Eight-element chunks of one pack or unpack launch (four per thread, < 2^32 threads).
+constexpr int64_t kActMaxChunks = ((int64_t(1) << 32) - 256) * 4;
+
+hipError_t launch_act_pack(const void* src, int dt, int64_t stride, int64_t rows, int64_t cols, const Act& act,
+                           hipStream_t s);
+hipError_t launch_act_unpack(const Act& act, int64_t rows, int64_t cols, void* dst, int dt, int64_t stride,
+                             hipStream_t s);
+
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* residual;  // or null
+  const uint16_t* weight;
+  uint16_t* h;  // or null
+  uint16_t* y;  // or null
+  float* rstd;  // or null
+  int64_t x_stride, residual_stride, h_stride, y_stride;
+  Act y8, h8;  // codes null: none
+  int64_t rows;
+  int32_t cols;
+  double eps;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, int dt, hipStream_t s);
+
+struct NormBackwardArgs {
+  const uint16_t* dy;
+  const uint16_t* dh;  // or null
+  const uint16_t* h;   // or null: h8
+  Act h8;
+  const uint16_t* weight;
+  const float* rstd;
+  uint16_t* dx;
+  int64_t dy_stride, dh_stride, h_stride, dx_stride;
+  int64_t rows;
+  int32_t cols;
+  void* dweight;  // or null
+  const void* base;  // or null
+  int dweight_dt;
+  float* partials;  // rmsnorm_partials(rows, cols) rows of round_up(cols, 8) sums
+};
+// Workgroups of the backward pass, each leaving one row of partial weight-gradient sums.
+int64_t rmsnorm_partials(int64_t rows, int64_t cols);
+hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, int dt, hipStream_t s);
+
+struct WgradArgs {
+  Act x8;
+  const uint16_t* dy;
+  void* dw;
+  const void* base;  // or null
+  float* partials;
+  int64_t rows, cols, outs, dy_stride, dw_stride;
+  int dy_dt, dw_dt;
+  bool in_major;
+};
+int64_t wgrad_workspace(int64_t rows, int64_t cols, int64_t outs);  // bytes; < 0: past one launch
+hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s);
+
 }  // namespace zs
