@@ -36,17 +36,51 @@ __device__ __forceinline__ v16f mfma(const v8s& a, const v8s& b, const v16f& c) 
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8hf, a), __builtin_bit_cast(v8hf, b), c, 0, 0, 0);
 }
 
-// Sixteen codes under scale byte b as 2-byte values in memory order.
+// An infinity in either half of a pair of fp16 values becomes the largest number: code * s may lie
+// up to one code step past it although the source did not.  NaN stays.
+__device__ __forceinline__ uint32_t fp16_range(uint32_t x) {
+  typedef unsigned short v2h __attribute__((ext_vector_type(2)));
+  const v2h one = {1, 1};
+  const v2h away = __builtin_bit_cast(v2h, (x & 0x7FFF7FFFu) ^ 0x7C007C00u);  // zero where infinite
+  const v2h keep = __builtin_elementwise_min(away, one);
+  return __builtin_bit_cast(uint32_t, static_cast<v2h>(__builtin_bit_cast(v2h, x) - one + keep));
+}
+
+// Sixteen codes under scale byte b as 2-byte values in memory order.  gfx950 converts a pair of
+// e4m3 codes with a power-of-two scale in one instruction, which takes the scale from the exponent
+// field alone: exact for every code and scale byte, 0 (2^-127) and 255 (NaN) included.
 template <int DT, int CODE>
 __device__ __forceinline__ void values16(const v4u& c, int b, v4u& lo, v4u& hi) {
-  float f[8];
-  const float s = scale_value(b);
-  decode8<CODE>(v2u{c[0], c[1]}, s, f);
-  clamp8<DT>(f);
-  lo = narrow8<DT>(f);
-  decode8<CODE>(v2u{c[2], c[3]}, s, f);
-  clamp8<DT>(f);
-  hi = narrow8<DT>(f);
+  if constexpr (CODE == ZS_E4M3) {
+    const float s = bits_f(static_cast<uint32_t>(b) << 23);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t x, y;
+      if constexpr (DT == ZS_BF16) {
+        x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[j], s, false));
+        y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[j], s, true));
+      } else {
+        x = fp16_range(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[j], s, false)));
+        y = fp16_range(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[j], s, true)));
+      }
+      (j < 2 ? lo : hi)[2 * (j & 1)] = x;
+      (j < 2 ? lo : hi)[2 * (j & 1) + 1] = y;
+    }
+  } else {
+    float f[8];
+    const float s = scale_value(b);
+    decode8<CODE>(v2u{c[0], c[1]}, s, f);
+    lo = narrow8<DT>(f);
+    decode8<CODE>(v2u{c[2], c[3]}, s, f);
+    hi = narrow8<DT>(f);
+    if constexpr (DT == ZS_FP16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        lo[j] = fp16_range(lo[j]);
+        hi[j] = fp16_range(hi[j]);
+      }
+    }
+  }
 }
 
 // A workgroup's tile: WN x WK waves, each FN x FK matrix instructions of 32 x 32; a stage holds
@@ -83,40 +117,74 @@ struct Stage {
   int scale[TL::kLoadsK];
 };
 
-// Tokens t .. t + T - 1 of the two operands into registers; what lies past the tokens or columns
-// of the task reads as zero, and its memory is not touched.
+// Tokens t .. t + T - 1 of the two operands into registers; tokens past the task's read as zero.
+// Whole stages take plain loads: a uniform base per load and a lane offset that never changes.
+// Loads that begin past the last column are left out; one that begins before and ends behind it
+// takes the elements behind a row of dy along (padding, or the next row: a stage with the last row
+// does not come here), which reach columns of the tile that are never stored.
 template <class TL>
-__device__ __forceinline__ void fetch(const WgradArgs& g, const WgradTask& w, int64_t t, Stage<TL>& st) {
-  const int64_t padded = act_padded(g.cols);
-  constexpr int kPerRowN = TL::kN / 8, kPerRowK = TL::kK / 16;
-  const bool inside = t + TL::T <= w.t1 && w.n0 + TL::kN <= g.outs && w.k0 + TL::kK <= padded;
-#pragma unroll
-  for (int u = 0; u < TL::kLoadsN; ++u) {
-    const int i = u * TL::kThreads + threadIdx.x;
-    const int64_t row = t + i / kPerRowN, col = w.n0 + (i % kPerRowN) * 8;
-    const uint16_t* p = g.dy + row * g.dy_stride + col;
-    if (inside) {
-      st.a[u] = *reinterpret_cast<const v4u_a2*>(p);
-    } else {
-      const int64_t left = g.outs - col;
-      st.a[u] = load8h(p, row < w.t1 ? (left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0) : 0);
-    }
+struct Fetcher {
+  static constexpr int kPerRowN = TL::kN / 8, kPerRowK = TL::kK / 16;         // loads of a row
+  static constexpr int kRowsN = TL::kThreads / kPerRowN, kRowsK = TL::kThreads / kPerRowK;  // rows of a load
+  const WgradArgs& g;
+  const WgradTask& w;
+  int64_t padded;
+  uint32_t off_n, off_k, off_s;
+  bool whole, any_n, any_k;  // the tile lies inside; this lane's loads begin inside
+  int64_t last;              // the first token that no plain stage may hold
+
+  __device__ __forceinline__ Fetcher(const WgradArgs& g_, const WgradTask& w_) : g(g_), w(w_) {
+    const int rn = threadIdx.x / kPerRowN, rk = threadIdx.x / kPerRowK;
+    padded = act_padded(g.cols);
+    off_n = static_cast<uint32_t>(rn * g.dy_stride + (threadIdx.x % kPerRowN) * 8) * 2;
+    off_k = static_cast<uint32_t>(rk * padded + (threadIdx.x % kPerRowK) * 16);
+    off_s = static_cast<uint32_t>(rk * (padded / kActGroup) + (threadIdx.x % kPerRowK) / 2);
+    whole = w.n0 + TL::kN <= g.outs && w.k0 + TL::kK <= padded;
+    any_n = w.n0 + static_cast<int64_t>(threadIdx.x % kPerRowN) * 8 < g.outs;
+    any_k = w.k0 + static_cast<int64_t>(threadIdx.x % kPerRowK) * 16 < padded;
+    last = whole || w.t1 < g.rows ? w.t1 : g.rows - 1;
+    if (g.dy_stride >= (1 << 24) || padded >= (1 << 24) || g.dy_stride < 8) last = 0;  // offsets of 32 bits
   }
+
+  __device__ __forceinline__ void operator()(int64_t t, Stage<TL>& st) const {
+    if (t + TL::T <= last) {
+      const char* pn = reinterpret_cast<const char*>(g.dy + t * g.dy_stride + w.n0);
+      const uint8_t* pk = g.x8.codes + t * padded + w.k0;
+      const uint8_t* ps = g.x8.scales + (t * padded + w.k0) / kActGroup;
+      if (whole || any_n) {
 #pragma unroll
-  for (int u = 0; u < TL::kLoadsK; ++u) {
-    const int i = u * TL::kThreads + threadIdx.x;
-    const int64_t row = t + i / kPerRowK, col = w.k0 + (i % kPerRowK) * 16;
-    const int64_t at = row * padded + col;
-    if (inside || (row < w.t1 && col < padded)) {
-      st.b[u] = *reinterpret_cast<const v4u*>(g.x8.codes + at);
-      st.scale[u] = g.x8.scales[at / kActGroup];
-    } else {
+        for (int u = 0; u < TL::kLoadsN; ++u)
+          st.a[u] = *reinterpret_cast<const v4u_a2*>(pn + u * kRowsN * g.dy_stride * 2 + off_n);
+      }
+      if (whole || any_k) {
+#pragma unroll
+        for (int u = 0; u < TL::kLoadsK; ++u) {
+          st.b[u] = *reinterpret_cast<const v4u*>(pk + u * kRowsK * padded + off_k);
+          st.scale[u] = ps[u * kRowsK * (padded / kActGroup) + off_s];
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int u = 0; u < TL::kLoadsN; ++u) {
+      const int64_t row = t + u * kRowsN + threadIdx.x / kPerRowN, col = w.n0 + (threadIdx.x % kPerRowN) * 8;
+      const int64_t left = row < w.t1 ? g.outs - col : 0;
+      st.a[u] = load8h(g.dy + row * g.dy_stride + col, left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < TL::kLoadsK; ++u) {
+      const int64_t row = t + u * kRowsK + threadIdx.x / kPerRowK, col = w.k0 + (threadIdx.x % kPerRowK) * 16;
       st.b[u] = v4u{0u, 0u, 0u, 0u};
       st.scale[u] = 0;
+      if (row < w.t1 && col < padded) {
+        st.b[u] = *reinterpret_cast<const v4u*>(g.x8.codes + row * padded + col);
+        st.scale[u] = g.x8.scales[(row * padded + col) / kActGroup];
+      }
     }
   }
-}
+};
 
+// A stage into LDS.
 template <int DT, int CODE, class TL>
 __device__ __forceinline__ void stage_to_lds(const Stage<TL>& st, char* buf) {
   constexpr int kPerRowN = TL::kN / 8, kPerRowK = TL::kK / 16;
@@ -147,33 +215,21 @@ __device__ __forceinline__ v8s read_operand(const char* p) {
   return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-__device__ __forceinline__ float load_dw(const void* p, int dt, int64_t i) {
-  if (dt == ZS_FP32) return static_cast<const float*>(p)[i];
-  const uint32_t b = static_cast<const uint16_t*>(p)[i];
-  return dt == ZS_BF16 ? lo_f<ZS_BF16>(b) : lo_f<ZS_FP16>(b);
-}
-__device__ __forceinline__ void store_dw(void* p, int dt, int64_t i, float x) {
-  if (dt == ZS_FP32)
-    static_cast<float*>(p)[i] = x;
-  else
-    static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(dt == ZS_BF16 ? half_bits<ZS_BF16>(x) : half_bits<ZS_FP16>(x));
-}
-
+// Work units of a launch: the first `direct` tiles each as one workgroup over all tokens, the
+// others in `splits` workgroups each, over `per` tokens.
 struct WgradGrid {
-  int32_t tiles_n, tiles_k, splits;
-  int64_t per;     // tokens per split
-  int64_t pitch;   // row pitch of the partial sums, in elements
+  int32_t tiles_n, tiles_k, direct, splits;
+  int64_t per;
 };
 
 // Eight sums of one row of the output, from column col on, cnt of them inside: added to the base
-// and rounded once, or left in fp32 among the partial sums.
+// and rounded once.
 template <int DT>
-__device__ __forceinline__ void write8(const WgradArgs& g, float* part, int64_t stride, int64_t row, int64_t col, int cnt,
-                                       float (&f)[8]) {
-  const int64_t at = row * stride + col;
-  if (part != nullptr || g.dw_dt == ZS_FP32) {
-    float* p = (part != nullptr ? part : static_cast<float*>(g.dw)) + at;
-    const float* base = part != nullptr ? nullptr : static_cast<const float*>(g.base);
+__device__ __forceinline__ void write8(const WgradArgs& g, int64_t row, int64_t col, int cnt, float (&f)[8]) {
+  const int64_t at = row * g.dw_stride + col;
+  if (g.dw_dt == ZS_FP32) {
+    float* p = static_cast<float*>(g.dw) + at;
+    const float* base = static_cast<const float*>(g.base);
     if (cnt == 8) {
       v4u lo, hi;
       if (base != nullptr) {
@@ -210,18 +266,25 @@ __device__ __forceinline__ void write8(const WgradArgs& g, float* part, int64_t 
 template <int DT, int CODE, class TL>
 __global__ __launch_bounds__(TL::kThreads, TL::FN* TL::FK >= 16 ? 1 : 2) void k_wgrad(WgradArgs g, WgradGrid gr) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  // one contiguous run of tiles per XCD, so that neighbouring tiles share their operands in its L2
-  const int64_t units = int64_t(gr.tiles_n) * gr.tiles_k * gr.splits;
-  const int64_t per_xcd = (units + kXcds - 1) / kXcds;
-  const int64_t unit = (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
-  if (unit >= units) return;
-  const int64_t tiles = int64_t(gr.tiles_n) * gr.tiles_k;
-  const int64_t split = unit / tiles, tile = unit % tiles;
+  // one contiguous run of units per XCD, of the direct tiles and of the split ones, so that
+  // neighbouring tiles share their operands in its L2
+  const int tiles = gr.tiles_n * gr.tiles_k;
+  int tile, split = -1;
+  if (blockIdx.x < static_cast<unsigned>(gr.direct)) {  // a multiple of the XCDs
+    tile = blockIdx.x % kXcds * (gr.direct / kXcds) + blockIdx.x / kXcds;
+  } else {
+    const int units = (tiles - gr.direct) * gr.splits;
+    const int b = blockIdx.x - gr.direct;
+    const int unit = b % kXcds * ((units + kXcds - 1) / kXcds) + b / kXcds;
+    if (unit >= units) return;
+    tile = gr.direct + unit / gr.splits;
+    split = unit % gr.splits;
+  }
   WgradTask w;
-  w.t0 = split * gr.per;
-  w.t1 = w.t0 + gr.per < g.rows ? w.t0 + gr.per : g.rows;
-  w.n0 = tile / gr.tiles_k * TL::kN;
-  w.k0 = tile % gr.tiles_k * TL::kK;
+  w.t0 = split < 0 ? 0 : split * gr.per;
+  w.t1 = split < 0 || w.t0 + gr.per > g.rows ? g.rows : w.t0 + gr.per;
+  w.n0 = int64_t(tile / gr.tiles_k) * TL::kN;
+  w.k0 = int64_t(tile % gr.tiles_k) * TL::kK;
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wn = wave / TL::WK * TL::FN * 32, wk = wave % TL::WK * TL::FK * 32;  // the wave's part of the tile
@@ -236,31 +299,79 @@ __global__ __launch_bounds__(TL::kThreads, TL::FN* TL::FK >= 16 ? 1 : 2) void k_
 #pragma unroll
     for (int j = 0; j < TL::FK; ++j) acc[i][j] = v16f(0.0f);
 
-  Stage<TL> st;
-  int turn = 0;
-  if (w.t0 < w.t1) {
-    fetch<TL>(g, w, w.t0, st);
-    stage_to_lds<DT, CODE, TL>(st, lds);
-  }
-  __syncthreads();
-  for (int64_t t = w.t0; t < w.t1; t += TL::T, turn ^= 1) {
-    const bool more = t + TL::T < w.t1;
-    if (more) fetch<TL>(g, w, t + TL::T, st);
-    const char* buf = lds + turn * TL::kBuffer;
+  struct Operands {
+    v8s a[TL::FN], b[TL::FK];
+  };
+  auto read = [&](Operands& f, const char* buf, int step) {
 #pragma unroll
-    for (int s = 0; s < TL::T / 16; ++s) {
-      v8s a[TL::FN], b[TL::FK];
+    for (int i = 0; i < TL::FN; ++i) f.a[i] = read_operand<TL::kPitchN>(buf + at_n + step * 16 * TL::kPitchN + i * 64);
 #pragma unroll
-      for (int i = 0; i < TL::FN; ++i) a[i] = read_operand<TL::kPitchN>(buf + at_n + s * 16 * TL::kPitchN + i * 64);
+    for (int j = 0; j < TL::FK; ++j) f.b[j] = read_operand<TL::kPitchK>(buf + at_k + step * 16 * TL::kPitchK + j * 64);
+  };
+  auto multiply = [&](const Operands& f) {
 #pragma unroll
-      for (int j = 0; j < TL::FK; ++j) b[j] = read_operand<TL::kPitchK>(buf + at_k + s * 16 * TL::kPitchK + j * 64);
+    for (int i = 0; i < TL::FN; ++i)
 #pragma unroll
-      for (int i = 0; i < TL::FN; ++i)
+      for (int j = 0; j < TL::FK; ++j) acc[i][j] = mfma<DT>(f.a[i], f.b[j], acc[i][j]);
+  };
+  // Between two matrix instructions: a share of the next step's LDS reads, of the conversions and
+  // of the LDS writes, so that the matrix cores do not wait for any of them.
+  auto interleave = [&]() {
+    constexpr int kM = TL::FN * TL::FK, kReads = 2 * (TL::FN + TL::FK);
+    constexpr int kEach = (kReads + kM - 1) / kM;
 #pragma unroll
-        for (int j = 0; j < TL::FK; ++j) acc[i][j] = mfma<DT>(a[i], b[j], acc[i][j]);
+    for (int m = 0; m < kM; ++m) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // matrix
+      __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);  // LDS reads
+      __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);      // vector
+      __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);      // LDS writes
     }
-    if (more) stage_to_lds<DT, CODE, TL>(st, lds + (turn ^ 1) * TL::kBuffer);
+  };
+  // One barrier per stage.  While stage i is multiplied from one LDS buffer, stage i + 1 goes from
+  // registers into the other, whose readers passed the barrier of stage i - 1, during the first
+  // step; then stage i + 2 sets out from memory.  The operands of a step are read during the step
+  // before, the first ones of the next stage after the barrier, during the last step.
+  constexpr int kSteps = TL::T / 16;
+  static_assert(kSteps % 2 == 0, "the operand sets alternate");
+  const Fetcher<TL> fetch(g, w);
+  const int64_t stages = (w.t1 - w.t0 + TL::T - 1) / TL::T;
+  if (stages > 0) {
+    Stage<TL> st{};
+    Operands f[2];
+    fetch(w.t0, st);
+    stage_to_lds<DT, CODE, TL>(st, lds);
+    if (stages > 1) fetch(w.t0 + TL::T, st);
     __syncthreads();
+    read(f[0], lds, 0);
+    char* cur = lds;
+    char* other = lds + TL::kBuffer;
+    for (int64_t i = 0; i + 1 < stages; ++i) {
+#pragma unroll
+      for (int step = 0; step + 1 < kSteps; ++step) {
+        read(f[(step + 1) & 1], cur, step + 1);
+        multiply(f[step & 1]);
+        if (step == 0) stage_to_lds<DT, CODE, TL>(st, other);
+        interleave();
+        __builtin_amdgcn_sched_barrier(0);
+        if (step == 0 && i + 2 < stages) fetch(w.t0 + (i + 2) * TL::T, st);
+      }
+      __syncthreads();
+      read(f[0], other, 0);
+      multiply(f[(kSteps - 1) & 1]);
+      interleave();
+      __builtin_amdgcn_sched_barrier(0);
+      char* x = cur;
+      cur = other;
+      other = x;
+    }
+#pragma unroll
+    for (int step = 0; step < kSteps; ++step) {
+      if (step + 1 < kSteps) read(f[(step + 1) & 1], cur, step + 1);
+      multiply(f[step & 1]);
+      interleave();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();  // the strips below reuse the buffers
   }
 
   // The sums leave through LDS, a strip of 32 output rows of the wave at a time, so that a lane
@@ -268,26 +379,35 @@ __global__ __launch_bounds__(TL::kThreads, TL::FN* TL::FK >= 16 ? 1 : 2) void k_
   // 8 * (r / 4) + 4 * (lane / 32) + r % 4 (dy's column), column lane % 32 (x8's column).
   float* strip = reinterpret_cast<float*>(lds) + wave * 32 * TL::kStripPitch;
   const int64_t out_rows = g.in_major ? g.cols : g.outs, out_cols = g.in_major ? g.outs : g.cols;
-  float* part = gr.splits > 1 ? g.partials + split * out_rows * gr.pitch : nullptr;
-  const int64_t stride = part != nullptr ? gr.pitch : g.dw_stride;
-  const int64_t row0 = g.in_major ? w.k0 + wk : w.n0 + wn, col0 = g.in_major ? w.n0 + wn : w.k0 + wk;
+  const int64_t row0 = g.in_major ? w.k0 : w.n0, col0 = g.in_major ? w.n0 : w.k0;
+  const int wave_row = g.in_major ? wk : wn, wave_col = g.in_major ? wn : wk;
+  const int tile_cols = g.in_major ? TL::kN : TL::kK;
+  // a split leaves its whole tile, row by row, in the workspace
+  float* part = nullptr;
+  if (split >= 0 && gr.splits > 1) part = g.partials + (int64_t(tile - gr.direct) * gr.splits + split) * (TL::kN * TL::kK);
   auto leave = [&](int index, int groups) {  // rows of the strip, `groups` eights of columns to a row
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     for (int q = lane; q < 32 * groups; q += 64) {
       const int r = q / groups, c = q % groups * 8;
-      const int64_t row = row0 + index * 32 + r, col = col0 + c;
-      const int64_t left = out_cols - col;
-      if (row >= out_rows || left <= 0) continue;
-      float f[8];
       const v4u x = *reinterpret_cast<const v4u*>(strip + r * TL::kStripPitch + c);
       const v4u y = *reinterpret_cast<const v4u*>(strip + r * TL::kStripPitch + c + 4);
+      const int tr = wave_row + index * 32 + r, tc = wave_col + c;
+      if (part != nullptr) {
+        v4u* p = reinterpret_cast<v4u*>(part + tr * tile_cols + tc);
+        p[0] = x;
+        p[1] = y;
+        continue;
+      }
+      const int64_t row = row0 + tr, col = col0 + tc, left = out_cols - col;
+      if (row >= out_rows || left <= 0) continue;
+      float f[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         f[j] = bits_f(x[j]);
         f[4 + j] = bits_f(y[j]);
       }
-      write8<DT>(g, part, stride, row, col, left >= 8 ? 8 : static_cast<int>(left), f);
+      write8<DT>(g, row, col, left >= 8 ? 8 : static_cast<int>(left), f);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -319,73 +439,110 @@ __global__ __launch_bounds__(TL::kThreads, TL::FN* TL::FK >= 16 ? 1 : 2) void k_
   }
 }
 
-// dw = base + the splits' sums in token order, added in fp32 as one long sum would be.
-__global__ __launch_bounds__(kThreads) void k_wgrad_fold(const float* __restrict__ partials, int32_t splits, int64_t rows,
-                                                         int64_t cols, int64_t pitch, void* dw, const void* base, int dt,
-                                                         int64_t dw_stride) {
-  const int64_t quads = pitch / 4;
-  const int64_t q = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  if (q >= rows * quads) return;
-  const int64_t row = q / quads, col = q % quads * 4;
-  float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < splits; ++s) {
-    const v4u x = *reinterpret_cast<const v4u*>(partials + (s * rows + row) * pitch + col);
+// The split tiles of dw: base + the splits' sums in token order, added in fp32 as one long sum
+// would be, rounded once.  A thread takes eight consecutive elements.
+template <int DT, class TL>
+__global__ __launch_bounds__(kThreads) void k_wgrad_fold(WgradArgs g, WgradGrid gr) {
+  constexpr int kArea = TL::kN * TL::kK, kBlocks = kArea / 8 / kThreads;
+  const int tile = blockIdx.x / kBlocks, e = (blockIdx.x % kBlocks * kThreads + threadIdx.x) * 8;
+  const int tile_cols = g.in_major ? TL::kN : TL::kK;
+  const int64_t n0 = int64_t((gr.direct + tile) / gr.tiles_k) * TL::kN, k0 = int64_t((gr.direct + tile) % gr.tiles_k) * TL::kK;
+  const int64_t row = (g.in_major ? k0 : n0) + e / tile_cols, col = (g.in_major ? n0 : k0) + e % tile_cols;
+  const int64_t left = (g.in_major ? g.outs : g.cols) - col;
+  if (row >= (g.in_major ? g.cols : g.outs) || left <= 0) return;
+  const float* p = g.partials + int64_t(tile) * gr.splits * kArea + e;
+  float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int s = 0; s < gr.splits; ++s) {
+    const v4u x = *reinterpret_cast<const v4u*>(p + int64_t(s) * kArea), y = *reinterpret_cast<const v4u*>(p + int64_t(s) * kArea + 4);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) t[j] += bits_f(x[j]);
+    for (int j = 0; j < 4; ++j) {
+      f[j] += bits_f(x[j]);
+      f[4 + j] += bits_f(y[j]);
+    }
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (col + j >= cols) break;
-    const int64_t at = row * dw_stride + col + j;
-    store_dw(dw, dt, at, t[j] + (base != nullptr ? load_dw(base, dt, at) : 0.0f));
-  }
+  write8<DT>(g, row, col, left >= 8 ? 8 : static_cast<int>(left), f);
 }
 
 // ------------------------------------------------------------------ launch choices
 
 using SmallTile = Tile<2, 2, 2, 2, 32>;  // 128 x 128
 #ifndef ZS_LARGE
-#define ZS_LARGE 2, 2, 4, 4, 64
+#define ZS_LARGE 2, 4, 4, 2, 64
 #endif
 using LargeTile = Tile<ZS_LARGE>;  // 256 x 256
-constexpr int64_t kMaxUnits = (int64_t(1) << 23) - 64;  // workgroups of 512 threads in one launch
-
 struct WgradChoice {
   bool large;
   WgradGrid grid;
+  int64_t workspace;
 };
+
+// Time of a launch in microseconds as a function of the tile, the tiles done directly and the
+// splits of the others, from what the kernels measure on MI355X (256 CUs): a stage of the large
+// tile, one workgroup to a CU, and of the small one, up to three to a CU; the start and end of
+// a workgroup; the partial sums on their way to memory and back, and the launch that folds them.
+template <class TL>
+double launch_cost(int64_t tiles, int64_t direct, int64_t splits, int64_t stages) {
+  constexpr bool kBig = TL::kN == 256;
+  auto rounds = [&](int64_t units, int64_t n) {
+    if (kBig) return double((units + 255) / 256) * (n * 1.75 + 6.0);
+    const int64_t full = units / 768, rest = units % 768;
+    const double q = rest == 0 ? 0.0 : rest <= 256 ? 0.5 : rest <= 512 ? 0.7 : 1.0;
+    return (full + q) * (n * 0.85 + 4.0);
+  };
+  double t = direct > 0 ? rounds(direct, stages) : 0.0;
+  if (tiles > direct) t += rounds((tiles - direct) * splits, (stages + splits - 1) / splits);
+  if (splits > 1) t += 5.0 + double(tiles - direct) * splits * (TL::kN * TL::kK) * 8 / 5.0e6;
+  return t;
+}
+
+template <class TL>
+void consider(int64_t rows, int64_t cols, int64_t outs, WgradChoice* best, double* cost) {
+  constexpr int64_t kSlots = TL::kN == 256 ? 256 : 768;
+  const int64_t tn = (outs + TL::kN - 1) / TL::kN, tk = (cols + TL::kK - 1) / TL::kK, tiles = tn * tk;
+  const int64_t stages = std::max<int64_t>(1, (rows + TL::T - 1) / TL::T);
+  const int64_t whole = tiles / kSlots * kSlots;
+  for (int64_t s = 1; s <= 64; ++s) {
+    const int64_t per = (stages + s - 1) / s;
+    if (s > 1 && per < 4) break;
+    if ((stages + per - 1) / per != s) continue;
+    for (const int64_t direct : {int64_t(0), whole}) {
+      if (s == 1 && direct != 0) continue;
+      if (s > 1 && (tiles - direct) * s > 4 * kSlots) continue;  // splitting more than that only adds sums
+      const double t = launch_cost<TL>(tiles, direct, s, stages);
+      if (t >= *cost) continue;
+      *cost = t;
+      best->large = TL::kN == 256;
+      best->grid = {static_cast<int32_t>(tn), static_cast<int32_t>(tk), static_cast<int32_t>(direct), static_cast<int32_t>(s),
+                    per * TL::T};
+      best->workspace = s == 1 ? 16 : (tiles - direct) * s * (TL::kN * TL::kK) * int64_t(sizeof(float));
+    }
+  }
+}
 
 WgradChoice choose(int64_t rows, int64_t cols, int64_t outs) {
   WgradChoice c{};
-  auto count = [&](int64_t sn, int64_t sk) { return ((outs + sn - 1) / sn) * ((cols + sk - 1) / sk); };
-  c.large = count(LargeTile::kN, LargeTile::kK) >= 192 && rows >= 512;
-  const int64_t sn = c.large ? LargeTile::kN : SmallTile::kN, sk = c.large ? LargeTile::kK : SmallTile::kK;
-  const int64_t step = c.large ? LargeTile::T : SmallTile::T;
-  const int64_t n = count(sn, sk);
-  int64_t splits = 1;
-  if (!c.large && n < 512) {
-    splits = std::min<int64_t>(768 / n, rows / (8 * step));  // three workgroups per CU, at least eight stages each
-    splits = std::max<int64_t>(splits, 1);
-  }
-  const int64_t steps = std::max<int64_t>(1, (rows + step - 1) / step);
-  const int64_t per = (steps + splits - 1) / splits;
-  c.grid.tiles_n = static_cast<int32_t>((outs + sn - 1) / sn);
-  c.grid.tiles_k = static_cast<int32_t>((cols + sk - 1) / sk);
-  c.grid.splits = static_cast<int32_t>((steps + per - 1) / per);
-  c.grid.per = per * step;
+  double cost = 1e30;
+  consider<LargeTile>(rows, cols, outs, &c, &cost);
+  consider<SmallTile>(rows, cols, outs, &c, &cost);
   return c;
 }
 
 template <int DT, int CODE, class TL>
 hipError_t wgrad_launch(const WgradArgs& a, const WgradGrid& gr, hipStream_t s) {
-  const int64_t units = int64_t(gr.tiles_n) * gr.tiles_k * gr.splits;
+  const int64_t rest = int64_t(gr.tiles_n) * gr.tiles_k - gr.direct;
   if (TL::kLds > 65536) {
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_wgrad<DT, CODE, TL>),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, TL::kLds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((k_wgrad<DT, CODE, TL>), dim3(static_cast<unsigned>(launch_units(units, kXcdWhole))),
+  hipLaunchKernelGGL((k_wgrad<DT, CODE, TL>),
+                     dim3(static_cast<unsigned>(gr.direct + launch_units(rest * gr.splits, kXcdWhole))),
                      dim3(TL::kThreads), TL::kLds, s, a, gr);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || gr.splits == 1) return e;
+  hipLaunchKernelGGL((k_wgrad_fold<DT, TL>), dim3(static_cast<unsigned>(rest * (TL::kN * TL::kK / 8 / kThreads))),
+                     dim3(kThreads), 0, s, a, gr);
   return hipGetLastError();
 }
 
@@ -395,34 +552,24 @@ hipError_t wgrad_size(const WgradArgs& a, const WgradChoice& c, hipStream_t s) {
 }
 
 template <int DT>
-hipError_t wgrad_code(const WgradArgs& a, const WgradChoice& c, hipStream_t s) {
+hipError_t wgrad_code(const WgradArgs& a, hipStream_t s) {
+  const WgradChoice c = choose(a.rows, a.cols, a.outs);
   return a.x8.code == ZS_E4M3 ? wgrad_size<DT, ZS_E4M3>(a, c, s) : wgrad_size<DT, ZS_INT8>(a, c, s);
 }
-
-int64_t fold_pitch(int64_t row) { return (row + 3) / 4 * 4; }
 
 }  // namespace
 
 int64_t wgrad_workspace(int64_t rows, int64_t cols, int64_t outs) {
-  // 128 x 128 tiles are the most there can be (sides are bounded first so that nothing overflows)
+  // the most workgroups of 512 threads that one launch holds, counted in the smaller tile (the
+  // sides are bounded first so that nothing overflows)
+  constexpr int64_t kMaxUnits = (int64_t(1) << 23) - 64;
   if (cols > (int64_t(1) << 30) || outs > (int64_t(1) << 30)) return -1;
-  if (((outs + 127) / 128) * ((cols + 127) / 128) > kMaxUnits / 2) return -1;
-  const WgradChoice c = choose(rows, cols, outs);
-  if (c.grid.splits == 1) return 16;
-  // either orientation of dw: its rows are padded to whole groups of four
-  return int64_t(4) * c.grid.splits * std::max(outs * fold_pitch(cols), cols * fold_pitch(outs));
+  if (((outs + 127) / 128) * ((cols + 127) / 128) > kMaxUnits) return -1;
+  return choose(rows, cols, outs).workspace;
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s) {
-  WgradChoice c = choose(a.rows, a.cols, a.outs);
-  const int64_t dw_rows = a.in_major ? a.cols : a.outs, dw_cols = a.in_major ? a.outs : a.cols;
-  c.grid.pitch = fold_pitch(dw_cols);
-  hipError_t e = a.dy_dt == ZS_BF16 ? wgrad_code<ZS_BF16>(a, c, s) : wgrad_code<ZS_FP16>(a, c, s);
-  if (e != hipSuccess || c.grid.splits == 1) return e;
-  const int64_t n = dw_rows * (c.grid.pitch / 4);
-  hipLaunchKernelGGL(k_wgrad_fold, dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
-                     a.partials, c.grid.splits, dw_rows, dw_cols, c.grid.pitch, a.dw, a.base, a.dw_dt, a.dw_stride);
-  return hipGetLastError();
+  return a.dy_dt == ZS_BF16 ? wgrad_code<ZS_BF16>(a, s) : wgrad_code<ZS_FP16>(a, s);
 }
 
 }  // namespace zs
