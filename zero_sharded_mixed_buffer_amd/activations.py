@@ -17,7 +17,7 @@ A wrong type, shape, stride or device is a ValueError before anything is enqueue
 
 from __future__ import annotations
 
-import contextlib
+import ctypes
 from collections import namedtuple
 
 import torch
@@ -36,7 +36,7 @@ class Act8:
     `scales`, uint8 [rows, groups of 32], both contiguous on one GPU; `code` is "e4m3" or
     "int8".  The arrays are the caller's, or Act8.empty's."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "code", "device", "arrays")
+    __slots__ = ("codes", "scales", "rows", "cols", "code", "device", "arrays", "address")
 
     def __init__(self, codes, scales, cols, code="e4m3"):
         if code not in CODES:
@@ -47,19 +47,22 @@ class Act8:
         groups = -(-cols // GROUP)
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise ValueError("codes and scales must be uint8")
-        rows = codes.shape[0] if codes.dim() else -1
-        if codes.shape != (rows, groups * GROUP) or scales.shape != (rows, groups):
+        shape = codes.shape
+        rows = shape[0] if shape else -1
+        if shape != (rows, groups * GROUP) or scales.shape != (rows, groups):
             raise ValueError(f"a checkpoint of {cols} columns holds codes [rows, {groups * GROUP}] and scales "
                              f"[rows, {groups}], got {tuple(codes.shape)} and {tuple(scales.shape)}")
         if not codes.is_contiguous() or not scales.is_contiguous():
             raise ValueError("codes and scales must be contiguous")
-        if codes.device != scales.device:
+        device, at = codes.device, codes.data_ptr()
+        if device != scales.device:
             raise ValueError(f"codes are on {codes.device}, scales on {scales.device}")
-        if codes.data_ptr() % 16:
+        if at % 16:
             raise ValueError("codes must be 16-byte aligned")
         self.codes, self.scales, self.rows, self.cols, self.code = codes, scales, rows, cols, code
-        self.device = codes.device
-        self.arrays = A.ActArrays(codes.data_ptr(), scales.data_ptr(), CODES[code], 0)
+        self.device = device
+        self.arrays = A.ActArrays(at, scales.data_ptr(), CODES[code], 0)
+        self.address = ctypes.addressof(self.arrays)
 
     @classmethod
     def empty(cls, rows, cols, code="e4m3", device="cuda"):
@@ -91,15 +94,23 @@ def _need_gpu(device):
         raise ValueError(f"the tensors must live on a GPU, not on {device}")
 
 
-def _on(device):
-    """The device as the current one (a no-op when it is already)."""
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _enqueue(name, device, *args):
+    """Call a C entry point on the current stream of `device`, made the current device for it.
+    (The tensor checks above each call stand in for those of the ctypes wrappers; the raw stream
+    and device lookups are the ones that cost a fraction of a microsecond.)"""
+    fn = getattr(A.lib(), name)
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        A._check(status, name)
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+def _at(t):
+    return t.data_ptr() if t is not None else None
 
 
 def _matrix(t, what, dtype, rows, cols, device):
@@ -119,7 +130,7 @@ def _matrix(t, what, dtype, rows, cols, device):
 def _vector(t, what, dtypes, n, device):
     if t.dtype not in dtypes:
         raise ValueError(f"{what} is {t.dtype}, not one of {dtypes}")
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and not t.is_contiguous()):
         raise ValueError(f"{what} must be a contiguous vector of {n} elements")
     if t.device != device:
         raise ValueError(f"{what} lives on {t.device}, not on {device}")
@@ -131,7 +142,7 @@ def _checkpoint(act, what, rows, cols, device):
         raise ValueError(f"{what} is a checkpoint of {act.rows} x {act.cols}, not of {rows} x {cols}")
     if act.device != device:
         raise ValueError(f"{what} lives on {act.device}, not on {device}")
-    return act.arrays
+    return act.address
 
 
 def _input(t, what, dtypes):
@@ -161,8 +172,7 @@ def act_pack(x, act):
     rows, cols, dev = _input(x, "x", _DTYPES)
     stride = _matrix(x, "x", x.dtype, rows, cols, dev)
     arrays = _checkpoint(act, "act", rows, cols, dev)
-    with _on(dev):
-        A.zs_act_pack(x, _DTYPES[x.dtype], stride, rows, cols, arrays, _stream(dev))
+    _enqueue("zs_act_pack", dev, x.data_ptr(), _DTYPES[x.dtype], stride, rows, cols, arrays)
 
 
 def act_unpack(act, out):
@@ -170,8 +180,7 @@ def act_unpack(act, out):
     rows, cols, dev = _input(out, "out", _DTYPES)
     stride = _matrix(out, "out", out.dtype, rows, cols, dev)
     arrays = _checkpoint(act, "act", rows, cols, dev)
-    with _on(dev):
-        A.zs_act_unpack(arrays, rows, cols, out, _DTYPES[out.dtype], stride, _stream(dev))
+    _enqueue("zs_act_unpack", dev, arrays, rows, cols, out.data_ptr(), _DTYPES[out.dtype], stride)
 
 
 def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, y8=None, h8=None, rstd=None):
@@ -191,9 +200,8 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, y8=None, h8=None
         _vector(rstd, "rstd", (torch.float32,), rows, dev)
     ya = _checkpoint(y8, "y8", rows, cols, dev) if y8 is not None else None
     ha = _checkpoint(h8, "h8", rows, cols, dev) if h8 is not None else None
-    with _on(dev):
-        A.zs_rmsnorm(x, xs, residual, rs, weight, _DTYPES[dt], rows, cols, eps, h, hs, y, ys, ya, ha, rstd,
-                     _stream(dev))
+    _enqueue("zs_rmsnorm", dev, x.data_ptr(), xs, _at(residual), rs, weight.data_ptr(), _DTYPES[dt], rows, cols, eps,
+             _at(h), hs, _at(y), ys, ya, ha, _at(rstd))
 
 
 def rmsnorm_backward(dy, saved, weight, rstd, dx, dh=None, dweight=None, base=None, workspace=None):
@@ -221,10 +229,9 @@ def rmsnorm_backward(dy, saved, weight, rstd, dx, dh=None, dweight=None, base=No
         workspace, size = _workspace(workspace, A.zs_rmsnorm_workspace(rows, cols), dev)
     elif base is not None:
         raise ValueError("base without dweight")
-    with _on(dev):
-        A.zs_rmsnorm_backward(dy, dys, dh, dhs, h, hs, h8, weight, rstd, _DTYPES[dt], rows, cols, dx, dxs, dweight,
-                              _DTYPES[dweight.dtype] if dweight is not None else A.ZS_FP32, base, workspace, size,
-                              _stream(dev))
+    _enqueue("zs_rmsnorm_backward", dev, dy.data_ptr(), dys, _at(dh), dhs, _at(h), hs, h8, weight.data_ptr(),
+             rstd.data_ptr(), _DTYPES[dt], rows, cols, dx.data_ptr(), dxs, _at(dweight),
+             _DTYPES[dweight.dtype] if dweight is not None else A.ZS_FP32, _at(base), _at(workspace), size)
 
 
 def act_wgrad(x8, dy, dw, base=None, in_major=False, workspace=None):
@@ -242,9 +249,8 @@ def act_wgrad(x8, dy, dw, base=None, in_major=False, workspace=None):
     if base is not None and _matrix(base, "base", dw.dtype, *shape, dev) != dws and shape[0] > 1:
         raise ValueError("base and dw must have the same strides")
     workspace, size = _workspace(workspace, A.zs_act_wgrad_workspace(rows, x8.cols, outs), dev)
-    with _on(dev):
-        A.zs_act_wgrad(arrays, rows, x8.cols, dy, _DTYPES[dy.dtype], dys, outs, dw, _DTYPES[dw.dtype], dws, in_major,
-                       base, workspace, size, _stream(dev))
+    _enqueue("zs_act_wgrad", dev, arrays, rows, x8.cols, dy.data_ptr(), _DTYPES[dy.dtype], dys, outs, dw.data_ptr(),
+             _DTYPES[dw.dtype], dws, int(bool(in_major)), _at(base), _at(workspace), size)
 
 
 # ------------------------------------------------------------------------------ autograd
