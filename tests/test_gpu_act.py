@@ -180,6 +180,29 @@ def test_norm(Z, rows, cols, dtype, code):
         _check_codes_near(y8, y64, 4 * U, code, what + " y8")
 
 
+@pytest.mark.parametrize("cols", [96, 128, 300, 512])
+def test_norm_of_many_rows(Z, cols):
+    """Short rows by the ten thousands, where a lane takes two of them: bit for bit what the same
+    rows give a thousand at a time."""
+    rows = 33001
+    x = torch.randn(rows, cols, device="cuda", generator=torch.Generator("cuda").manual_seed(5)).to(BF16)
+    w = _matrix(1, cols, BF16, 6)[0]
+
+    def outputs(n):
+        return (torch.empty(n, cols, dtype=BF16, device="cuda"), torch.empty(n, device="cuda"), Z.Act8.empty(n, cols),
+                Z.Act8.empty(n, cols, "int8"))
+
+    y, rstd, y8, h8 = outputs(rows)
+    Z.rmsnorm(x, w, residual=x, y=y, rstd=rstd, y8=y8, h8=h8)
+    for a in range(0, rows, 1000):
+        b = min(a + 1000, rows)
+        y1, rstd1, y81, h81 = outputs(b - a)
+        Z.rmsnorm(x[a:b], w, residual=x[a:b], y=y1, rstd=rstd1, y8=y81, h8=h81)
+        assert torch.equal(y[a:b], y1) and torch.equal(rstd[a:b], rstd1)
+        for whole, part in ((y8, y81), (h8, h81)):
+            assert torch.equal(whole.codes[a:b], part.codes) and torch.equal(whole.scales[a:b], part.scales)
+
+
 def test_norm_single_outputs(Z):
     """Each output alone, and h in place of x or of the residual."""
     x, r = _matrix(6, 300, BF16, 31), _matrix(6, 300, BF16, 32)
@@ -374,12 +397,14 @@ def test_wgrad_in_a_gradient_buffer(Z):
     assert torch.equal(flat[:13], before[:13]) and torch.equal(flat[13 + 150 * 200:], before[13 + 150 * 200:])
 
 
-def test_wgrad_of_lost_groups(Z):
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_wgrad_of_lost_groups(Z, dtype, code):
     """A group that stands for NaN reaches its 32 columns of dw and no others."""
-    x = _matrix(100, 128, BF16, 111)
+    x = _matrix(100, 128, dtype, 111)
     x[77, 40] = float("nan")
     dw = torch.empty(64, 128, device="cuda")
-    Z.act_wgrad(Z.Act8.of(x), _matrix(100, 64, BF16, 112), dw)
+    Z.act_wgrad(Z.Act8.of(x, code), _matrix(100, 64, dtype, 112), dw)
     bad = torch.isnan(dw).cpu()
     assert bool(bad[:, 32:64].all()) and not bool(bad[:, :32].any()) and not bool(bad[:, 64:].any())
 
@@ -395,6 +420,23 @@ def test_wgrad_at_the_ends_of_fp16(Z):
         dw = torch.empty(4, 32, device="cuda")
         Z.act_wgrad(act, dy, dw)
         assert torch.equal(dw.cpu(), seen.float())
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_wgrad_takes_every_code(Z, dtype, code):
+    """All codes under the scale bytes whose values are normal numbers of the type (or past its
+    end), one row at a time through an identity: dw is the checkpoint's values in dy's type."""
+    lo, hi = (20, 240) if dtype == BF16 else (127, 255)
+    table = [c for c in range(256) if code == "int8" or c & 127 != 127]
+    codes = torch.tensor(table + [0] * (256 - len(table)), dtype=torch.uint8).repeat(hi - lo, 1)
+    scales = torch.arange(lo, hi).to(torch.uint8)[:, None].repeat(1, 8)
+    act = Z.Act8(codes.cuda(), scales.cuda(), 256, code)
+    dy = torch.eye(hi - lo, dtype=dtype, device="cuda")
+    dw = torch.empty(hi - lo, 256, device="cuda")
+    Z.act_wgrad(act, dy, dw)
+    want = AO.rounded(AO.values(codes, scales, 256, code), dtype).float()
+    assert torch.equal(dw.cpu(), want)
 
 
 # ------------------------------------------------------------------------------ refusals with GPU tensors

@@ -39,11 +39,10 @@ __device__ __forceinline__ v16f mfma(const v8s& a, const v8s& b, const v16f& c) 
 // An infinity in either half of a pair of fp16 values becomes the largest number: code * s may lie
 // up to one code step past it although the source did not.  NaN stays.
 __device__ __forceinline__ uint32_t fp16_range(uint32_t x) {
-  typedef unsigned short v2h __attribute__((ext_vector_type(2)));
-  const v2h one = {1, 1};
-  const v2h away = __builtin_bit_cast(v2h, (x & 0x7FFF7FFFu) ^ 0x7C007C00u);  // zero where infinite
-  const v2h keep = __builtin_elementwise_min(away, one);
-  return __builtin_bit_cast(uint32_t, static_cast<v2h>(__builtin_bit_cast(v2h, x) - one + keep));
+  typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+  const v2h top = {static_cast<_Float16>(65504.0f), static_cast<_Float16>(65504.0f)};
+  return __builtin_bit_cast(
+      uint32_t, __builtin_elementwise_maximum(__builtin_elementwise_minimum(__builtin_bit_cast(v2h, x), top), -top));
 }
 
 // Sixteen codes under scale byte b as 2-byte values in memory order.  gfx950 converts a pair of
