@@ -8,11 +8,18 @@
 // four tokens of one column per lane and load.  The checkpoint's codes become 2-byte values
 // (code * 2^k, exact) on the way into LDS, once per workgroup instead of once per wave.
 //
-// When the output has few tiles the tokens are split over several workgroups per tile; each
-// leaves its fp32 sums in the workspace and k_wgrad_fold adds them in token order: no
+// The matrix cores bound it: 2 * rows * cols * outs operations, at 1.15 to 1.25 PFLOP/s where
+// there are enough tiles (8192 tokens, 4096 -> 14336 with a bf16 base: 0.82 ms), what the library
+// reaches with operands laid out the way it likes best (1.23), and 1.3 times its rate on the
+// token-major operands that a backward pass has (0.90).  Codes in int8 need five vector
+// instructions for two values where e4m3 has one: 0.89 ms.
+//
+// Where the tiles do not fill the last round of CUs, those of it are split over the tokens; each
+// split leaves its fp32 sums in the workspace and k_wgrad_fold adds them in token order: no
 // atomics, the same result from call to call.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "zs_act_dev.h"
 
@@ -83,14 +90,17 @@ __device__ __forceinline__ void values16(const v4u& c, int b, v4u& lo, v4u& hi) 
 }
 
 // A workgroup's tile: WN x WK waves, each FN x FK matrix instructions of 32 x 32; a stage holds
-// T tokens of both operands, and there are two of them in LDS.
-template <int WN_, int WK_, int FN_, int FK_, int T_>
+// T tokens of both operands, and there are two of them in LDS.  The four rows that a transposing
+// load takes 64 bytes of must lie on different banks.  Either 64 bytes of padding behind each row
+// do that (PAD), or the 64-byte blocks of row r change places by block ^ (r % 4), which takes no
+// LDS but an address register for each instruction of the tile.
+template <int WN_, int WK_, int FN_, int FK_, int T_, bool PAD_>
 struct Tile {
+  static constexpr bool kPad = PAD_;
   static constexpr int WN = WN_, WK = WK_, FN = FN_, FK = FK_, T = T_;
   static constexpr int kThreads = WN * WK * 64;
   static constexpr int kN = WN * FN * 32, kK = WK * FK * 32;  // columns of dy, and of x8
-  // 64 bytes behind each row put the four rows of a transposing load on different banks
-  static constexpr int kPitchN = kN * 2 + 64, kPitchK = kK * 2 + 64;
+  static constexpr int kPitchN = kN * 2 + (kPad ? 64 : 0), kPitchK = kK * 2 + (kPad ? 64 : 0);
   static constexpr int kOperandN = kPitchN * T;
   static constexpr int kBuffer = kOperandN + kPitchK * T;
   static constexpr int kLoadsN = T * kN / 8 / kThreads;   // 16-byte loads per thread: dy
@@ -102,6 +112,12 @@ struct Tile {
   static constexpr int kLds = 2 * kBuffer > kStrips ? 2 * kBuffer : kStrips;
   static_assert(kLoadsN * kThreads * 8 == T * kN && kLoadsK * kThreads * 16 == T * kK, "whole loads");
   static_assert(kLds <= 163840, "LDS of a CU");
+  // a thread's rows of a stage are equal modulo 4, so that its blocks change places alike
+  static_assert(kThreads / (kN / 8) % 4 == 0 && kThreads / (kK / 16) % 4 == 0, "rows of a load");
+  // byte of column `at` (in bytes) in row `row` of an operand
+  static __device__ __forceinline__ int place(int row, int pitch, int at) {
+    return row * pitch + (kPad ? at : (at ^ ((row & 3) * 64)));
+  }
 };
 
 struct WgradTask {
@@ -128,7 +144,7 @@ struct Fetcher {
   const WgradArgs& g;
   const WgradTask& w;
   int64_t padded;
-  uint32_t off_n, off_k, off_s;
+  uint32_t off_n, off_k;     // off_k / 32 is the scale's offset
   bool whole, any_n, any_k;  // the tile lies inside; this lane's loads begin inside
   int64_t last;              // the first token that no plain stage may hold
 
@@ -137,7 +153,6 @@ struct Fetcher {
     padded = act_padded(g.cols);
     off_n = static_cast<uint32_t>(rn * g.dy_stride + (threadIdx.x % kPerRowN) * 8) * 2;
     off_k = static_cast<uint32_t>(rk * padded + (threadIdx.x % kPerRowK) * 16);
-    off_s = static_cast<uint32_t>(rk * (padded / kActGroup) + (threadIdx.x % kPerRowK) / 2);
     whole = w.n0 + TL::kN <= g.outs && w.k0 + TL::kK <= padded;
     any_n = w.n0 + static_cast<int64_t>(threadIdx.x % kPerRowN) * 8 < g.outs;
     any_k = w.k0 + static_cast<int64_t>(threadIdx.x % kPerRowK) * 16 < padded;
@@ -159,20 +174,23 @@ struct Fetcher {
 #pragma unroll
         for (int u = 0; u < TL::kLoadsK; ++u) {
           st.b[u] = *reinterpret_cast<const v4u*>(pk + u * kRowsK * padded + off_k);
-          st.scale[u] = ps[u * kRowsK * (padded / kActGroup) + off_s];
+          st.scale[u] = ps[u * kRowsK * (padded / kActGroup) + off_k / kActGroup];
         }
       }
       return;
     }
+    // the seldom way: its addresses are worked out here each time, not kept over the main loop
+    int id = threadIdx.x;
+    asm volatile("" : "+v"(id));
 #pragma unroll
     for (int u = 0; u < TL::kLoadsN; ++u) {
-      const int64_t row = t + u * kRowsN + threadIdx.x / kPerRowN, col = w.n0 + (threadIdx.x % kPerRowN) * 8;
+      const int64_t row = t + u * kRowsN + id / kPerRowN, col = w.n0 + (id % kPerRowN) * 8;
       const int64_t left = row < w.t1 ? g.outs - col : 0;
       st.a[u] = load8h(g.dy + row * g.dy_stride + col, left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0);
     }
 #pragma unroll
     for (int u = 0; u < TL::kLoadsK; ++u) {
-      const int64_t row = t + u * kRowsK + threadIdx.x / kPerRowK, col = w.k0 + (threadIdx.x % kPerRowK) * 16;
+      const int64_t row = t + u * kRowsK + id / kPerRowK, col = w.k0 + (id % kPerRowK) * 16;
       st.b[u] = v4u{0u, 0u, 0u, 0u};
       st.scale[u] = 0;
       if (row < w.t1 && col < padded) {
@@ -183,23 +201,23 @@ struct Fetcher {
   }
 };
 
-// A stage into LDS.
+// Part `part` of `parts` of a stage into LDS.
 template <int DT, int CODE, class TL>
-__device__ __forceinline__ void stage_to_lds(const Stage<TL>& st, char* buf) {
+__device__ __forceinline__ void stage_to_lds(const Stage<TL>& st, char* buf, int part, int parts) {
   constexpr int kPerRowN = TL::kN / 8, kPerRowK = TL::kK / 16;
+  constexpr int kRowsN = TL::kThreads / kPerRowN, kRowsK = TL::kThreads / kPerRowK;
+  char* pn = buf + TL::place(threadIdx.x / kPerRowN, TL::kPitchN, threadIdx.x % kPerRowN * 16);
+  char* pk = buf + TL::kOperandN + TL::place(threadIdx.x / kPerRowK, TL::kPitchK, threadIdx.x % kPerRowK * 32);
 #pragma unroll
-  for (int u = 0; u < TL::kLoadsN; ++u) {
-    const int i = u * TL::kThreads + threadIdx.x;
-    *reinterpret_cast<v4u*>(buf + (i / kPerRowN) * TL::kPitchN + (i % kPerRowN) * 16) = st.a[u];
-  }
+  for (int u = 0; u < TL::kLoadsN; ++u)
+    if (u % parts == part) *reinterpret_cast<v4u*>(pn + u * kRowsN * TL::kPitchN) = st.a[u];
 #pragma unroll
   for (int u = 0; u < TL::kLoadsK; ++u) {
-    const int i = u * TL::kThreads + threadIdx.x;
+    if (u % parts != part) continue;
     v4u lo, hi;
     values16<DT, CODE>(st.b[u], st.scale[u], lo, hi);
-    char* p = buf + TL::kOperandN + (i / kPerRowK) * TL::kPitchK + (i % kPerRowK) * 32;
-    *reinterpret_cast<v4u*>(p) = lo;
-    *reinterpret_cast<v4u*>(p + 16) = hi;
+    *reinterpret_cast<v4u*>(pk + u * kRowsK * TL::kPitchK) = lo;
+    *reinterpret_cast<v4u*>(pk + u * kRowsK * TL::kPitchK + 16) = hi;
   }
 }
 
@@ -287,10 +305,17 @@ __global__ __launch_bounds__(TL::kThreads, TL::FN* TL::FK >= 16 ? 1 : 2) void k_
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wn = wave / TL::WK * TL::FN * 32, wk = wave % TL::WK * TL::FK * 32;  // the wave's part of the tile
-  // address of the lane's transposing loads within an operand
+  // addresses of the lane's transposing loads within a buffer for each instruction of the wave's
+  // part; with padding they differ by constants
   const int lane_row = (lane >> 5) * 8 + ((lane & 15) >> 2), lane_col = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-  const int at_n = lane_row * TL::kPitchN + (wn + lane_col) * 2;
-  const int at_k = TL::kOperandN + lane_row * TL::kPitchK + (wk + lane_col) * 2;
+  int at_n[TL::FN], at_k[TL::FK];
+#pragma unroll
+  for (int i = 0; i < TL::FN; ++i)
+    at_n[i] = TL::kPad && i > 0 ? at_n[0] + i * 64 : TL::place(lane_row, TL::kPitchN, (wn + i * 32 + lane_col) * 2);
+#pragma unroll
+  for (int j = 0; j < TL::FK; ++j)
+    at_k[j] = TL::kPad && j > 0 ? at_k[0] + j * 64
+                                : TL::kOperandN + TL::place(lane_row, TL::kPitchK, (wk + j * 32 + lane_col) * 2);
 
   v16f acc[TL::FN][TL::FK];
 #pragma unroll
@@ -303,29 +328,33 @@ __global__ __launch_bounds__(TL::kThreads, TL::FN* TL::FK >= 16 ? 1 : 2) void k_
   };
   auto read = [&](Operands& f, const char* buf, int step) {
 #pragma unroll
-    for (int i = 0; i < TL::FN; ++i) f.a[i] = read_operand<TL::kPitchN>(buf + at_n + step * 16 * TL::kPitchN + i * 64);
+    for (int i = 0; i < TL::FN; ++i) f.a[i] = read_operand<TL::kPitchN>(buf + at_n[i] + step * 16 * TL::kPitchN);
 #pragma unroll
-    for (int j = 0; j < TL::FK; ++j) f.b[j] = read_operand<TL::kPitchK>(buf + at_k + step * 16 * TL::kPitchK + j * 64);
+    for (int j = 0; j < TL::FK; ++j) f.b[j] = read_operand<TL::kPitchK>(buf + at_k[j] + step * 16 * TL::kPitchK);
   };
-  auto multiply = [&](const Operands& f) {
+  auto multiply = [&](const Operands& f, int from = 0, int to = TL::FN) {
 #pragma unroll
-    for (int i = 0; i < TL::FN; ++i)
+    for (int i = from; i < to; ++i)
 #pragma unroll
       for (int j = 0; j < TL::FK; ++j) acc[i][j] = mfma<DT>(f.a[i], f.b[j], acc[i][j]);
   };
   // Between two matrix instructions: a share of the next step's LDS reads, of the conversions and
   // of the LDS writes, so that the matrix cores do not wait for any of them.
-  auto interleave = [&]() {
-    constexpr int kM = TL::FN * TL::FK, kReads = 2 * (TL::FN + TL::FK);
-    constexpr int kEach = (kReads + kM - 1) / kM;
+  auto interleave = [&](auto matrix, auto reads) {
+    constexpr int kM = decltype(matrix)::value, kReads = decltype(reads)::value;
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // matrix
-      __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);  // LDS reads
-      __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);      // vector
-      __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);      // LDS writes
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                        // matrix
+      __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kM - 1) / kM, 0);  // LDS reads
+      __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);                        // vector
+      __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);                        // LDS writes
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
+  constexpr std::integral_constant<int, TL::FN * TL::FK> kAll{};
+  constexpr std::integral_constant<int, TL::FN * TL::FK / 2> kHalf{};
+  constexpr std::integral_constant<int, 2 * (TL::FN + TL::FK)> kReads{};
+  constexpr std::integral_constant<int, 0> kNone{};
   // One barrier per stage.  While stage i is multiplied from one LDS buffer, stage i + 1 goes from
   // registers into the other, whose readers passed the barrier of stage i - 1, during the first
   // step; then stage i + 2 sets out from memory.  The operands of a step are read during the step
@@ -338,27 +367,32 @@ __global__ __launch_bounds__(TL::kThreads, TL::FN* TL::FK >= 16 ? 1 : 2) void k_
     Stage<TL> st{};
     Operands f[2];
     fetch(w.t0, st);
-    stage_to_lds<DT, CODE, TL>(st, lds);
+    stage_to_lds<DT, CODE, TL>(st, lds, 0, 1);
     if (stages > 1) fetch(w.t0 + TL::T, st);
     __syncthreads();
     read(f[0], lds, 0);
     char* cur = lds;
     char* other = lds + TL::kBuffer;
     for (int64_t i = 0; i + 1 < stages; ++i) {
+      // the first step, in halves: the conversions of one are done before those of the other begin
+      read(f[1], cur, 1);
+      multiply(f[0], 0, TL::FN / 2);
+      stage_to_lds<DT, CODE, TL>(st, other, 0, 2);
+      interleave(kHalf, kReads);
+      multiply(f[0], TL::FN / 2, TL::FN);
+      stage_to_lds<DT, CODE, TL>(st, other, 1, 2);
+      interleave(kHalf, kNone);
+      if (i + 2 < stages) fetch(w.t0 + (i + 2) * TL::T, st);
 #pragma unroll
-      for (int step = 0; step + 1 < kSteps; ++step) {
+      for (int step = 1; step + 1 < kSteps; ++step) {
         read(f[(step + 1) & 1], cur, step + 1);
         multiply(f[step & 1]);
-        if (step == 0) stage_to_lds<DT, CODE, TL>(st, other);
-        interleave();
-        __builtin_amdgcn_sched_barrier(0);
-        if (step == 0 && i + 2 < stages) fetch(w.t0 + (i + 2) * TL::T, st);
+        interleave(kAll, kReads);
       }
       __syncthreads();
       read(f[0], other, 0);
       multiply(f[(kSteps - 1) & 1]);
-      interleave();
-      __builtin_amdgcn_sched_barrier(0);
+      interleave(kAll, kReads);
       char* x = cur;
       cur = other;
       other = x;
@@ -367,8 +401,7 @@ __global__ __launch_bounds__(TL::kThreads, TL::FN* TL::FK >= 16 ? 1 : 2) void k_
     for (int step = 0; step < kSteps; ++step) {
       if (step + 1 < kSteps) read(f[(step + 1) & 1], cur, step + 1);
       multiply(f[step & 1]);
-      interleave();
-      __builtin_amdgcn_sched_barrier(0);
+      interleave(kAll, kReads);
     }
     __syncthreads();  // the strips below reuse the buffers
   }
@@ -465,11 +498,15 @@ __global__ __launch_bounds__(kThreads) void k_wgrad_fold(WgradArgs g, WgradGrid 
 
 // ------------------------------------------------------------------ launch choices
 
-using SmallTile = Tile<2, 2, 2, 2, 32>;  // 128 x 128
-#ifndef ZS_LARGE
-#define ZS_LARGE 2, 4, 4, 2, 64
-#endif
-using LargeTile = Tile<ZS_LARGE>;  // 256 x 256
+// Both tiles take stages of 64 tokens.  The large one, one workgroup of eight waves to a CU, reads
+// half as many operand bytes from L2 and LDS for each product: 8192 x 4096 -> 4096 in 219 us (1.25
+// PFLOP/s) against 303.  The small one, two workgroups of four waves to a CU, serves outputs with
+// few large tiles: 16384 x 1024 -> 1024 in 52 us against 54, 1024 x 1024 -> 4096 in 16 against 28
+// (four splits).  Wave shapes of 4 x 4 instructions (half the waves, less LDS traffic still) took 298
+// us at 8192 x 4096 -> 4096 and stages of 32 tokens 231, where 64 took 228.
+using SmallTile = Tile<2, 2, 2, 2, 64, false>;  // 128 x 128
+using LargeTile = Tile<2, 4, 4, 2, 64, true>;   // 256 x 256
+
 struct WgradChoice {
   bool large;
   WgradGrid grid;
@@ -478,26 +515,25 @@ struct WgradChoice {
 
 // Time of a launch in microseconds as a function of the tile, the tiles done directly and the
 // splits of the others, from what the kernels measure on MI355X (256 CUs): a stage of the large
-// tile, one workgroup to a CU, and of the small one, up to three to a CU; the start and end of
-// a workgroup; the partial sums on their way to memory and back, and the launch that folds them.
+// tile, one workgroup to a CU, and of the small one, one or two to a CU; the start and end of
+// a workgroup; the partial sums and the launch that folds them.  Within 10 % of the best choice
+// on fourteen shapes from 128 x 64 -> 256 to 8192 x 4096 -> 14336.
 template <class TL>
 double launch_cost(int64_t tiles, int64_t direct, int64_t splits, int64_t stages) {
-  constexpr bool kBig = TL::kN == 256;
   auto rounds = [&](int64_t units, int64_t n) {
-    if (kBig) return double((units + 255) / 256) * (n * 1.75 + 6.0);
-    const int64_t full = units / 768, rest = units % 768;
-    const double q = rest == 0 ? 0.0 : rest <= 256 ? 0.5 : rest <= 512 ? 0.7 : 1.0;
-    return (full + q) * (n * 0.85 + 4.0);
+    if (TL::kN == 256) return double((units + 255) / 256) * (n * 1.65 + (splits > 1 ? 8.0 : 6.0));
+    const int64_t full = units / 512, rest = units % 512;
+    return full * (n * 1.22 + 4.0) + (rest == 0 ? 0.0 : rest <= 256 ? n * 0.74 + 4.0 : n * 1.22 + 4.0);
   };
   double t = direct > 0 ? rounds(direct, stages) : 0.0;
   if (tiles > direct) t += rounds((tiles - direct) * splits, (stages + splits - 1) / splits);
-  if (splits > 1) t += 5.0 + double(tiles - direct) * splits * (TL::kN * TL::kK) * 8 / 5.0e6;
+  if (splits > 1) t += 4.0 + double(tiles - direct) * splits * (TL::kN * TL::kK) * 4 / 6.0e6;
   return t;
 }
 
 template <class TL>
 void consider(int64_t rows, int64_t cols, int64_t outs, WgradChoice* best, double* cost) {
-  constexpr int64_t kSlots = TL::kN == 256 ? 256 : 768;
+  constexpr int64_t kSlots = TL::kN == 256 ? 256 : 512;
   const int64_t tn = (outs + TL::kN - 1) / TL::kN, tk = (cols + TL::kK - 1) / TL::kK, tiles = tn * tk;
   const int64_t stages = std::max<int64_t>(1, (rows + TL::T - 1) / TL::T);
   const int64_t whole = tiles / kSlots * kSlots;
