@@ -381,6 +381,86 @@ def test_wgrad(Z, rows, cols, outs, dtype, grad, code):
         assert torch.equal(turned.t(), dw)
 
 
+# (tokens, cols, outs) that take: one round of large tiles; large tiles with edges; large
+# tiles of which the last are split; the same of small tiles; small tiles alone; splits of few
+LARGE = [(512, 4096, 4096), (1100, 2051, 4099), (1030, 4097, 4100), (4097, 2051, 4099), (640, 4096, 5000), (9000, 512, 700)]
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("rows,cols,outs", LARGE)
+def test_wgrad_of_large_weights(Z, rows, cols, outs, dtype, code):
+    """Whole numbers again, at sizes that take every tile and split, in both orientations, with
+    NaN behind each row of dy; the reference is an exact product in 64 bits on the GPU."""
+    g = torch.Generator("cuda").manual_seed(121)
+    x = torch.randint(-3, 4, (rows, cols), device="cuda", generator=g).to(dtype)
+    wide = torch.full((rows, outs + 9), float("nan"), dtype=dtype, device="cuda")
+    wide[:, :outs] = torch.randint(-2, 3, (rows, outs), device="cuda", generator=g).to(dtype)
+    dy = wide[:, :outs]
+    act = Z.Act8.of(x, code)
+    want = dy.double().t().contiguous() @ x.double()
+    for in_major in (False, True):
+        ref = want.t() if in_major else want
+        dw = torch.full(ref.shape, 7.0, device="cuda")
+        Z.act_wgrad(act, dy, dw, in_major=in_major)
+        assert torch.equal(dw.double(), ref)
+        half = torch.zeros(ref.shape, dtype=dtype, device="cuda")
+        Z.act_wgrad(act, dy, half, base=half, in_major=in_major)
+        assert torch.equal(half, ref.to(dtype))
+
+
+def test_offsets_past_32_bits(Z):
+    """Matrices of more than 2^32 elements (and bytes of codes): their last rows, packed, read
+    back, normalised, differentiated and multiplied like the same rows by themselves."""
+    rows, cols = 270000, 16000
+    x = torch.empty(rows, cols, dtype=BF16, device="cuda")
+    x.normal_(generator=torch.Generator("cuda").manual_seed(131))
+    tail = slice(rows - 300, rows)
+    act = Z.Act8.of(x)
+    part = Z.Act8.of(x[tail])
+    assert torch.equal(act.codes[tail], part.codes) and torch.equal(act.scales[tail], part.scales)
+    back = act.unpack()
+    assert torch.equal(back[tail], part.unpack())
+    del back
+    w = _matrix(1, cols, BF16, 132)[0]
+    y, rstd = torch.empty_like(x), torch.empty(rows, device="cuda")
+    Z.rmsnorm(x, w, y=y, rstd=rstd)
+    y1, rstd1 = torch.empty(300, cols, dtype=BF16, device="cuda"), torch.empty(300, device="cuda")
+    Z.rmsnorm(x[tail], w, y=y1, rstd=rstd1)
+    assert torch.equal(y[tail], y1) and torch.equal(rstd[tail], rstd1)
+    Z.rmsnorm_backward(x, act, w, rstd, y)
+    Z.rmsnorm_backward(x[tail], part, w, rstd1, y1)
+    assert torch.equal(y[tail], y1)
+    # the weight gradient: whole numbers in the last rows, zeros before them
+    del y, act
+    x.zero_()
+    x[tail] = torch.randint(-2, 3, (300, cols), device="cuda").to(BF16)
+    other = torch.zeros(rows, 64, dtype=BF16, device="cuda")
+    other[tail] = torch.randint(-2, 3, (300, 64), device="cuda").to(BF16)
+    for wide, narrow in ((x, other), (other, x)):
+        dw = torch.empty(narrow.shape[1], wide.shape[1], device="cuda")
+        Z.act_wgrad(Z.Act8.of(wide), narrow, dw)
+        assert torch.equal(dw.double(), narrow[tail].double().t().contiguous() @ wide[tail].double())
+
+
+def test_checkpoint_storage_may_move(Z):
+    """A checkpoint whose storage was freed and allocated again is found where it is now; freed
+    storage is refused."""
+    x = _matrix(40, 64, BF16, 141)
+    act = Z.Act8.of(x)
+    keep = act.codes.clone()
+    storage = act.codes.untyped_storage()
+    n = storage.nbytes()
+    storage.resize_(0)
+    with pytest.raises(ValueError):
+        Z.act_unpack(act, x)
+    block = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")  # takes the place that was free
+    storage.resize_(n)
+    act.codes.copy_(keep)
+    assert torch.equal(act.unpack().cpu().double(), AO.values(*AO.quantise(x, "e4m3"), 64, "e4m3"))
+    del block
+
+
 def test_wgrad_in_a_gradient_buffer(Z):
     """dw as an unaligned slice of a flat bf16 buffer, added to what is there; the neighbours
     keep their bits."""

@@ -298,6 +298,25 @@ def test_captured_and_replayed(Z):
             assert all(torch.equal(a, b) for a, b in zip(replayed[i], want)), (turn, i)
 
 
+def test_captured_large_weight_gradient(Z):
+    """The large tile's launch, captured and replayed, and the one with split tiles."""
+    for rows, cols, outs in ((512, 4096, 4096), (1030, 4097, 4100)):
+        x, dy = _randn((rows, cols), BF16, 601), _randn((rows, outs), BF16, 602, 0.01)
+        act = Z.Act8.of(x)
+        dw, eager = torch.empty(outs, cols, dtype=BF16, device="cuda"), torch.empty(outs, cols, dtype=BF16, device="cuda")
+        ws = torch.empty(Z.zs_act_wgrad_workspace(rows, cols, outs), dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            Z.act_wgrad(act, dy, dw, workspace=ws)
+        for turn in range(3):
+            dy.copy_(_randn((rows, outs), BF16, 610 + turn, 0.01))
+            graph.replay()
+            torch.cuda.synchronize()
+            Z.act_wgrad(act, dy, eager)
+            assert torch.equal(dw, eager)
+
+
 def test_captured_training_pass(Z):
     """Forward and backward of the block captured whole, gradients added to the flat buffer: each
     replay adds the same gradient again."""

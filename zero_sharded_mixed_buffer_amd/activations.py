@@ -38,6 +38,9 @@ class Act8:
 
     __slots__ = ("codes", "scales", "rows", "cols", "code", "device", "arrays", "address")
 
+    # `arrays` is the struct that the C calls read; every call writes the tensors' present
+    # addresses into it, so that storage which was freed and allocated again is found
+
     def __init__(self, codes, scales, cols, code="e4m3"):
         if code not in CODES:
             raise ValueError(f"code is 'e4m3' or 'int8', not {code!r}")
@@ -54,14 +57,12 @@ class Act8:
                              f"[rows, {groups}], got {tuple(codes.shape)} and {tuple(scales.shape)}")
         if not codes.is_contiguous() or not scales.is_contiguous():
             raise ValueError("codes and scales must be contiguous")
-        device, at = codes.device, codes.data_ptr()
+        device = codes.device
         if device != scales.device:
             raise ValueError(f"codes are on {codes.device}, scales on {scales.device}")
-        if at % 16:
-            raise ValueError("codes must be 16-byte aligned")
         self.codes, self.scales, self.rows, self.cols, self.code = codes, scales, rows, cols, code
         self.device = device
-        self.arrays = A.ActArrays(at, scales.data_ptr(), CODES[code], 0)
+        self.arrays = A.ActArrays(0, 0, CODES[code], 0)
         self.address = ctypes.addressof(self.arrays)
 
     @classmethod
@@ -142,6 +143,8 @@ def _checkpoint(act, what, rows, cols, device):
         raise ValueError(f"{what} is a checkpoint of {act.rows} x {act.cols}, not of {rows} x {cols}")
     if act.device != device:
         raise ValueError(f"{what} lives on {act.device}, not on {device}")
+    arrays = act.arrays
+    arrays.codes, arrays.scales = act.codes.data_ptr(), act.scales.data_ptr()
     return act.address
 
 
