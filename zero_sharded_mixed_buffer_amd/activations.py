@@ -149,12 +149,21 @@ def _checkpoint(act, what, rows, cols, device):
 
 
 def _input(t, what, dtypes):
-    if t.dim() != 2 or t.shape[1] < 1:
-        raise ValueError(f"{what} must be a matrix with at least one column, got shape {tuple(t.shape)}")
+    """Check the argument that sets a call's sizes; returns its rows, columns, device and row
+    stride."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"{what} must be a matrix with at least one column, got shape {tuple(shape)}")
     if t.dtype not in dtypes:
-        raise ValueError(f"{what} is {t.dtype}, not one of {dtypes}")
-    _need_gpu(t.device)
-    return t.shape[0], t.shape[1], t.device
+        raise ValueError(f"{what} is {t.dtype}, not one of {tuple(dtypes)}")
+    device = t.device
+    if not t.is_cuda:
+        _need_gpu(device)
+    rows, cols = shape
+    row, col = t.stride()
+    if col != 1 and cols > 1:
+        raise ValueError(f"{what}: the columns must be consecutive (its stride is {t.stride()})")
+    return rows, cols, device, row
 
 
 def _workspace(workspace, need, device):
@@ -172,16 +181,14 @@ def _workspace(workspace, need, device):
 
 def act_pack(x, act):
     """Write the checkpoint of matrix x (bf16, fp16 or fp32; any row stride) into `act`."""
-    rows, cols, dev = _input(x, "x", _DTYPES)
-    stride = _matrix(x, "x", x.dtype, rows, cols, dev)
+    rows, cols, dev, stride = _input(x, "x", _DTYPES)
     arrays = _checkpoint(act, "act", rows, cols, dev)
     _enqueue("zs_act_pack", dev, x.data_ptr(), _DTYPES[x.dtype], stride, rows, cols, arrays)
 
 
 def act_unpack(act, out):
     """Read a checkpoint back into matrix `out` (bf16, fp16 or fp32; any row stride)."""
-    rows, cols, dev = _input(out, "out", _DTYPES)
-    stride = _matrix(out, "out", out.dtype, rows, cols, dev)
+    rows, cols, dev, stride = _input(out, "out", _DTYPES)
     arrays = _checkpoint(act, "act", rows, cols, dev)
     _enqueue("zs_act_unpack", dev, arrays, rows, cols, out.data_ptr(), _DTYPES[out.dtype], stride)
 
@@ -190,9 +197,8 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, y8=None, h8=None
     """h = x + residual, rstd = (mean(h^2) + eps)^-1/2 per row, y = h * rstd * weight, in one
     pass; every output that is given is written: h, y (matrices of x's dtype), y8, h8
     (checkpoints of y and h), rstd (fp32 vector).  h may be x or residual itself."""
-    rows, cols, dev = _input(x, "x", HALF)
+    rows, cols, dev, xs = _input(x, "x", HALF)
     dt = x.dtype
-    xs = _matrix(x, "x", dt, rows, cols, dev)
     _vector(weight, "weight", (dt,), cols, dev)
     rs = _matrix(residual, "residual", dt, rows, cols, dev) if residual is not None else 0
     hs = _matrix(h, "h", dt, rows, cols, dev) if h is not None else 0
@@ -212,9 +218,8 @@ def rmsnorm_backward(dy, saved, weight, rstd, dx, dh=None, dweight=None, base=No
     given, dh, the gradient that reaches h by other ways; dweight (bf16, fp16 or fp32) = base +
     the weight's gradient.  `saved` is h or its Act8.  base may be dweight itself: the gradient
     is then added to what is there.  dx may be dy or dh."""
-    rows, cols, dev = _input(dy, "dy", HALF)
+    rows, cols, dev, dys = _input(dy, "dy", HALF)
     dt = dy.dtype
-    dys = _matrix(dy, "dy", dt, rows, cols, dev)
     dxs = _matrix(dx, "dx", dt, rows, cols, dev)
     dhs = _matrix(dh, "dh", dt, rows, cols, dev) if dh is not None else 0
     _vector(weight, "weight", (dt,), cols, dev)
@@ -242,8 +247,7 @@ def act_wgrad(x8, dy, dw, base=None, in_major=False, workspace=None):
     gradient dy [rows, outs] of y.  dw is [outs, cols], or [cols, outs] with in_major (weights
     kept as (in, out)), in dy's dtype or fp32; base has dw's dtype, shape and stride and may be
     dw itself: the gradient is then added to what is there."""
-    rows, outs, dev = _input(dy, "dy", HALF)
-    dys = _matrix(dy, "dy", dy.dtype, rows, outs, dev)
+    rows, outs, dev, dys = _input(dy, "dy", HALF)
     arrays = _checkpoint(x8, "x8", rows, x8.cols, dev)
     shape = (x8.cols, outs) if in_major else (outs, x8.cols)
     if dw.dtype not in (dy.dtype, torch.float32):

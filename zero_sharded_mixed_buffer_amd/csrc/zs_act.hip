@@ -16,38 +16,49 @@ using namespace act;
 
 // ------------------------------------------------------------------ pack, unpack
 
-constexpr int kChunksPerThread = 4;
-constexpr int kChunksPerBlock = kThreads * kChunksPerThread;
-
-// Row and chunk of task `first + k` (k < kChunksPerBlock), chunks_per_row to a row: one 64-bit
-// division per workgroup, a 32-bit one per chunk.
-struct ChunkAt {
-  int64_t row;
-  uint32_t chunk;
+// Task t of a matrix is chunk t % chunks_per_row of row t / chunks_per_row; a workgroup takes U * 256
+// consecutive ones.  One wide division per workgroup finds its first row, a 32-bit one per chunk
+// the others; a matrix without gaps is one long row and needs neither.
+struct Tasks {
+  int64_t row0;
+  uint32_t rem0, chunks_per_row;
+  bool one;
+  __device__ __forceinline__ Tasks(int64_t first, int64_t ntasks, uint32_t cpr) : chunks_per_row(cpr) {
+    one = ntasks <= cpr;
+    if (one)
+      row0 = 0;
+    else if (ntasks <= 0xFFFFFFFFll)
+      row0 = static_cast<uint32_t>(first) / cpr;
+    else
+      row0 = first / cpr;
+    rem0 = static_cast<uint32_t>(first - row0 * cpr);
+  }
+  __device__ __forceinline__ void at(uint32_t k, int64_t* row, uint32_t* chunk) const {
+    const uint32_t r = rem0 + k;
+    const uint32_t d = one ? 0 : r / chunks_per_row;
+    *row = row0 + d;
+    *chunk = r - d * chunks_per_row;
+  }
 };
-__device__ __forceinline__ ChunkAt chunk_at(int64_t row0, uint32_t rem0, uint32_t k, uint32_t chunks_per_row) {
-  const uint32_t r = rem0 + k;
-  const uint32_t d = r / chunks_per_row;
-  return {row0 + d, r - d * chunks_per_row};
-}
 
 __device__ __forceinline__ int clamp_count(int64_t left) { return left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0; }
 
 // Reads 2 (or 4) bytes and writes 1.03 per element.
-template <int DT, int CODE>
+template <int DT, int CODE, int U>
 __global__ __launch_bounds__(kThreads) void k_act_pack(const void* __restrict__ src, int64_t stride, int64_t cols,
                                                        uint32_t chunks_per_row, int64_t ntasks,
                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const int64_t first = int64_t(blockIdx.x) * kChunksPerBlock;
-  const int64_t row0 = first / chunks_per_row;
-  const uint32_t rem0 = static_cast<uint32_t>(first - row0 * chunks_per_row);
-  float f[kChunksPerThread][8];
+  const int64_t first = int64_t(blockIdx.x) * (U * kThreads);
+  const Tasks tasks(first, ntasks, chunks_per_row);
+  float f[U][8];
 #pragma unroll
-  for (int u = 0; u < kChunksPerThread; ++u) {
+  for (int u = 0; u < U; ++u) {
     const uint32_t k = u * kThreads + threadIdx.x;
-    const ChunkAt at = chunk_at(row0, rem0, k, chunks_per_row);
-    const int cnt = first + k < ntasks ? clamp_count(cols - int64_t(at.chunk) * 8) : 0;
-    const int64_t e = at.row * stride + int64_t(at.chunk) * 8;
+    int64_t row;
+    uint32_t chunk;
+    tasks.at(k, &row, &chunk);
+    const int cnt = first + k < ntasks ? clamp_count(cols - int64_t(chunk) * 8) : 0;
+    const int64_t e = row * stride + int64_t(chunk) * 8;
     if constexpr (DT == ZS_FP32) {
       const float* p = static_cast<const float*>(src) + e;
 #pragma unroll
@@ -70,24 +81,23 @@ __global__ __launch_bounds__(kThreads) void k_act_pack(const void* __restrict__ 
     }
   }
 #pragma unroll
-  for (int u = 0; u < kChunksPerThread; ++u) {
+  for (int u = 0; u < U; ++u) {
     const int64_t t = first + u * kThreads + threadIdx.x;
     if (t < ntasks) encode_store<CODE>(f[u], codes, scales, t);
   }
 }
 
-template <int DT, int CODE>
+template <int DT, int CODE, int U>
 __global__ __launch_bounds__(kThreads) void k_act_unpack(const uint8_t* __restrict__ codes,
                                                          const uint8_t* __restrict__ scales, int64_t cols,
                                                          uint32_t chunks_per_row, int64_t ntasks,
                                                          void* __restrict__ dst, int64_t stride) {
-  const int64_t first = int64_t(blockIdx.x) * kChunksPerBlock;
-  const int64_t row0 = first / chunks_per_row;
-  const uint32_t rem0 = static_cast<uint32_t>(first - row0 * chunks_per_row);
-  v2u c[kChunksPerThread];
-  int b[kChunksPerThread];
+  const int64_t first = int64_t(blockIdx.x) * (U * kThreads);
+  const Tasks tasks(first, ntasks, chunks_per_row);
+  v2u c[U];
+  int b[U];
 #pragma unroll
-  for (int u = 0; u < kChunksPerThread; ++u) {
+  for (int u = 0; u < U; ++u) {
     const int64_t t = first + u * kThreads + threadIdx.x;
     c[u] = v2u{0u, 0u};
     b[u] = 0;
@@ -97,12 +107,14 @@ __global__ __launch_bounds__(kThreads) void k_act_unpack(const uint8_t* __restri
     }
   }
 #pragma unroll
-  for (int u = 0; u < kChunksPerThread; ++u) {
+  for (int u = 0; u < U; ++u) {
     const uint32_t k = u * kThreads + threadIdx.x;
-    const ChunkAt at = chunk_at(row0, rem0, k, chunks_per_row);
-    const int cnt = first + k < ntasks ? clamp_count(cols - int64_t(at.chunk) * 8) : 0;
+    int64_t row;
+    uint32_t chunk;
+    tasks.at(k, &row, &chunk);
+    const int cnt = first + k < ntasks ? clamp_count(cols - int64_t(chunk) * 8) : 0;
     if (cnt == 0) continue;
-    const int64_t e = at.row * stride + int64_t(at.chunk) * 8;
+    const int64_t e = row * stride + int64_t(chunk) * 8;
     float f[8];
     decode8<CODE>(c[u], scale_value(b[u]), f);
     if constexpr (DT == ZS_FP32) {
@@ -259,7 +271,7 @@ __global__ __launch_bounds__(norm_block<LPR>()) void k_rmsnorm(NormArgs a) {
       float w[8];
       widen8<DT>(load8h(a.weight + col, cnt), w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = j < cnt ? f[j] * rstd * w[j] : 0.0f;
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];  // zeros behind the row, unless all of it is NaN
       if (a.y != nullptr) store8h(a.y + row * a.y_stride + col, narrow8<DT>(f), cnt);
       if (a.y8.codes != nullptr) {
         if (a.y8.code == ZS_E4M3)
@@ -467,29 +479,55 @@ __global__ __launch_bounds__(kFoldCols* kFoldSlices) void k_dweight(const float*
 
 // ------------------------------------------------------------------ launch choices
 
+// Four chunks to a thread keep enough loads in flight on their own; with fewer than eight
+// workgroups to a CU that way, one chunk to a thread spreads the work (4097 x 1003 int8: pack
+// 7.6 -> 5.7 us, unpack 7.2 -> 4.9).
+constexpr int64_t kFewChunks = int64_t(8) * 256 * 4 * kThreads;
+
+template <int DT, int CODE, int U>
+hipError_t pack_launch(const void* src, int64_t stride, int64_t cols, uint32_t cpr, int64_t n, const Act& act,
+                       hipStream_t s) {
+  hipLaunchKernelGGL((k_act_pack<DT, CODE, U>), dim3(static_cast<unsigned>((n + U * kThreads - 1) / (U * kThreads))),
+                     dim3(kThreads), 0, s, src, stride, cols, cpr, n, act.codes, act.scales);
+  return hipGetLastError();
+}
+template <int DT, int CODE>
+hipError_t pack_size(const void* src, int64_t stride, int64_t cols, uint32_t cpr, int64_t n, const Act& act,
+                     hipStream_t s) {
+  return n < kFewChunks ? pack_launch<DT, CODE, 1>(src, stride, cols, cpr, n, act, s)
+                        : pack_launch<DT, CODE, 4>(src, stride, cols, cpr, n, act, s);
+}
 template <int DT>
 hipError_t pack_code(const void* src, int64_t stride, int64_t cols, uint32_t cpr, int64_t n, const Act& act,
                      hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((n + kChunksPerBlock - 1) / kChunksPerBlock));
-  if (act.code == ZS_E4M3)
-    hipLaunchKernelGGL((k_act_pack<DT, ZS_E4M3>), grid, dim3(kThreads), 0, s, src, stride, cols, cpr, n, act.codes,
-                       act.scales);
-  else
-    hipLaunchKernelGGL((k_act_pack<DT, ZS_INT8>), grid, dim3(kThreads), 0, s, src, stride, cols, cpr, n, act.codes,
-                       act.scales);
-  return hipGetLastError();
+  return act.code == ZS_E4M3 ? pack_size<DT, ZS_E4M3>(src, stride, cols, cpr, n, act, s)
+                             : pack_size<DT, ZS_INT8>(src, stride, cols, cpr, n, act, s);
 }
 
+template <int DT, int CODE, int U>
+hipError_t unpack_launch(const Act& act, int64_t cols, uint32_t cpr, int64_t n, void* dst, int64_t stride,
+                         hipStream_t s) {
+  hipLaunchKernelGGL((k_act_unpack<DT, CODE, U>), dim3(static_cast<unsigned>((n + U * kThreads - 1) / (U * kThreads))),
+                     dim3(kThreads), 0, s, act.codes, act.scales, cols, cpr, n, dst, stride);
+  return hipGetLastError();
+}
+template <int DT, int CODE>
+hipError_t unpack_size(const Act& act, int64_t cols, uint32_t cpr, int64_t n, void* dst, int64_t stride, hipStream_t s) {
+  return n < kFewChunks ? unpack_launch<DT, CODE, 1>(act, cols, cpr, n, dst, stride, s)
+                        : unpack_launch<DT, CODE, 4>(act, cols, cpr, n, dst, stride, s);
+}
 template <int DT>
 hipError_t unpack_code(const Act& act, int64_t cols, uint32_t cpr, int64_t n, void* dst, int64_t stride, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((n + kChunksPerBlock - 1) / kChunksPerBlock));
-  if (act.code == ZS_E4M3)
-    hipLaunchKernelGGL((k_act_unpack<DT, ZS_E4M3>), grid, dim3(kThreads), 0, s, act.codes, act.scales, cols, cpr, n,
-                       dst, stride);
-  else
-    hipLaunchKernelGGL((k_act_unpack<DT, ZS_INT8>), grid, dim3(kThreads), 0, s, act.codes, act.scales, cols, cpr, n,
-                       dst, stride);
-  return hipGetLastError();
+  return act.code == ZS_E4M3 ? unpack_size<DT, ZS_E4M3>(act, cols, cpr, n, dst, stride, s)
+                             : unpack_size<DT, ZS_INT8>(act, cols, cpr, n, dst, stride, s);
+}
+
+// A matrix without gaps between its rows, whole groups to a row, is one row.
+void one_row(int64_t stride, int64_t* rows, int64_t* cols) {
+  if (*rows > 1 && stride == *cols && *cols % kActPad == 0 && *cols / 8 <= (int64_t(1) << 31) / *rows) {
+    *cols *= *rows;
+    *rows = 1;
+  }
 }
 
 template <int DT, int LPR, int V, int R = 1>
@@ -548,6 +586,7 @@ hipError_t backward_saved(const NormBackwardArgs& a, hipStream_t s) {
 
 hipError_t launch_act_pack(const void* src, int dt, int64_t stride, int64_t rows, int64_t cols, const Act& act,
                            hipStream_t s) {
+  one_row(stride, &rows, &cols);
   const uint32_t cpr = static_cast<uint32_t>(act_padded(cols) / 8);
   const int64_t n = rows * cpr;
   if (n == 0) return hipSuccess;
@@ -558,6 +597,7 @@ hipError_t launch_act_pack(const void* src, int dt, int64_t stride, int64_t rows
 
 hipError_t launch_act_unpack(const Act& act, int64_t rows, int64_t cols, void* dst, int dt, int64_t stride,
                              hipStream_t s) {
+  one_row(stride, &rows, &cols);
   const uint32_t cpr = static_cast<uint32_t>(act_padded(cols) / 8);
   const int64_t n = rows * cpr;
   if (n == 0) return hipSuccess;

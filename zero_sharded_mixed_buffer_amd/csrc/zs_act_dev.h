@@ -108,23 +108,26 @@ __device__ __forceinline__ float scale_value(int b) {
 __device__ __forceinline__ float scale_inverse(int b) { return bits_f(static_cast<uint32_t>(254 - b) << 23); }
 
 // Codes of eight values under scale byte b: x / s is exact (a power of two), the rounding to
-// the code is the only one.  For int8 the sum with 1.5 * 2^23 rounds to an integer, to
-// nearest even, whose low byte is the code.
+// the code is the only one.  gfx950 divides and rounds a pair to e4m3 in one instruction, which
+// takes the scale from the exponent field alone.  For int8 the sum with 1.5 * 2^23 rounds to an
+// integer, to nearest even, whose low byte is the code.
 template <int CODE>
 __device__ __forceinline__ v2u encode8(const float (&f)[8], int b) {
   if (b == 255) return v2u{0u, 0u};
-  const float inv = scale_inverse(b);
   v2u c;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const float* q = f + 4 * j;
     if constexpr (CODE == ZS_E4M3) {
-      int w = 0;
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0] * inv, q[1] * inv, w, false);
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2] * inv, q[3] * inv, w, true);
-      c[j] = static_cast<uint32_t>(w);
+      typedef short v2s __attribute__((ext_vector_type(2)));
+      const float s = bits_f(static_cast<uint32_t>(b) << 23);
+      v2s w = {0, 0};
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, q[0], q[1], s, false);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, q[2], q[3], s, true);
+      c[j] = __builtin_bit_cast(uint32_t, w);
     } else {
       constexpr float kRound = 12582912.0f;
+      const float inv = scale_inverse(b);
       const uint32_t i0 = f_bits(q[0] * inv + kRound), i1 = f_bits(q[1] * inv + kRound);
       const uint32_t i2 = f_bits(q[2] * inv + kRound), i3 = f_bits(q[3] * inv + kRound);
       c[j] = (i0 & 0xFFu) | ((i1 & 0xFFu) << 8) | ((i2 & 0xFFu) << 16) | (i3 << 24);
@@ -165,15 +168,14 @@ __device__ __forceinline__ void clamp8(float (&f)[8]) {
   }
 }
 
-// Largest magnitude bits of eight values, then over the four neighbouring lanes that hold a
-// group of 32 (two quad permutes).
+// Bits of the largest magnitude of eight values (a NaN among them wins), then over the four
+// neighbouring lanes that hold a group of 32 (two quad permutes).
 __device__ __forceinline__ uint32_t group_amax(const float (&f)[8]) {
-  uint32_t m = 0;
+  float top = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t a = f_bits(f[j]) & 0x7FFFFFFFu;
-    m = a > m ? a : m;
-  }
+  for (int j = 0; j < 8; j += 2)
+    top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(top, fabsf(f[j])), fabsf(f[j + 1]));
+  uint32_t m = f_bits(top) & 0x7FFFFFFFu;
   uint32_t o = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0xB1, 0xF, 0xF, true));
   m = o > m ? o : m;
   o = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x4E, 0xF, 0xF, true));
