@@ -203,6 +203,27 @@ def test_norm_of_many_rows(Z, cols):
             assert torch.equal(whole.codes[a:b], part.codes) and torch.equal(whole.scales[a:b], part.scales)
 
 
+@pytest.mark.parametrize("cols", [2600, 4096])
+def test_norm_of_many_wide_rows(Z, cols):
+    """Wide rows with a residual by the thousands, where more threads share a row: the rows' sums of
+    squares are the same to fp64, so every output is that of the same rows a few at a time."""
+    rows = 8200
+    x = torch.randn(rows, cols, device="cuda", generator=torch.Generator("cuda").manual_seed(7)).to(BF16)
+    r, w = x.flip(0).contiguous(), _matrix(1, cols, BF16, 8)[0]
+    y, h, h8 = torch.empty_like(x), torch.empty_like(x), Z.Act8.empty(rows, cols)
+    rstd = torch.empty(rows, device="cuda")
+    Z.rmsnorm(x, w, residual=r, h=h, y=y, h8=h8, rstd=rstd)
+    for a in (0, 4000, rows - 100):
+        b = a + 100
+        y1, h1, h81, rstd1 = torch.empty_like(x[a:b]), torch.empty_like(x[a:b]), Z.Act8.empty(100, cols), rstd[a:b].clone()
+        Z.rmsnorm(x[a:b], w, residual=r[a:b], h=h1, y=y1, h8=h81, rstd=rstd1)
+        assert torch.equal(h[a:b], h1) and torch.equal(h8.codes[a:b], h81.codes) and torch.equal(h8.scales[a:b], h81.scales)
+        # the order of the fp64 sum differs: rstd may land on the neighbouring fp32 number, and y on
+        # the neighbouring bf16 number where it lay between two
+        assert float(((rstd[a:b] - rstd1) / rstd1).abs().max()) <= 2 * U
+        assert float(((y[a:b].float() - y1.float()).abs() / y1.float().abs().clamp_min(1e-30)).max()) <= 2.0 ** -7
+
+
 def test_norm_single_outputs(Z):
     """Each output alone, and h in place of x or of the residual."""
     x, r = _matrix(6, 300, BF16, 31), _matrix(6, 300, BF16, 32)

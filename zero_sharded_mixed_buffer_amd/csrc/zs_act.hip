@@ -539,20 +539,28 @@ hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rows of up to 512 columns leave a lane one chunk of a row; with many of them it takes two rows,
-// for more loads in flight (131072 x 128: 17.8 us against 18.5 with one row and 19.4 with four).
+// Lanes and chunks to a row.  Rows of up to 512 columns leave a lane one chunk; with many of them
+// it takes two rows, for more loads in flight (131072 x 128: 17.8 us against 18.5 with one row and
+// 19.4 with four).  Up to 1024 columns a wave takes a row without a barrier (16384 x 1024: 16.6 us
+// against 24.0 with a workgroup to a row, half its lanes idle).  From there a workgroup takes a row:
+// of 256 threads with two chunks each, except that with a residual, whose outputs too are twice as
+// many, and rows enough, 512 threads with one chunk are faster (16384 x 4096, all outputs: 109.9 us
+// against 117.4; without a residual 64.9 against 57.1; 2048 rows 16.7 against 14.2).
 template <int DT>
 hipError_t norm_cols(const NormArgs& a, hipStream_t s) {
   const bool many = a.rows >= 32768;
   if (a.cols <= 128) return many ? norm_launch<DT, 16, 1, 2>(a, s) : norm_launch<DT, 16, 1>(a, s);
   if (a.cols <= 512) return many ? norm_launch<DT, 64, 1, 2>(a, s) : norm_launch<DT, 64, 1>(a, s);
+  if (a.cols <= 1024) return norm_launch<DT, 64, 2>(a, s);
   if (a.cols <= 2048) return norm_launch<DT, 256, 1>(a, s);
-  if (a.cols <= 4096) return norm_launch<DT, 256, 2>(a, s);
-  if (a.cols <= 8192) return norm_launch<DT, 256, 4>(a, s);
+  if (a.cols <= 4096)
+    return a.residual != nullptr && a.rows >= 8192 && a.cols > 2560 ? norm_launch<DT, 512, 1>(a, s)
+                                                                    : norm_launch<DT, 256, 2>(a, s);
+  if (a.cols <= 8192) return norm_launch<DT, 512, 2>(a, s);
   return norm_launch<DT, 1024, 2>(a, s);
 }
 
-int norm_rows_per_block(int64_t cols) { return cols <= 128 ? norm_block<16>() / 16 : cols <= 512 ? norm_block<64>() / 64 : 1; }
+int norm_rows_per_block(int64_t cols) { return cols <= 128 ? norm_block<16>() / 16 : cols <= 1024 ? norm_block<64>() / 64 : 1; }
 int backward_rows_per_block(int64_t cols) {
   return cols <= 128 ? backward_block<16>() / 16 : cols <= 1024 ? backward_block<64>() / 64 : 1;
 }
@@ -612,7 +620,8 @@ hipError_t launch_rmsnorm(const NormArgs& a, int dt, hipStream_t s) {
 }
 
 int64_t rmsnorm_max_rows(int64_t cols) {
-  return ((int64_t(1) << (cols <= 8192 ? 24 : 22)) - 1) * norm_rows_per_block(cols);
+  const int threads = cols <= 2048 ? 256 : cols <= 8192 ? 512 : 1024;
+  return ((int64_t(1) << 32) / threads - 1) * norm_rows_per_block(cols);
 }
 
 int64_t rmsnorm_partials(int64_t rows, int64_t cols) {
