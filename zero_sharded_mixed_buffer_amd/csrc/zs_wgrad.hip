@@ -294,8 +294,9 @@ __global__ __launch_bounds__(TL::kThreads, TL::FN* TL::FK >= 16 ? 1 : 2) void k_
     const int b = blockIdx.x - gr.direct;
     const int unit = b % kXcds * ((units + kXcds - 1) / kXcds) + b / kXcds;
     if (unit >= units) return;
-    tile = gr.direct + unit / gr.splits;
-    split = unit % gr.splits;
+    // all tiles of one split before the next: they share its tokens
+    tile = gr.direct + unit % (tiles - gr.direct);
+    split = unit / (tiles - gr.direct);
   }
   WgradTask w;
   w.t0 = split < 0 ? 0 : split * gr.per;
@@ -358,7 +359,9 @@ __global__ __launch_bounds__(TL::kThreads, TL::FN* TL::FK >= 16 ? 1 : 2) void k_
   // One barrier per stage.  While stage i is multiplied from one LDS buffer, stage i + 1 goes from
   // registers into the other, whose readers passed the barrier of stage i - 1, during the first
   // step; then stage i + 2 sets out from memory.  The operands of a step are read during the step
-  // before, the first ones of the next stage after the barrier, during the last step.
+  // before, the first ones of the next stage after the barrier, during the last step.  (Operands
+  // read two or three steps ahead, or two stages under way from memory, change neither tile's time
+  // by more than 2 %: neither LDS nor memory latency is what is left.)
   constexpr int kSteps = TL::T / 16;
   static_assert(kSteps % 2 == 0, "the operand sets alternate");
   const Fetcher<TL> fetch(g, w);
