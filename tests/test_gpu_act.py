@@ -565,6 +565,8 @@ def test_tensor_calls_refuse(Z):
            lambda: Z.act_wgrad(act, x, torch.zeros(64, 64, device="cuda", dtype=FP16)),
            lambda: Z.act_wgrad(act, x, torch.zeros(64, 64, device="cuda"), base=torch.zeros(64, 80, device="cuda")[:, :64]),
            lambda: Z.act_wgrad(act, x, torch.zeros(64, 64)),
+           lambda: Z.norm(x[:, :0], w[:0]), lambda: Z.linear(x[:, :0], torch.zeros(8, 0, dtype=BF16, device="cuda")),
+           lambda: Z.linear(x, torch.zeros(8, 64, dtype=BF16, device="cuda"), code="fp8"),
            lambda: Z.norm(x, w, save="fp8"), lambda: Z.norm(x, w, residual=x[:3]),
            lambda: Z.norm(x, w, grad_into=r), lambda: Z.linear(x, torch.zeros(8, 63, dtype=BF16, device="cuda")),
            lambda: Z.linear(x, torch.zeros(8, 64, dtype=BF16, device="cuda"), x8=Z.Act8.empty(3, 64))]

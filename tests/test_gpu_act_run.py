@@ -120,6 +120,26 @@ def test_grad_into_accumulates(Z):
         _close(bn, plain[1], 3 * 2.0 ** -8, "norm")
 
 
+def test_layers_share_a_checkpoint(Z):
+    """Two layers read one norm's output and its one checkpoint; a frozen layer keeps nothing; the
+    gradients of a sum's two terms are tensors of their own."""
+    x, r = _randn((40, 96), BF16, 36).requires_grad_(), _randn((40, 96), BF16, 37).requires_grad_()
+    nw = torch.ones(96, dtype=BF16, device="cuda")
+    ws = [_randn((24, 96), BF16, 38, 0.1).requires_grad_(), _randn((56, 96), BF16, 39, 0.1).requires_grad_()]
+    frozen = _randn((8, 96), BF16, 40, 0.1)
+    out = Z.norm(x, nw, residual=r, y8="int8")
+    ys = [Z.linear(out.y, w, x8=out.y8) for w in ws] + [Z.linear(out.y, frozen)]
+    dys = [_randn(y.shape, BF16, 44 + i) for i, y in enumerate(ys)]
+    torch.autograd.backward(ys, dys)
+    for w, dy in zip(ws, dys):
+        alone = torch.empty_like(w)
+        Z.act_wgrad(out.y8, dy, alone)
+        assert torch.equal(w.grad, alone)
+    assert torch.equal(x.grad, r.grad) and x.grad.data_ptr() != r.grad.data_ptr()
+    with torch.no_grad():
+        assert torch.equal(Z.linear(out.y, ws[0]), ys[0])
+
+
 def test_changed_checkpoint_is_noticed(Z):
     x = _randn((8, 64), BF16, 41)
     w = _randn((16, 64), BF16, 42).requires_grad_()

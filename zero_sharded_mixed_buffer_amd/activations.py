@@ -335,14 +335,14 @@ def norm(x, weight, eps=1e-6, residual=None, save="e4m3", y8=None, grad_into=Non
     alive: autograd would join their streams in the capture."""
     if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
         raise ValueError("residual must have x's shape and dtype")
-    if x.dim() < 1 or x.dtype not in HALF:
-        raise ValueError("x must be a bf16 or fp16 tensor")
+    if x.dim() < 1 or x.shape[-1] < 1 or x.dtype not in HALF:
+        raise ValueError("x must be a bf16 or fp16 tensor with at least one column")
     _need_gpu(x.device)
     _check_grad_into(grad_into, weight)
     if save is not None and save not in CODES:
         raise ValueError(f"save is 'e4m3', 'int8' or None, not {save!r}")
     cols = x.shape[-1]
-    act = Act8.empty(x.numel() // max(cols, 1), cols, y8, x.device) if y8 is not None else None
+    act = Act8.empty(x.numel() // cols, cols, y8, x.device) if y8 is not None else None
     out = _Norm.apply(x, residual, weight, eps, save, act, grad_into)
     y, h = out if residual is not None else (out, x)
     return NormOutput(y, h, act)
@@ -375,10 +375,13 @@ def linear(x, weight, x8=None, code="e4m3", grad_into=None):
     checkpoint of x for the weight's gradient instead of x.
 
     x8: the checkpoint of x if there is one already (norm's y8: several layers that read one
-    tensor share it); otherwise it is taken here, with `code`.  grad_into: as for norm."""
+    tensor share it); otherwise it is taken here, with `code`.  grad_into: as for norm.  The two
+    products with the weight are the library's; the weight's gradient is act_wgrad's."""
+    if code not in CODES:
+        raise ValueError(f"code is 'e4m3' or 'int8', not {code!r}")
     if x.dim() < 1 or x.dtype not in HALF or weight.dtype != x.dtype or weight.dim() != 2:
         raise ValueError("x and a weight of two dimensions must have one dtype, bf16 or fp16")
-    if x.shape[-1] != weight.shape[1]:
+    if x.shape[-1] != weight.shape[1] or x.shape[-1] < 1:
         raise ValueError(f"x has {x.shape[-1]} columns, the weight {weight.shape[1]}")
     if not weight.is_contiguous():
         raise ValueError("the weight must be contiguous")
@@ -386,8 +389,10 @@ def linear(x, weight, x8=None, code="e4m3", grad_into=None):
     if weight.device != x.device:
         raise ValueError(f"the weight lives on {weight.device}, not on {x.device}")
     _check_grad_into(grad_into, weight)
+    if x8 is not None:
+        _checkpoint(x8, "x8", x.numel() // x.shape[-1], x.shape[-1], x.device)
+    if not (weight.requires_grad and torch.is_grad_enabled()):  # nothing of x is kept
+        return torch.nn.functional.linear(x, weight)
     if x8 is None:
         x8 = Act8.of(_rows(x.detach()), code)
-    else:
-        _checkpoint(x8, "x8", x.numel() // x.shape[-1], x.shape[-1], x.device)
     return _Linear.apply(x, weight, x8, grad_into)

@@ -281,7 +281,7 @@ __device__ __forceinline__ void write8(const WgradArgs& g, int64_t row, int64_t 
 }
 
 template <int DT, int CODE, class TL>
-__global__ __launch_bounds__(TL::kThreads, TL::FN* TL::FK >= 16 ? 1 : 2) void k_wgrad(WgradArgs g, WgradGrid gr) {
+__global__ __launch_bounds__(TL::kThreads, 2) void k_wgrad(WgradArgs g, WgradGrid gr) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   // one contiguous run of units per XCD, of the direct tiles and of the split ones, so that
   // neighbouring tiles share their operands in its L2
@@ -506,8 +506,8 @@ __global__ __launch_bounds__(kThreads) void k_wgrad_fold(WgradArgs g, WgradGrid 
 // half as many operand bytes from L2 and LDS for each product: 8192 x 4096 -> 4096 in 219 us (1.25
 // PFLOP/s) against 303.  The small one, two workgroups of four waves to a CU, serves outputs with
 // few large tiles: 16384 x 1024 -> 1024 in 52 us against 54, 1024 x 1024 -> 4096 in 16 against 28
-// (four splits).  Wave shapes of 4 x 4 instructions (half the waves, less LDS traffic still) took 298
-// us at 8192 x 4096 -> 4096 and stages of 32 tokens 231, where 64 took 228.
+// (four splits).  Four waves of 4 x 4 instructions, with less LDS traffic still, were slower than
+// eight of 4 x 2 (298 us against 270, both before the interleaving below was in place).
 using SmallTile = Tile<2, 2, 2, 2, 64, false>;  // 128 x 128
 using LargeTile = Tile<2, 4, 4, 2, 64, true>;   // 256 x 256
 
