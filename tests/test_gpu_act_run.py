@@ -286,6 +286,34 @@ def test_two_streams_at_once(Z):
                 assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
 
 
+def test_several_host_threads(Z):
+    """Four host threads, each with its stream and buffers, run their chains at once."""
+    import threading
+    states = [_state(Z, 700 + 10 * i, rows=300 + 50 * i) for i in range(4)]
+    want = [_chain(Z, s) for s in states]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(10):
+                    got = _chain(Z, states[i])
+                    stream.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                        bad.append(i)
+        except Exception as e:  # reported below, in the test's own thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not bad, bad
+
+
 def test_captured_and_replayed(Z):
     """Two graphs of chains, replayed several times in turn on changing inputs, with eager calls
     and synchronizations between; every replay against the eager result."""

@@ -635,10 +635,10 @@ int64_t rmsnorm_partials(int64_t rows, int64_t cols) {
   const int64_t steps = (rows + per - 1) / per;
   // Up to eight rounds one workgroup does alone, with no partial sums and no second launch.
   // Otherwise as many workgroups as bring sixteen waves to every CU: more only add partial sums
-  // (16384 x 4096: 82 us with 512, 85 with 1024; 16384 x 2048, where a workgroup has four waves:
-  // 54 with 512, 47 with 1024).
+  // (16384 x 4096, eight waves: 82 us with 512, 85 with 1024; 16384 x 2048, four waves: 54 with 512,
+  // 47 with 1024; 2048 x 16384, sixteen waves: 52 with 256, 59 with 512).
   if (steps <= 8) return 1;
-  const int64_t most = cols > 1024 && cols <= 2048 ? 1024 : 512;
+  const int64_t most = cols > 8192 ? 256 : cols > 1024 && cols <= 2048 ? 1024 : 512;
   return steps < most ? steps : most;
 }
 
