@@ -174,7 +174,7 @@ __device__ __forceinline__ T row_sum(T x, T* slot) {
     x += __shfl_xor(x, 32, 64);
   }
   if constexpr (LPR > 64) {
-    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = x;
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x % LPR >> 6] = x;
     __syncthreads();
     x = slot[0];
 #pragma unroll
@@ -187,11 +187,12 @@ template <int LPR>
 constexpr int norm_block() {
   return LPR > kThreads ? LPR : kThreads;
 }
-// The backward pass of short rows takes more of them at once: fewer rounds where there is one
-// workgroup, fewer partial sums where there are many.
+// The backward pass takes shorter rows several at once: fewer rounds where there is one workgroup,
+// fewer partial sums where there are many (16384 x 2048: 45.7 us with two rows to a workgroup, 49.2
+// with one and twice the workgroups).
 template <int LPR>
 constexpr int backward_block() {
-  return LPR > 256 ? LPR : LPR < 256 ? 512 : 256;
+  return LPR > 512 ? LPR : 512;
 }
 
 // LPR lanes share a row, V chunks each (LPR * V * 8 >= cols), and take R rows.  The sum of squares
@@ -314,7 +315,7 @@ template <int DT, int SAVED, int LPR, int V>
 __global__ __launch_bounds__(backward_block<LPR>(), 4) void k_rmsnorm_backward(NormBackwardArgs a) {
   constexpr int kBlock = backward_block<LPR>();
   constexpr int kRows = kBlock / LPR;
-    __shared__ float slot[2][LPR > 64 ? LPR / 64 : 1];
+    __shared__ float slot[2][kRows][LPR > 64 ? LPR / 64 : 1];
   __shared__ float fold[kRows > 1 ? kRows : 1][kRows > 1 ? LPR * V * 8 : 1];
   const int sub = threadIdx.x / LPR;
   const int lane = threadIdx.x % LPR;
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(backward_block<LPR>(), 4) void k_rmsnorm_backward(N
         acc[v][j] += t;
       }
     }
-    dot = row_sum<LPR>(dot, slot[turn]);
+    dot = row_sum<LPR>(dot, slot[turn][sub]);
     const float mean = dot / static_cast<float>(a.cols);
     if (row >= a.rows) continue;
     // The row waits for its mean in packed form: without this the compiler keeps the widened
@@ -568,7 +569,7 @@ hipError_t norm_cols(const NormArgs& a, hipStream_t s) {
 
 int norm_rows_per_block(int64_t cols) { return cols <= 128 ? norm_block<16>() / 16 : cols <= 1024 ? norm_block<64>() / 64 : 1; }
 int backward_rows_per_block(int64_t cols) {
-  return cols <= 128 ? backward_block<16>() / 16 : cols <= 1024 ? backward_block<64>() / 64 : 1;
+  return cols <= 128 ? backward_block<16>() / 16 : cols <= 1024 ? backward_block<64>() / 64 : cols <= 2048 ? 2 : 1;
 }
 
 template <int DT, int SAVED, int LPR, int V>
@@ -635,10 +636,10 @@ int64_t rmsnorm_partials(int64_t rows, int64_t cols) {
   const int64_t steps = (rows + per - 1) / per;
   // Up to eight rounds one workgroup does alone, with no partial sums and no second launch.
   // Otherwise as many workgroups as bring sixteen waves to every CU: more only add partial sums
-  // (16384 x 4096, eight waves: 82 us with 512, 85 with 1024; 16384 x 2048, four waves: 54 with 512,
-  // 47 with 1024; 2048 x 16384, sixteen waves: 52 with 256, 59 with 512).
+  // (16384 x 4096, eight waves to one: 82 us with 512, 85 with 1024; 2048 x 16384, sixteen: 52 with
+  // 256, 59 with 512).
   if (steps <= 8) return 1;
-  const int64_t most = cols > 8192 ? 256 : cols > 1024 && cols <= 2048 ? 1024 : 512;
+  const int64_t most = cols > 8192 ? 256 : 512;
   return steps < most ? steps : most;
 }
 
