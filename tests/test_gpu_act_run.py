@@ -120,6 +120,30 @@ def test_grad_into_accumulates(Z):
         _close(bn, plain[1], 3 * 2.0 ** -8, "norm")
 
 
+def test_broadcast_inputs_and_gradients(Z):
+    """Inputs that are one row seen many times, and gradients that arrive that way (from a sum over
+    rows), with a residual of the same kind: as their copies give."""
+    row, row2 = _randn((1, 96), BF16, 301), _randn((96,), BF16, 302)
+    nw, w = _randn((96,), BF16, 303), _randn((24, 96), BF16, 304, 0.1)
+    g, gy = _randn((96,), BF16, 305), _randn((24,), BF16, 306)
+
+    def run(copy):
+        x, r = row.clone().requires_grad_(), row2.clone().requires_grad_()
+        a, b = nw.clone().requires_grad_(), w.clone().requires_grad_()
+        wide, wide2 = x.expand(50, 96), r.expand(50, 96)
+        if copy:
+            wide, wide2 = wide.contiguous(), wide2.contiguous()
+        out = Z.norm(wide, a, residual=wide2, y8="int8")
+        out.y.sum(0).backward(g, retain_graph=True)
+        out.h.sum(0).backward(g, retain_graph=True)
+        Z.linear(out.y, b, x8=out.y8).sum(0).backward(gy)
+        Z.linear(wide, b).sum(0).backward(gy)
+        return [t.grad for t in (x, r, a, b)]
+
+    for p, q in zip(run(False), run(True)):
+        assert torch.equal(p, q)
+
+
 def test_layers_share_a_checkpoint(Z):
     """Two layers read one norm's output and its one checkpoint; a frozen layer keeps nothing; the
     gradients of a sum's two terms are tensors of their own."""

@@ -266,9 +266,12 @@ NormOutput = namedtuple("NormOutput", ["y", "h", "y8"])
 
 
 def _rows(t):
-    """A tensor's last dimension as matrix columns, copied only if that takes it."""
+    """A tensor's last dimension as matrix columns, copied only if that takes it: rows that overlap,
+    such as a broadcast tensor's, are no matrix that the kernels take."""
     m = t.reshape(-1, t.shape[-1])
-    return m if m.shape[1] == 1 or m.stride(1) == 1 else m.contiguous()
+    rows, cols = m.shape
+    row, col = m.stride()
+    return m if (cols == 1 or col == 1) and (rows <= 1 or row >= cols) else m.contiguous()
 
 
 def _check_grad_into(grad_into, weight):
