@@ -162,6 +162,8 @@ def test_layers_share_a_checkpoint(Z):
     assert torch.equal(x.grad, r.grad) and x.grad.data_ptr() != r.grad.data_ptr()
     with torch.no_grad():
         assert torch.equal(Z.linear(out.y, ws[0]), ys[0])
+        same = Z.norm(x, nw, residual=r, y8="int8")
+        assert torch.equal(same.y, out.y) and torch.equal(same.h, out.h) and torch.equal(same.y8.codes, out.y8.codes)
 
 
 def test_changed_checkpoint_is_noticed(Z):

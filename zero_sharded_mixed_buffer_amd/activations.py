@@ -346,6 +346,8 @@ def norm(x, weight, eps=1e-6, residual=None, save="e4m3", y8=None, grad_into=Non
         raise ValueError(f"save is 'e4m3', 'int8' or None, not {save!r}")
     cols = x.shape[-1]
     act = Act8.empty(x.numel() // cols, cols, y8, x.device) if y8 is not None else None
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, residual, weight))):
+        save = None  # no backward will read it
     out = _Norm.apply(x, residual, weight, eps, save, act, grad_into)
     y, h = out if residual is not None else (out, x)
     return NormOutput(y, h, act)
