@@ -144,6 +144,26 @@ def test_broadcast_inputs_and_gradients(Z):
         assert torch.equal(p, q)
 
 
+@pytest.mark.parametrize("shape", [(12, 64), (3, 4, 64)])
+def test_outputs_may_be_changed_in_place(Z, shape):
+    """y and h are tensors of their own: changing them in place is an operation like any other,
+    and the saved checkpoint does not notice."""
+    x, r = _randn(shape, BF16, 311).requires_grad_(), _randn(shape, BF16, 312).requires_grad_()
+    w = _randn((64,), BF16, 313).requires_grad_()
+    g = _randn(shape, BF16, 314)
+    grads = []
+    for in_place in (False, True):
+        out = Z.norm(x, w, residual=r)
+        if in_place:
+            y, h = out.y.mul_(2), out.h.mul_(4)
+        else:
+            y, h = out.y * 2, out.h * 4
+        torch.autograd.backward([y, h], [g, g])
+        grads.append([t.grad.clone() for t in (x, r, w)])
+        x.grad = r.grad = w.grad = None
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+
+
 def test_layers_share_a_checkpoint(Z):
     """Two layers read one norm's output and its one checkpoint; a frozen layer keeps nothing; the
     gradients of a sum's two terms are tensors of their own."""

@@ -291,20 +291,19 @@ class _Norm(torch.autograd.Function):
         ctx.set_materialize_grads(False)
         x2 = _rows(x)
         rows, cols = x2.shape
-        y = torch.empty(rows, cols, dtype=x.dtype, device=x.device)
+        # in x's shape from the start: a view made here could not be changed in place afterwards
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         h = torch.empty_like(y) if residual is not None else None
         rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
         h8 = Act8.empty(rows, cols, save, x.device) if save is not None else None
-        rmsnorm(x2, weight, eps, residual=_rows(residual) if residual is not None else None, h=h, y=y, y8=y8, h8=h8,
-                rstd=rstd)
+        rmsnorm(x2, weight, eps, residual=_rows(residual) if residual is not None else None,
+                h=h.view(rows, cols) if h is not None else None, y=y.view(rows, cols), y8=y8, h8=h8, rstd=rstd)
         ctx.save, ctx.cols, ctx.grad_into, ctx.two = save, cols, grad_into, residual is not None
-        out = y.view(x.shape)
-        sum_ = h.view(x.shape) if h is not None else None
         if h8 is not None:
             ctx.save_for_backward(weight, rstd, h8.codes, h8.scales)
         else:
-            ctx.save_for_backward(weight, rstd, sum_ if sum_ is not None else x)
-        return (out, sum_) if ctx.two else out
+            ctx.save_for_backward(weight, rstd, h if h is not None else x)
+        return (y, h) if ctx.two else y
 
     @staticmethod
     @once_differentiable
