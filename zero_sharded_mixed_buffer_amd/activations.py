@@ -379,8 +379,8 @@ def linear(x, weight, x8=None, code="e4m3", grad_into=None):
     checkpoint of x for the weight's gradient instead of x.
 
     x8: the checkpoint of x if there is one already (norm's y8: several layers that read one
-    tensor share it); otherwise it is taken here, with `code`.  grad_into: as for norm.  The two
-    products with the weight are the library's; the weight's gradient is act_wgrad's."""
+    tensor share it); otherwise it is taken here, with `code`.  grad_into, and
+    capture into graphs: as for norm.  The two products with the weight are the library's; the weight's gradient is act_wgrad's."""
     if code not in CODES:
         raise ValueError(f"code is 'e4m3' or 'int8', not {code!r}")
     if x.dim() < 1 or x.dtype not in HALF or weight.dtype != x.dtype or weight.dim() != 2:
