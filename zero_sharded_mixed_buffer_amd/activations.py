@@ -12,6 +12,7 @@ gradients that backward then writes into the optimizer's gradient buffer:
 
 The functions work on the current stream of their tensors' device, write into the tensors they
 are given, allocate nothing but a workspace that was not passed in, and never wait for the GPU.
+What a call writes, a checkpoint's arrays among it, counts as changed in place for autograd.
 A wrong type, shape, stride or device is a ValueError before anything is enqueued.
 """
 
@@ -110,6 +111,17 @@ def _enqueue(name, device, *args):
         A._check(status, name)
 
 
+def _wrote(*tensors):
+    """Mark what a call has written as changed, as torch's own writes are: autograd then refuses a
+    backward pass that would read a saved tensor's later contents.  (Tensors made in inference
+    mode carry no version.)"""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None and not t.is_inference()])
+
+
+def _wrote_act(act):
+    return (act.codes, act.scales) if act is not None else ()
+
+
 def _at(t):
     return t.data_ptr() if t is not None else None
 
@@ -184,6 +196,7 @@ def act_pack(x, act):
     rows, cols, dev, stride = _input(x, "x", _DTYPES)
     arrays = _checkpoint(act, "act", rows, cols, dev)
     _enqueue("zs_act_pack", dev, x.data_ptr(), _DTYPES[x.dtype], stride, rows, cols, arrays)
+    _wrote(act.codes, act.scales)
 
 
 def act_unpack(act, out):
@@ -191,6 +204,7 @@ def act_unpack(act, out):
     rows, cols, dev, stride = _input(out, "out", _DTYPES)
     arrays = _checkpoint(act, "act", rows, cols, dev)
     _enqueue("zs_act_unpack", dev, arrays, rows, cols, out.data_ptr(), _DTYPES[out.dtype], stride)
+    _wrote(out)
 
 
 def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, y8=None, h8=None, rstd=None):
@@ -211,6 +225,7 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, y8=None, h8=None
     ha = _checkpoint(h8, "h8", rows, cols, dev) if h8 is not None else None
     _enqueue("zs_rmsnorm", dev, x.data_ptr(), xs, _at(residual), rs, weight.data_ptr(), _DTYPES[dt], rows, cols, eps,
              _at(h), hs, _at(y), ys, ya, ha, _at(rstd))
+    _wrote(h, y, rstd, *_wrote_act(y8), *_wrote_act(h8))
 
 
 def rmsnorm_backward(dy, saved, weight, rstd, dx, dh=None, dweight=None, base=None, workspace=None):
@@ -240,6 +255,7 @@ def rmsnorm_backward(dy, saved, weight, rstd, dx, dh=None, dweight=None, base=No
     _enqueue("zs_rmsnorm_backward", dev, dy.data_ptr(), dys, _at(dh), dhs, _at(h), hs, h8, weight.data_ptr(),
              rstd.data_ptr(), _DTYPES[dt], rows, cols, dx.data_ptr(), dxs, _at(dweight),
              _DTYPES[dweight.dtype] if dweight is not None else A.ZS_FP32, _at(base), _at(workspace), size)
+    _wrote(dx, dweight, workspace if dweight is not None else None)
 
 
 def act_wgrad(x8, dy, dw, base=None, in_major=False, workspace=None):
@@ -258,6 +274,7 @@ def act_wgrad(x8, dy, dw, base=None, in_major=False, workspace=None):
     workspace, size = _workspace(workspace, A.zs_act_wgrad_workspace(rows, x8.cols, outs), dev)
     _enqueue("zs_act_wgrad", dev, arrays, rows, x8.cols, dy.data_ptr(), _DTYPES[dy.dtype], dys, outs, dw.data_ptr(),
              _DTYPES[dw.dtype], dws, int(bool(in_major)), _at(base), _at(workspace), size)
+    _wrote(dw, workspace)
 
 
 # ------------------------------------------------------------------------------ autograd
