@@ -1,6 +1,8 @@
 """CPU tests of what the activation operators tell autograd and of how they order streams: the
 tensor-level calls run on host tensors with the launch itself replaced, so that no kernel runs."""
 
+import contextlib
+
 import pytest
 import torch
 
@@ -10,6 +12,7 @@ BF16 = torch.bfloat16
 @pytest.fixture
 def Z(monkeypatch):
     import zero_sharded_mixed_buffer_amd as Z
+    monkeypatch.setattr(Z.activations, "_adding", {}, raising=False)
     monkeypatch.setattr(Z.activations, "_need_gpu", lambda device: None)
     monkeypatch.setattr(Z.activations, "_enqueue", lambda name, device, *args: None)
     Z.lib()
@@ -102,3 +105,132 @@ def test_inference_tensors_are_written(Z):
         Z.rmsnorm(x, w, y=y, y8=act)
     Z.rmsnorm(x, w, y=y, y8=act)
     Z.act_unpack(act, y)
+
+
+# ------------------------------------------------------------------------------ streams
+
+class _Stream:
+    """A stream that only logs what waits for what."""
+
+    def __init__(self, name, log):
+        self.name, self.log = name, log
+
+    def __eq__(self, other):
+        return isinstance(other, _Stream) and self.name == other.name
+
+    def __ne__(self, other):
+        return not self == other
+
+    def wait_stream(self, other):
+        self.log.append((self.name, "waits for", other.name))
+
+
+class _Streams:
+    """torch.cuda's current stream, by name, as the test sets it, and a log of launches and waits."""
+
+    def __init__(self, monkeypatch, Z):
+        self.log, self.name, self.capturing = [], "main", ()
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: _Stream(self.name, self.log))
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.name in self.capturing)
+        monkeypatch.setattr(torch.cuda, "stream", self.entered)
+        monkeypatch.setattr(Z.activations, "_enqueue", lambda name, device, *args: self.log.append((self.name, name)))
+
+    @contextlib.contextmanager
+    def entered(self, stream):
+        outer, self.name = self.name, stream.name
+        yield
+        self.name = outer
+
+
+def _node(streams, name, t):
+    """t, whose gradient is computed with `name` as the current stream."""
+    t.register_hook(lambda g: setattr(streams, "name", name))
+    return t
+
+
+def _ends_on(streams, name):
+    """At the end of the pass the engine makes the caller's stream current again."""
+    torch.autograd.Variable._execution_engine.queue_callback(lambda: setattr(streams, "name", name))
+
+
+@pytest.mark.parametrize("what", ["linear", "norm"])
+def test_additions_of_two_streams_are_ordered(Z, monkeypatch, what):
+    """One buffer that two layers add to, their forwards on two streams: the second addition waits
+    for the first, and the stream that called backward for both."""
+    streams = _Streams(monkeypatch, Z)
+    w = _randn(64, 64).requires_grad_() if what == "linear" else _randn(64).requires_grad_()
+    into = torch.zeros_like(w, requires_grad=False)
+    x = _randn(4, 64)
+    outs = []
+    for name in ("s1", "s2"):
+        streams.name = name
+        if what == "linear":
+            outs.append(Z.linear(x, w, x8=_act(Z, 4, 64), grad_into=into))
+        else:
+            outs.append(Z.norm(x, w, grad_into=into).y)
+    for _ in range(2):
+        streams.name, streams.log[:] = "main", []
+        total = outs[0].sum()
+        _node(streams, "s1", outs[0])
+        total = total + outs[1].sum()
+        _node(streams, "s2", outs[1])
+        total.register_hook(lambda g: _ends_on(streams, "main"))
+        total.backward(retain_graph=True)
+        call = "zs_act_wgrad" if what == "linear" else "zs_rmsnorm_backward"
+        first, second = [a for a, b, *_ in streams.log if b == call]
+        assert {first, second} == {"s1", "s2"}
+        assert streams.log == [(first, call), (second, "waits for", first), (second, call),
+                               ("main", "waits for", second)]
+
+
+def test_one_stream_waits_for_nothing(Z, monkeypatch):
+    streams = _Streams(monkeypatch, Z)
+    w = _randn(64, 64).requires_grad_()
+    into = torch.zeros(64, 64)
+    x = _randn(4, 64)
+    total = sum(Z.linear(x, w, x8=_act(Z, 4, 64), grad_into=into).sum() for _ in range(3))
+    total.backward()
+    assert [e for e in streams.log if e[1] != "zs_act_wgrad"] == []
+
+
+def test_a_failed_pass_leaves_no_harm(Z, monkeypatch):
+    """A pass that ends in an error leaves its stream behind as one to wait for, and no more."""
+    streams = _Streams(monkeypatch, Z)
+    w = _randn(64, 64).requires_grad_()
+    into = torch.zeros(64, 64)
+    x = _randn(4, 64).requires_grad_()
+
+    def fail(grad):
+        raise KeyError("from the test")
+
+    y = x * 1
+    y.register_hook(fail)
+    streams.name = "s1"
+    with pytest.raises(KeyError):
+        Z.linear(y, w, x8=_act(Z, 4, 64), grad_into=into).sum().backward()
+    for name in ("s2", "s2"):
+        streams.name, streams.log[:] = name, []
+        Z.linear(x, w, x8=_act(Z, 4, 64), grad_into=into).sum().backward()
+        assert (name, "zs_act_wgrad") in streams.log
+        assert all(e in (("s2", "waits for", "s1"), ("s2", "zs_act_wgrad")) for e in streams.log)
+
+
+def test_captured_and_eager_streams_do_not_wait_for_each_other(Z, monkeypatch):
+    """A wait between a stream that is being captured and one that is not would end the capture:
+    there is none, nor for a stream whose capture has ended since."""
+    streams = _Streams(monkeypatch, Z)
+    A = Z.activations
+    for name, streams.capturing in (("c1", ("c1",)), ("s1", ("c1", "c2")), ("c2", ("c1", "c2")), ("c1", ("c1", "c2")),
+                                    ("c2", ("c2",))):
+        def add(name=name):
+            streams.name = name
+            A._add_in_turn(torch.device("cpu"), lambda: streams.log.append((name, "adds")))
+        x = torch.zeros(1, requires_grad=True)
+        y = x * 1
+        y.register_hook(lambda g: add())
+        # the pass fails after its addition, so that its stream stays the last one
+        x.register_hook(lambda g: 1 / 0)
+        with pytest.raises(ZeroDivisionError):
+            y.backward()
+    assert streams.log == [("c1", "adds"), ("s1", "adds"), ("c2", "adds"), ("c1", "waits for", "c2"), ("c1", "adds"),
+                           ("c2", "adds")]

@@ -74,3 +74,100 @@ def test_inference_mode(Z):
     assert torch.equal(y, y2) and torch.equal(act.codes, act2.codes) and torch.equal(out.y, y)
     Z.rmsnorm(x, w, y=y2, y8=act2)
     assert torch.equal(act.unpack(), act2.unpack())
+
+
+# ------------------------------------------------------------------------------ streams
+
+def _busy(n=6):
+    """A few milliseconds of products on the current stream."""
+    a = torch.ones(8192, 8192, dtype=BF16, device="cuda")
+    for _ in range(n):
+        a = torch.mm(a, a)
+    return a
+
+
+@pytest.mark.parametrize("what", ["linear", "norm"])
+@pytest.mark.parametrize("late", [0, 1])
+def test_additions_of_two_streams(Z, what, late):
+    """One weight, two micro-batches on two streams, one of which is busy when backward begins:
+    both gradients are in the buffer when the calling stream reads it, at once, after backward."""
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    gen = torch.Generator("cuda").manual_seed(11)
+    xs = [torch.randint(-3, 4, (64, 96), device="cuda", generator=gen).to(BF16) for _ in range(2)]
+    dys = [torch.randint(-2, 3, (64, 96), device="cuda", generator=gen).to(BF16) for _ in range(2)]
+    w = torch.ones((96, 96) if what == "linear" else (96,), dtype=BF16, device="cuda", requires_grad=True)
+    into = torch.zeros(w.shape, device="cuda")
+
+    def forward(x, buffer):
+        if what == "linear":
+            return Z.linear(x, w, code="int8", grad_into=buffer)
+        return Z.norm(x, w, eps=1e-5, save="int8", grad_into=buffer).y
+
+    parts = []
+    for x, dy in zip(xs, dys):
+        alone = torch.zeros_like(into)
+        forward(x, alone).backward(dy)
+        parts.append(alone)
+    # the buffer is added to the second part's fp32 sum in one rounding, as here, in either order
+    want = parts[0] + parts[1]
+    torch.cuda.synchronize()
+    for turn in range(4):
+        into.zero_()
+        ys = []
+        for s, x in zip(streams, xs):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                ys.append(forward(x, into))
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        with torch.cuda.stream(streams[late]):
+            _busy()
+        if turn % 2:
+            torch.autograd.backward(ys, dys)
+        else:
+            for y, dy in zip(ys, dys):
+                y.backward(dy)
+        got = into.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), turn
+        assert w.grad is None
+    assert Z.activations._adding[w.device] == [None, 0]
+
+
+def test_captured_additions_of_two_streams(Z):
+    """The same captured into one graph, replayed with changing gradients."""
+    side = torch.cuda.Stream()
+    gen = torch.Generator("cuda").manual_seed(12)
+    xs = [torch.randint(-3, 4, (64, 96), device="cuda", generator=gen).to(BF16) for _ in range(2)]
+    dys = [torch.zeros(64, 40, dtype=BF16, device="cuda") for _ in range(2)]
+    w = torch.ones(40, 96, dtype=BF16, device="cuda", requires_grad=True)
+    into = torch.zeros(40, 96, device="cuda")
+
+    def run():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        ys = [Z.linear(xs[0], w, code="int8", grad_into=into)]
+        with torch.cuda.stream(side):
+            ys.append(Z.linear(xs[1], w, code="int8", grad_into=into))
+        main.wait_stream(side)
+        torch.autograd.backward(ys, dys)
+
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        run()
+    torch.cuda.current_stream().wait_stream(warm)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for turn in range(4):
+        for dy in dys:
+            dy.copy_(torch.randint(-2, 3, dy.shape, device="cuda", generator=gen).to(BF16))
+        into.zero_()
+        graph.replay()
+        if turn % 2:
+            _busy(1)
+        torch.cuda.synchronize()
+        want = sum(dy.double().t().contiguous() @ x.double() for x, dy in zip(xs, dys))
+        assert torch.equal(into.double(), want), turn

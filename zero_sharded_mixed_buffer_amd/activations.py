@@ -19,6 +19,7 @@ A wrong type, shape, stride or device is a ValueError before anything is enqueue
 from __future__ import annotations
 
 import ctypes
+import threading
 from collections import namedtuple
 
 import torch
@@ -302,6 +303,49 @@ def _check_grad_into(grad_into, weight):
         raise ValueError("grad_into is a plain buffer, without requires_grad")
 
 
+# Additions to a caller's buffer (grad_into) in a backward pass.  Autograd runs each backward on the
+# stream of its forward and orders only the gradients that it is handed; these it never sees.  So
+# each addition waits for the one before it on the device if that ran on another stream, and at the
+# end of a pass the stream that called it waits for the last.  By device: the stream of the
+# last addition, and how many additions belong to passes that have not ended.  (A pass that fails
+# never reports its end: its stream then stays one to wait for, which is harmless.)
+_adding = {}
+_adding_lock = threading.RLock()
+
+
+def _captured(stream):
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _wait_for(stream, last):
+    """Let `stream` wait for what `last` holds so far, unless just one of them is being captured
+    into a graph, which the wait would end."""
+    if last is not None and last != stream and _captured(stream) == _captured(last):
+        stream.wait_stream(last)
+
+
+def _add_in_turn(device, add):
+    """Call `add`, which enqueues work that adds to a caller's buffer, within a backward pass."""
+    stream = torch.cuda.current_stream(device)
+    with _adding_lock:
+        state = _adding.setdefault(device, [None, 0])
+        _wait_for(stream, state[0])
+        add()
+        state[0] = stream
+        state[1] += 1
+    torch.autograd.Variable._execution_engine.queue_callback(lambda: _pass_ended(device))
+
+
+def _pass_ended(device):
+    caller = torch.cuda.current_stream(device)
+    with _adding_lock:
+        state = _adding[device]
+        _wait_for(caller, state[0])
+        state[1] -= 1
+        state[0] = caller if state[1] else None
+
+
 class _Norm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, eps, save, y8, grad_into):
@@ -334,8 +378,12 @@ class _Norm(torch.autograd.Function):
         into, dweight = ctx.grad_into, None
         if ctx.needs_input_grad[2]:
             dweight = torch.empty_like(weight) if into is None else into
-        rmsnorm_backward(dy2, saved, weight, rstd, dx, dh=_rows(dh) if dh is not None else None, dweight=dweight,
-                         base=into if dweight is not None else None)
+        dh2 = _rows(dh) if dh is not None else None
+        if dweight is None or into is None:
+            rmsnorm_backward(dy2, saved, weight, rstd, dx, dh=dh2, dweight=dweight)
+        else:
+            _add_in_turn(dy.device, lambda: rmsnorm_backward(dy2, saved, weight, rstd, dx, dh=dh2, dweight=into,
+                                                             base=into))
         dx = dx.view(dy.shape)
         return (dx, dx if ctx.two else None, dweight if into is None else None, None, None, None, None)
 
@@ -348,7 +396,10 @@ def norm(x, weight, eps=1e-6, residual=None, save="e4m3", y8=None, grad_into=Non
     "int8" writes the checkpoint of y in the same pass, for the linear layers that read y.
     grad_into: a buffer of the weight's shape (its dtype or fp32; with flat_views the weight's
     .grad) that backward adds the weight's gradient to; the weight then receives none from
-    autograd.
+    autograd.  Additions of one pass from several streams are ordered, and the stream that calls
+    backward waits for them, as it does for gradients that autograd accumulates; so are those of
+    passes that overlap on several host threads.  Passes called one after the other from different
+    streams are the caller's to order.
 
     To capture forward and backward into a graph, let no eager graph of the same leaves be
     alive: autograd would join their streams in the capture."""
@@ -384,10 +435,12 @@ class _Linear(torch.autograd.Function):
         if ctx.needs_input_grad[0]:
             dx = torch.matmul(dy.contiguous(), weight)
         if ctx.needs_input_grad[1]:
-            into = ctx.grad_into
-            target = torch.empty_like(weight) if into is None else into
-            act_wgrad(Act8(codes, scales, ctx.cols, ctx.code), _rows(dy), target, base=into)
-            dw = target if into is None else None
+            into, x8, dy2 = ctx.grad_into, Act8(codes, scales, ctx.cols, ctx.code), _rows(dy)
+            if into is None:
+                dw = torch.empty_like(weight)
+                act_wgrad(x8, dy2, dw)
+            else:
+                _add_in_turn(dy.device, lambda: act_wgrad(x8, dy2, into, base=into))
         return dx, dw, None, None
 
 
