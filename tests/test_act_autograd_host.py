@@ -234,3 +234,56 @@ def test_captured_and_eager_streams_do_not_wait_for_each_other(Z, monkeypatch):
             y.backward()
     assert streams.log == [("c1", "adds"), ("s1", "adds"), ("c2", "adds"), ("c1", "waits for", "c2"), ("c1", "adds"),
                            ("c2", "adds")]
+
+
+# ------------------------------------------------------------------------------ checkpoints in a pool
+
+def _pool(Z, layers, rows, cols):
+    codes = torch.zeros(layers, rows, cols, dtype=torch.uint8)
+    scales = torch.zeros(layers, rows, cols // 32, dtype=torch.uint8)
+    return [Z.Act8(codes[i], scales[i], cols) for i in range(layers)]
+
+
+def test_checkpoints_of_a_pool_are_marked_apart(Z):
+    """Checkpoints whose arrays are parts of one tensor share its version: filling one leaves the
+    others as they were, filling one anew is noticed by whichever handle it is done."""
+    x, nw = _randn(8, 64), _randn(64)
+    ws = [_randn(16, 64, seed=i).requires_grad_() for i in range(3)]
+    for refill in (None, 0, 1, 2):
+        acts = _pool(Z, 3, 8, 64)
+        ys = []
+        for i, w in enumerate(ws):
+            if i == 1:
+                Z.rmsnorm(x, nw, y8=acts[i])
+            else:
+                Z.act_pack(x, acts[i])
+            ys.append(Z.linear(x, w, x8=acts[i]))
+        if refill is not None:
+            Z.act_pack(x, Z.Act8(acts[refill].codes, acts[refill].scales, 64))
+        for i, y in enumerate(ys):
+            if i == refill:
+                with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                    y.sum().backward()
+            else:
+                y.sum().backward()
+    ys = [Z.linear(x, ws[0], x8=acts[0])]
+    acts[0].codes.zero_()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        ys[0].sum().backward()
+
+
+def test_half_pooled_checkpoints(Z):
+    """Codes of their own with scales in a pool, and the other way round."""
+    x, w = _randn(8, 64), _randn(16, 64).requires_grad_()
+    own = [torch.zeros(8, 64, dtype=torch.uint8) for _ in range(2)], [torch.zeros(8, 2, dtype=torch.uint8) for _ in range(2)]
+    pool = torch.zeros(2, 8, 64, dtype=torch.uint8), torch.zeros(2, 8, 2, dtype=torch.uint8)
+    for codes, scales in ((own[0], pool[1]), (pool[0], own[1])):
+        acts = [Z.Act8(codes[i], scales[i], 64) for i in range(2)]
+        ys = []
+        for act in acts:
+            Z.act_pack(x, act)
+            ys.append(Z.linear(x, w, x8=act))
+        Z.act_pack(x, acts[1])
+        ys[0].sum().backward()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            ys[1].sum().backward()

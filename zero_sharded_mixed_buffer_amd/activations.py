@@ -120,7 +120,21 @@ def _wrote(*tensors):
 
 
 def _wrote_act(act):
-    return (act.codes, act.scales) if act is not None else ()
+    """The arrays of a written checkpoint that get a new version.  Arrays that are parts of a larger
+    tensor share its version with all other parts, other checkpoints' among them: the fills of such
+    codes are counted beside their storage instead."""
+    if act is None:
+        return ()
+    codes = act.codes.untyped_storage()
+    if codes.nbytes() != act.codes.numel():
+        fills = codes.__dict__.setdefault("_act8_fills", {})
+        at = act.codes.storage_offset()
+        fills[at] = fills.get(at, 0) + 1
+    return [t for t in (act.codes, act.scales) if t.untyped_storage().nbytes() == t.numel()]
+
+
+def _fills(codes):
+    return codes.untyped_storage().__dict__.get("_act8_fills", {}).get(codes.storage_offset(), 0)
 
 
 def _at(t):
@@ -197,7 +211,7 @@ def act_pack(x, act):
     rows, cols, dev, stride = _input(x, "x", _DTYPES)
     arrays = _checkpoint(act, "act", rows, cols, dev)
     _enqueue("zs_act_pack", dev, x.data_ptr(), _DTYPES[x.dtype], stride, rows, cols, arrays)
-    _wrote(act.codes, act.scales)
+    _wrote(*_wrote_act(act))
 
 
 def act_unpack(act, out):
@@ -424,13 +438,16 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, x8, grad_into):
         ctx.save_for_backward(weight, x8.codes, x8.scales)
-        ctx.code, ctx.cols, ctx.grad_into = x8.code, x8.cols, grad_into
+        ctx.code, ctx.cols, ctx.grad_into, ctx.fills = x8.code, x8.cols, grad_into, _fills(x8.codes)
         return torch.nn.functional.linear(x, weight)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         weight, codes, scales = ctx.saved_tensors
+        if _fills(codes) > ctx.fills:
+            raise RuntimeError("the checkpoint of a linear layer's input, needed for its weight's gradient, has been "
+                               "modified by an inplace operation: it was filled anew before backward")
         dx = dw = None
         if ctx.needs_input_grad[0]:
             dx = torch.matmul(dy.contiguous(), weight)
