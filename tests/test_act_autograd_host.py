@@ -287,3 +287,99 @@ def test_half_pooled_checkpoints(Z):
         ys[0].sum().backward()
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             ys[1].sum().backward()
+
+
+# ------------------------------------------------------------------------------ a checkpoint and its tensor
+
+def _y8(Z, x, nw):
+    out = Z.norm(x, nw, y8="e4m3")
+    return out.y, out.y8
+
+
+@pytest.mark.parametrize("how", ["norm", "of", "act_pack", "rmsnorm_y8", "rmsnorm_h8", "rmsnorm_h8_of_x"])
+def test_checkpoint_of_a_tensor_changed_since_is_refused(Z, how):
+    """linear would multiply by what the tensor holds now and differentiate what it held then."""
+    x, nw, w = _randn(2, 4, 64), _randn(64), _randn(8, 64).requires_grad_()
+    flat, act = x.view(8, 64), _act(Z, 8, 64)
+    t = x
+    if how == "norm":
+        t, act = _y8(Z, x.requires_grad_(), nw)
+    elif how == "of":
+        act = Z.Act8.of(flat)
+    elif how == "act_pack":
+        Z.act_pack(flat, act)
+    else:
+        t = torch.empty_like(x)
+        if how == "rmsnorm_y8":
+            Z.rmsnorm(flat, nw, y=t.view(8, 64), y8=act)
+        elif how == "rmsnorm_h8":
+            Z.rmsnorm(flat, nw, residual=_randn(8, 64), h=t.view(8, 64), h8=act)
+        else:
+            t = x
+            Z.rmsnorm(flat, nw, h8=act)
+    for view in (t, t.view(8, 64), t.detach()):
+        torch.autograd.grad(Z.linear(view, w, x8=act).sum(), w)
+    with torch.no_grad():
+        t.mul_(2)
+    for view in (t, t.view(8, 64), t.detach()):
+        with pytest.raises(ValueError, match="changed"):
+            Z.linear(view, w, x8=act)
+    with torch.no_grad():
+        t.div_(2)
+        Z.act_pack(t.view(8, 64), act)  # the checkpoint of what it holds now
+    Z.linear(t, w, x8=act).sum().backward()
+    frozen = w.detach()
+    with torch.no_grad():
+        t.mul_(2)
+    Z.linear(t, frozen, x8=act)  # nothing is differentiated by the checkpoint
+
+
+def test_change_through_the_library_is_a_change(Z):
+    x, w = _randn(8, 64), _randn(8, 64).requires_grad_()
+    act = Z.Act8.of(x)
+    Z.act_unpack(_act(Z, 8, 64), x)
+    with pytest.raises(ValueError, match="changed"):
+        Z.linear(x, w, x8=act)
+
+
+def test_checkpoints_of_copies_and_plain_arrays_are_taken(Z):
+    """What cannot be known is the caller's: a copy, arrays made elsewhere, a tensor without versions,
+    one that lies where a freed one lay."""
+    x, w = _randn(8, 64), _randn(8, 64).requires_grad_()
+    act = Z.Act8.of(x)
+    Z.linear(x.clone(), w, x8=act).sum().backward()
+    Z.linear(x.data, w, x8=act).sum().backward()
+    x.mul_(2)
+    Z.linear(x.clone(), w, x8=act).sum().backward()
+    Z.linear(x, w, x8=Z.Act8(act.codes, act.scales, 64)).sum().backward()
+    act.codes.copy_(act.codes.clone())  # read back from somewhere, for what x holds now
+    Z.linear(x, w, x8=act).sum().backward()
+    parts = torch.zeros(2, 8, 64, dtype=BF16)
+    act = Z.Act8.of(parts[0])
+    parts[1].add_(1)
+    Z.linear(parts[0], w, x8=act).sum().backward()
+    with torch.inference_mode():
+        z = _randn(8, 64)
+        act = Z.Act8.of(z)
+    assert act.unpack().shape == (8, 64)
+    x = _randn(8, 64)
+    act = Z.Act8.of(x)
+    at = x.data_ptr()
+    del x
+    for _ in range(50):
+        again = torch.zeros(8, 64, dtype=BF16)
+        again.add_(1)
+        Z.linear(again, w, x8=act)
+        if again.data_ptr() == at:
+            break
+
+
+def test_checkpoint_does_not_keep_its_tensor(Z):
+    import weakref
+    x = _randn(8, 64)
+    storage = x.untyped_storage()
+    act = Z.Act8.of(x)
+    alive = weakref.ref(storage)
+    del x, storage
+    assert alive() is None
+    assert act.nbytes == 8 * 66

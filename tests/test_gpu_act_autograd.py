@@ -62,6 +62,51 @@ def test_overwritten_input_is_noticed(Z):
         loss.backward()
 
 
+def test_checkpoint_of_a_tensor_changed_since_is_refused(Z):
+    x, nw = _randn((8, 64), BF16, 31).requires_grad_(), torch.ones(64, dtype=BF16, device="cuda")
+    w = _randn((16, 64), BF16, 32).requires_grad_()
+    out = Z.norm(x, nw, y8="e4m3")
+    Z.linear(out.y.view(2, 4, 64), w, x8=out.y8)
+    out.y.mul_(2)
+    with pytest.raises(ValueError, match="changed"):
+        Z.linear(out.y, w, x8=out.y8)
+    Z.act_pack(out.y.detach(), out.y8)
+    dy = _randn((8, 16), BF16, 33)
+    Z.linear(out.y, w, x8=out.y8).backward(dy)
+    alone = torch.empty_like(w)
+    Z.act_wgrad(Z.Act8.of(out.y.detach()), dy, alone)
+    assert torch.equal(w.grad, alone) and x.grad is not None
+
+
+def test_checkpoints_of_a_pool(Z):
+    """Three layers' checkpoints as parts of one allocation, filled in turn: each backward takes its
+    own; one filled anew is an error."""
+    codes = torch.empty(3, 8, 64, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(3, 8, 2, dtype=torch.uint8, device="cuda")
+    acts = [Z.Act8(codes[i], scales[i], 64) for i in range(3)]
+    xs = [_randn((8, 64), BF16, 41 + i) for i in range(3)]
+    ws = [_randn((16, 64), BF16, 51 + i).requires_grad_() for i in range(3)]
+    dy = _randn((8, 16), BF16, 61)
+
+    def forward():
+        ys = []
+        for x, w, act in zip(xs, ws, acts):
+            Z.act_pack(x, act)
+            ys.append(Z.linear(x, w, x8=act))
+        return ys
+
+    for x, w, y in zip(xs, ws, forward()):
+        y.backward(dy)
+        alone = torch.empty_like(w)
+        Z.act_wgrad(Z.Act8.of(x), dy, alone)
+        assert torch.equal(w.grad, alone)
+    ys = forward()
+    Z.act_pack(xs[0], acts[1])
+    ys[0].backward(dy)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        ys[1].backward(dy)
+
+
 def test_inference_mode(Z):
     """Tensors of inference mode, inside and outside of it: the same outputs."""
     x, w = _randn((8, 64), BF16, 8), _randn((64,), BF16, 9)

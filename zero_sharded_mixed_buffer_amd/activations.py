@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import threading
+import weakref
 from collections import namedtuple
 
 import torch
@@ -38,10 +39,12 @@ class Act8:
     `scales`, uint8 [rows, groups of 32], both contiguous on one GPU; `code` is "e4m3" or
     "int8".  The arrays are the caller's, or Act8.empty's."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "code", "device", "arrays", "address")
+    __slots__ = ("codes", "scales", "rows", "cols", "code", "device", "arrays", "address", "source", "versions")
 
     # `arrays` is the struct that the C calls read; every call writes the tensors' present
-    # addresses into it, so that storage which was freed and allocated again is found
+    # addresses into it, so that storage which was freed and allocated again is found.
+    # `source` is the storage (weakly held) of the tensor that the checkpoint was last taken of, if
+    # that is known, `versions` that tensor's and the codes' version then
 
     def __init__(self, codes, scales, cols, code="e4m3"):
         if code not in CODES:
@@ -66,6 +69,21 @@ class Act8:
         self.device = device
         self.arrays = A.ActArrays(0, 0, CODES[code], 0)
         self.address = ctypes.addressof(self.arrays)
+        self.source, self.versions = None, None
+
+    def _taken_of(self, t):
+        self.source = None
+        if t is not None and not t.is_inference() and _has_own_version(t) and not self.codes.is_inference():
+            self.source, self.versions = weakref.ref(t.untyped_storage()), (t._version, self.codes._version)
+
+    def _outlived(self, t):
+        """Whether t is known to have been changed since the checkpoint was taken of it.  Versions
+        only grow; a smaller one is counted apart (t.data's) and says nothing, and neither does that
+        of a part of a larger tensor.  Codes written by other means since then may be anyone's."""
+        if self.source is None or t.is_inference() or self.source() is not t.untyped_storage():
+            return False
+        of_t, of_codes = self.versions
+        return t._version > of_t and self.codes._version == of_codes
 
     @classmethod
     def empty(cls, rows, cols, code="e4m3", device="cuda"):
@@ -119,18 +137,22 @@ def _wrote(*tensors):
     torch.autograd.graph.increment_version([t for t in tensors if t is not None and not t.is_inference()])
 
 
+def _has_own_version(t):
+    """Whether t is no part of a larger tensor, whose version it would share with other parts."""
+    return not t._is_view() or t.numel() * t.element_size() == t.untyped_storage().nbytes()
+
+
 def _wrote_act(act):
     """The arrays of a written checkpoint that get a new version.  Arrays that are parts of a larger
     tensor share its version with all other parts, other checkpoints' among them: the fills of such
     codes are counted beside their storage instead."""
     if act is None:
         return ()
-    codes = act.codes.untyped_storage()
-    if codes.nbytes() != act.codes.numel():
-        fills = codes.__dict__.setdefault("_act8_fills", {})
+    if not _has_own_version(act.codes):
+        fills = act.codes.untyped_storage().__dict__.setdefault("_act8_fills", {})
         at = act.codes.storage_offset()
         fills[at] = fills.get(at, 0) + 1
-    return [t for t in (act.codes, act.scales) if t.untyped_storage().nbytes() == t.numel()]
+    return [t for t in (act.codes, act.scales) if _has_own_version(t)]
 
 
 def _fills(codes):
@@ -212,6 +234,7 @@ def act_pack(x, act):
     arrays = _checkpoint(act, "act", rows, cols, dev)
     _enqueue("zs_act_pack", dev, x.data_ptr(), _DTYPES[x.dtype], stride, rows, cols, arrays)
     _wrote(*_wrote_act(act))
+    act._taken_of(x)
 
 
 def act_unpack(act, out):
@@ -241,6 +264,10 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, y8=None, h8=None
     _enqueue("zs_rmsnorm", dev, x.data_ptr(), xs, _at(residual), rs, weight.data_ptr(), _DTYPES[dt], rows, cols, eps,
              _at(h), hs, _at(y), ys, ya, ha, _at(rstd))
     _wrote(h, y, rstd, *_wrote_act(y8), *_wrote_act(h8))
+    if y8 is not None:
+        y8._taken_of(y)
+    if h8 is not None:
+        h8._taken_of(x if h is None and residual is None else h)
 
 
 def rmsnorm_backward(dy, saved, weight, rstd, dx, dh=None, dweight=None, base=None, workspace=None):
@@ -466,8 +493,11 @@ def linear(x, weight, x8=None, code="e4m3", grad_into=None):
     checkpoint of x for the weight's gradient instead of x.
 
     x8: the checkpoint of x if there is one already (norm's y8: several layers that read one
-    tensor share it); otherwise it is taken here, with `code`.  grad_into, and
-    capture into graphs: as for norm.  The two products with the weight are the library's; the weight's gradient is act_wgrad's."""
+    tensor share it); otherwise it is taken here, with `code`.  It has to hold what x holds: an x
+    changed in place since its checkpoint was taken is refused, any other x (a copy, a result of
+    x, a part of a larger tensor) is the caller's to match.  grad_into, and capture into graphs:
+    as for norm.  The two products with the weight are the library's; the weight's gradient is
+    act_wgrad's."""
     if code not in CODES:
         raise ValueError(f"code is 'e4m3' or 'int8', not {code!r}")
     if x.dim() < 1 or x.dtype not in HALF or weight.dtype != x.dtype or weight.dim() != 2:
@@ -486,4 +516,6 @@ def linear(x, weight, x8=None, code="e4m3", grad_into=None):
         return torch.nn.functional.linear(x, weight)
     if x8 is None:
         x8 = Act8.of(_rows(x.detach()), code)
+    elif x8._outlived(x):
+        raise ValueError("x has been changed in place since x8 was taken of it")
     return _Linear.apply(x, weight, x8, grad_into)
