@@ -55,7 +55,7 @@ typedef struct {
     void* codes;
     void* scales;
     int32_t code;     /* zs_code */
-    int32_t reserved; /* 0 */
+    int32_t reserved; /* 0 (anything else is ZS_EINVAL) */
 } zs_act;
 
 /* Bytes of the codes and scales arrays of a rows x cols checkpoint.  Host only.

@@ -1,0 +1,32 @@
+"""CPU tests of refusals of the activation operators' C entry points and tensor-level calls (no
+kernel runs)."""
+
+import pytest
+import torch
+
+# Addresses that pass the checks and are never read: every call below is refused on the host.
+P = 1 << 20
+S = 0  # the null stream
+
+
+@pytest.fixture
+def Z():
+    import zero_sharded_mixed_buffer_amd as Z
+    Z.lib()
+    return Z
+
+
+def _refused(Z, match, fn, *args, **kw):
+    with pytest.raises(Z._abi.ZsInvalidArgument, match=match):
+        fn(*args, stream=S, **kw)
+
+
+def test_reserved_field_is_checked(Z):
+    """zs_act.reserved is 0, in every call that takes a checkpoint."""
+    act = Z.ActArrays(P, P, 0, 1)
+    _refused(Z, "reserved", Z.zs_act_pack, P, 0, 64, 4, 64, act)
+    _refused(Z, "reserved", Z.zs_act_unpack, act, 4, 64, P, 0, 64)
+    _refused(Z, "reserved", Z.zs_rmsnorm, P, 64, None, 0, P, 0, 4, 64, 1e-6, y8=act)
+    _refused(Z, "reserved", Z.zs_rmsnorm, P, 64, None, 0, P, 0, 4, 64, 1e-6, h8=act)
+    _refused(Z, "reserved", Z.zs_rmsnorm_backward, P, 64, None, 0, None, 0, act, P, P, 0, 4, 64, P, 64)
+    _refused(Z, "reserved", Z.zs_act_wgrad, act, 4, 64, P, 0, 48, 48, P, 0, 64, workspace=P, workspace_bytes=1 << 20)

@@ -939,6 +939,7 @@ zs_status check_matrix(const void* p, int64_t stride, int dt, int64_t rows, int6
 zs_status check_act(const zs_act* a, int64_t rows, const char* what) {
   if (a == nullptr) return fail(ZS_EINVAL, "%s is NULL", what);
   if (a->code != ZS_E4M3 && a->code != ZS_INT8) return fail(ZS_EINVAL, "%s: unknown code %d", what, a->code);
+  if (a->reserved != 0) return fail(ZS_EINVAL, "%s: reserved must be 0", what);
   if (rows > 0 && (a->codes == nullptr || a->scales == nullptr))
     return fail(ZS_EINVAL, "%s: codes or scales is NULL", what);
   if (!aligned16(a->codes)) return fail(ZS_EINVAL, "%s: codes must be 16-byte aligned", what);
