@@ -85,8 +85,8 @@ zs_status zs_act_unpack(const zs_act* act, int64_t rows, int64_t cols, void* dst
  *       of h.
  *   rstd: NULL or rows fp32.
  * cols is 1 .. 16384.
- * Errors: ZS_EINVAL on NULL x or weight, no output at all, a bad dtype, size, stride,
- * alignment or code, or an eps that is no normal fp32 number above 0. */
+ * Errors: ZS_EINVAL on NULL x or weight, no output at all, h and y or y8 and h8 in one place, a
+ * bad dtype, size, stride, alignment or code, or an eps that is no normal fp32 number above 0. */
 zs_status zs_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                      const void* weight, zs_dtype dtype, int64_t rows, int64_t cols, double eps, void* h,
                      int64_t h_stride, void* y, int64_t y_stride, const zs_act* y8, const zs_act* h8, float* rstd,

@@ -30,3 +30,12 @@ def test_reserved_field_is_checked(Z):
     _refused(Z, "reserved", Z.zs_rmsnorm, P, 64, None, 0, P, 0, 4, 64, 1e-6, h8=act)
     _refused(Z, "reserved", Z.zs_rmsnorm_backward, P, 64, None, 0, None, 0, act, P, P, 0, 4, 64, P, 64)
     _refused(Z, "reserved", Z.zs_act_wgrad, act, 4, 64, P, 0, 48, 48, P, 0, 64, workspace=P, workspace_bytes=1 << 20)
+
+
+def test_norm_outputs_in_one_place_are_refused(Z):
+    """The checkpoint of y and that of h in one pair of arrays, y and h in one matrix: each output would
+    overwrite the other."""
+    call = dict(x=P, x_stride=64, residual=P, residual_stride=64, weight=P, dtype=0, rows=4, cols=64, eps=1e-6)
+    _refused(Z, "y8 and h8", Z.zs_rmsnorm, **call, y8=Z.ActArrays(P, 2 * P, 0, 0), h8=Z.ActArrays(P, 3 * P, 0, 0))
+    _refused(Z, "y8 and h8", Z.zs_rmsnorm, **call, y8=Z.ActArrays(P, 2 * P, 0, 0), h8=Z.ActArrays(3 * P, 2 * P, 1, 0))
+    _refused(Z, "h and y", Z.zs_rmsnorm, **call, h=2 * P, h_stride=64, y=2 * P, y_stride=64)

@@ -255,8 +255,6 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, y8=None, h8=None
     rs = _matrix(residual, "residual", dt, rows, cols, dev) if residual is not None else 0
     hs = _matrix(h, "h", dt, rows, cols, dev) if h is not None else 0
     ys = _matrix(y, "y", dt, rows, cols, dev) if y is not None else 0
-    if h is not None and y is not None and rows and h.data_ptr() == y.data_ptr():
-        raise ValueError("h and y are the same memory")
     if rstd is not None:
         _vector(rstd, "rstd", (torch.float32,), rows, dev)
     ya = _checkpoint(y8, "y8", rows, cols, dev) if y8 is not None else None

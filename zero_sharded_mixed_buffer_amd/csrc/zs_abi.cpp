@@ -1038,6 +1038,9 @@ extern "C" zs_status zs_rmsnorm(const void* x, int64_t x_stride, const void* res
   if (!grad_aligned(rstd, ZS_FP32)) return fail(ZS_EINVAL, "rstd must be aligned to its elements");
   if (h == nullptr && y == nullptr && y8 == nullptr && h8 == nullptr && rstd == nullptr)
     return fail(ZS_EINVAL, "no output: h, y, y8, h8 and rstd are all NULL");
+  if (rows > 0 && h != nullptr && h == y) return fail(ZS_EINVAL, "h and y are the same memory");
+  if (rows > 0 && y8 != nullptr && h8 != nullptr && (y8->codes == h8->codes || y8->scales == h8->scales))
+    return fail(ZS_EINVAL, "y8 and h8 are the same memory");
   if (!(eps >= 1.17549435e-38) || !(eps <= 3.4e38)) return fail(ZS_EINVAL, "eps must be a normal fp32 number above 0");
   zs::NormArgs a{};
   a.x = static_cast<const uint16_t*>(x);
