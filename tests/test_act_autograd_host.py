@@ -383,3 +383,16 @@ def test_checkpoint_does_not_keep_its_tensor(Z):
     del x, storage
     assert alive() is None
     assert act.nbytes == 8 * 66
+
+
+# ------------------------------------------------------------------------------ empty layers
+
+def test_linear_without_outputs(Z):
+    """A weight of no rows: an empty product, whose backward has nothing to add (it was refused in the
+    middle of the pass)."""
+    x, w = _randn(8, 64).requires_grad_(), torch.zeros(0, 64, dtype=BF16, requires_grad=True)
+    for grad_into in (None, torch.zeros(0, 64)):
+        y = Z.linear(x, w, grad_into=grad_into)
+        assert y.shape == (8, 0)
+        y.sum().backward()
+        assert x.grad.shape == (8, 64) and not x.grad.any()

@@ -510,7 +510,7 @@ def linear(x, weight, x8=None, code="e4m3", grad_into=None):
     _check_grad_into(grad_into, weight)
     if x8 is not None:
         _checkpoint(x8, "x8", x.numel() // x.shape[-1], x.shape[-1], x.device)
-    if not (weight.requires_grad and torch.is_grad_enabled()):  # nothing of x is kept
+    if not (weight.requires_grad and torch.is_grad_enabled()) or weight.shape[0] == 0:  # nothing of x is kept
         return torch.nn.functional.linear(x, weight)
     if x8 is None:
         x8 = Act8.of(_rows(x.detach()), code)
