@@ -12,7 +12,6 @@ BF16 = torch.bfloat16
 @pytest.fixture
 def Z(monkeypatch):
     import zero_sharded_mixed_buffer_amd as Z
-    monkeypatch.setattr(Z.activations, "_adding", {}, raising=False)
     monkeypatch.setattr(Z.activations, "_need_gpu", lambda device: None)
     monkeypatch.setattr(Z.activations, "_enqueue", lambda name, device, *args: None)
     Z.lib()
@@ -219,12 +218,12 @@ def test_captured_and_eager_streams_do_not_wait_for_each_other(Z, monkeypatch):
     """A wait between a stream that is being captured and one that is not would end the capture:
     there is none, nor for a stream whose capture has ended since."""
     streams = _Streams(monkeypatch, Z)
-    A = Z.activations
+    A, into = Z.activations, torch.zeros(4)
     for name, streams.capturing in (("c1", ("c1",)), ("s1", ("c1", "c2")), ("c2", ("c1", "c2")), ("c1", ("c1", "c2")),
                                     ("c2", ("c2",))):
         def add(name=name):
             streams.name = name
-            A._add_in_turn(torch.device("cpu"), lambda: streams.log.append((name, "adds")))
+            A._add_in_turn(into, lambda: streams.log.append((name, "adds")))
         x = torch.zeros(1, requires_grad=True)
         y = x * 1
         y.register_hook(lambda g: add())
@@ -396,3 +395,26 @@ def test_linear_without_outputs(Z):
         assert y.shape == (8, 0)
         y.sum().backward()
         assert x.grad.shape == (8, 64) and not x.grad.any()
+
+
+def test_buffers_apart_wait_for_nothing(Z, monkeypatch):
+    """Additions to two buffers on two streams have no order; two parts of one buffer have."""
+    for shared in (False, True):
+        streams = _Streams(monkeypatch, Z)
+        w = _randn(64, 64).requires_grad_()
+        flat = torch.zeros(2, 64, 64)
+        intos = [flat[0], flat[1]] if shared else [torch.zeros(64, 64), torch.zeros(64, 64)]
+        x = _randn(4, 64)
+        outs = [Z.linear(x, w, x8=_act(Z, 4, 64), grad_into=into) for into in intos]
+        total = sum(o.sum() for o in outs)
+        for o, name in zip(outs, ("s1", "s2")):
+            _node(streams, name, o)
+        total.register_hook(lambda g: _ends_on(streams, "main"))
+        total.backward()
+        assert ("s1", "zs_act_wgrad") in streams.log and ("s2", "zs_act_wgrad") in streams.log
+        waits = {e for e in streams.log if "waits for" in e}
+        if shared:
+            assert waits in ({("s2", "waits for", "s1"), ("main", "waits for", "s2")},
+                             {("s1", "waits for", "s2"), ("main", "waits for", "s1")})
+        else:
+            assert waits == {("main", "waits for", "s1"), ("main", "waits for", "s2")}

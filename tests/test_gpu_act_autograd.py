@@ -176,7 +176,8 @@ def test_additions_of_two_streams(Z, what, late):
         torch.cuda.synchronize()
         assert torch.equal(got, want), turn
         assert w.grad is None
-    assert Z.activations._adding[w.device] == [None, 0]
+    adds = into.untyped_storage()._adds
+    assert adds.last is None and adds.under_way == 0
 
 
 def test_captured_additions_of_two_streams(Z):

@@ -344,12 +344,20 @@ def _check_grad_into(grad_into, weight):
 
 # Additions to a caller's buffer (grad_into) in a backward pass.  Autograd runs each backward on the
 # stream of its forward and orders only the gradients that it is handed; these it never sees.  So
-# each addition waits for the one before it on the device if that ran on another stream, and at the
-# end of a pass the stream that called it waits for the last.  By device: the stream of the
-# last addition, and how many additions belong to passes that have not ended.  (A pass that fails
-# never reports its end: its stream then stays one to wait for, which is harmless.)
-_adding = {}
-_adding_lock = threading.RLock()
+# each addition waits for the one before it to the same storage if that ran on another stream, and
+# at the end of a pass the stream that called it waits for the last.  (A pass that fails never
+# reports its end: its stream then stays one to wait for, which is harmless.)
+class _Adds:
+    """The additions to one storage: the stream of the last one, as long as a pass is under way,
+    and how many the passes under way have made."""
+
+    __slots__ = ("last", "under_way")
+
+    def __init__(self):
+        self.last, self.under_way = None, 0
+
+
+_adds_lock = threading.RLock()
 
 
 def _captured(stream):
@@ -364,25 +372,25 @@ def _wait_for(stream, last):
         stream.wait_stream(last)
 
 
-def _add_in_turn(device, add):
-    """Call `add`, which enqueues work that adds to a caller's buffer, within a backward pass."""
+def _add_in_turn(into, add):
+    """Call `add`, which enqueues work that adds to `into`, within a backward pass."""
+    device = into.device
     stream = torch.cuda.current_stream(device)
-    with _adding_lock:
-        state = _adding.setdefault(device, [None, 0])
-        _wait_for(stream, state[0])
+    with _adds_lock:
+        adds = into.untyped_storage().__dict__.setdefault("_adds", _Adds())
+        _wait_for(stream, adds.last)
         add()
-        state[0] = stream
-        state[1] += 1
-    torch.autograd.Variable._execution_engine.queue_callback(lambda: _pass_ended(device))
+        adds.last = stream
+        adds.under_way += 1
+    torch.autograd.Variable._execution_engine.queue_callback(lambda: _pass_ended(adds, device))
 
 
-def _pass_ended(device):
+def _pass_ended(adds, device):
     caller = torch.cuda.current_stream(device)
-    with _adding_lock:
-        state = _adding[device]
-        _wait_for(caller, state[0])
-        state[1] -= 1
-        state[0] = caller if state[1] else None
+    with _adds_lock:
+        _wait_for(caller, adds.last)
+        adds.under_way -= 1
+        adds.last = caller if adds.under_way else None
 
 
 class _Norm(torch.autograd.Function):
@@ -421,8 +429,7 @@ class _Norm(torch.autograd.Function):
         if dweight is None or into is None:
             rmsnorm_backward(dy2, saved, weight, rstd, dx, dh=dh2, dweight=dweight)
         else:
-            _add_in_turn(dy.device, lambda: rmsnorm_backward(dy2, saved, weight, rstd, dx, dh=dh2, dweight=into,
-                                                             base=into))
+            _add_in_turn(into, lambda: rmsnorm_backward(dy2, saved, weight, rstd, dx, dh=dh2, dweight=into, base=into))
         dx = dx.view(dy.shape)
         return (dx, dx if ctx.two else None, dweight if into is None else None, None, None, None, None)
 
@@ -436,9 +443,8 @@ def norm(x, weight, eps=1e-6, residual=None, save="e4m3", y8=None, grad_into=Non
     grad_into: a buffer of the weight's shape (its dtype or fp32; with flat_views the weight's
     .grad) that backward adds the weight's gradient to; the weight then receives none from
     autograd.  Additions of one pass from several streams are ordered, and the stream that calls
-    backward waits for them, as it does for gradients that autograd accumulates; so are those of
-    passes that overlap on several host threads.  Passes called one after the other from different
-    streams are the caller's to order.
+    backward waits for them, as it does for gradients that autograd accumulates.  Passes called
+    from different streams, or host threads, that add to one buffer are the caller's to order.
 
     To capture forward and backward into a graph, let no eager graph of the same leaves be
     alive: autograd would join their streams in the capture."""
@@ -482,7 +488,7 @@ class _Linear(torch.autograd.Function):
                 dw = torch.empty_like(weight)
                 act_wgrad(x8, dy2, dw)
             else:
-                _add_in_turn(dy.device, lambda: act_wgrad(x8, dy2, into, base=into))
+                _add_in_turn(into, lambda: act_wgrad(x8, dy2, into, base=into))
         return dx, dw, None, None
 
 
