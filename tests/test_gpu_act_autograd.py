@@ -217,3 +217,40 @@ def test_captured_additions_of_two_streams(Z):
         torch.cuda.synchronize()
         want = sum(dy.double().t().contiguous() @ x.double() for x, dy in zip(xs, dys))
         assert torch.equal(into.double(), want), turn
+
+
+def test_several_host_threads_finish(Z):
+    """Four host threads, each with a layer, a stream and a buffer of its own: every one of them ends,
+    after all of its rounds, with the gradients that it has alone."""
+    import threading
+    rounds, count = 8, [0] * 4
+    xs = [_randn((64 + 16 * i, 96), BF16, 71 + i) for i in range(4)]
+    ws = [_randn((40, 96), BF16, 81 + i).requires_grad_() for i in range(4)]
+    intos = [torch.zeros(40, 96, device="cuda") for _ in range(4)]
+
+    def step(i):
+        intos[i].zero_()
+        Z.linear(xs[i], ws[i], grad_into=intos[i]).float().square().sum().backward()
+        return intos[i].clone()
+
+    want = [step(i) for i in range(4)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(rounds):
+                got = step(i)
+                stream.synchronize()
+                if not torch.equal(got, want[i]):
+                    wrong.append(i)
+                count[i] += 1
+
+    threads = [threading.Thread(target=work, args=(i,), daemon=True) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(30)
+    assert not any(t.is_alive() for t in threads)
+    assert count == [rounds] * 4 and not wrong
