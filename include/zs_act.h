@@ -21,7 +21,11 @@
  * group with an infinity or a NaN has b = 255 and stands for NaN throughout, so that it
  * reaches the overflow check of the step.  A power of two loses nothing more on the way
  * back: code * s is exact in bf16 and fp32 down to their smallest normal numbers, and in
- * fp16 if the source was fp16 (a value past the largest fp16 number is brought to it).
+ * fp16 if the source held fp16 numbers.  Other values are rounded to fp16 once, to nearest
+ * even: those of zs_rmsnorm's y8, which is taken before y is rounded, can lie below fp16's
+ * smallest step, and those of a bf16 or fp32 source anywhere.  Past fp16's range a value
+ * becomes its largest number, not an infinity: the code's rounding can lift an fp16 source
+ * there, but a bf16 or fp32 source that really held such a value is cut off in silence.
  *
  * Conventions as in zs.h, and:
  *   - A matrix argument is a device pointer with a row stride in elements (>= cols, or any
@@ -122,8 +126,9 @@ zs_status zs_act_wgrad_workspace(int64_t rows, int64_t cols, int64_t outs, int64
 
 /* Weight gradient of a linear layer y = x W^T from the checkpoint of its input:
  *   dw[n][k] = base[n][k] + sum over tokens t of dy[t][n] * x8[t][k]
- * on the matrix cores: x8's values take part in dy's dtype (exact, see above), products are
- * exact and summed in fp32, the result is rounded once to dw_dtype.
+ * on the matrix cores: x8's values take part in dy's dtype (for bf16 as they are, but that
+ * those below its normal numbers may count as zero; for fp16 see above), products are exact
+ * and summed in fp32, the result is rounded once to dw_dtype.
  *   x8: checkpoint of rows x cols;  dy: rows x outs, bf16 or fp16.
  *   dw: outs x cols of dw_dtype (dy's dtype or fp32), or cols x outs when in_major is not 0
  *       (weights kept as (in, out)); a view of the flat gradient buffer, for instance.

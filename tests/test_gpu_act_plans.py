@@ -186,3 +186,51 @@ def test_no_rows_under_autograd(Z, save):
     (y.sum() + z.sum()).backward()
     assert x.grad.shape == r.grad.shape == x.shape
     assert not bool(nw.grad.any()) and not bool(w.grad.any()) and bool((into == 2).all())
+
+
+# ------------------------------------------------------------------------------ weight gradient
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_wgrad_rounds_each_value_once(Z, dtype, code):
+    """Every code under every scale byte, one row at a time through an identity: a checkpoint's value
+    takes part rounded once into dy's type, to nearest even, fp16's subnormal numbers included and
+    past fp16's range its largest number.  Below bf16's normal numbers a value may count as zero; scale
+    bytes whose codes pass bf16's range are left out (448 * 2^(246 - 127) < 2^128), as an infinity
+    times the identity's zeros is NaN."""
+    n = 247 if dtype == BF16 else 255
+    table = [c for c in range(256) if code == "int8" or c & 127 != 127]
+    codes = torch.tensor(table + [0] * (256 - len(table)), dtype=torch.uint8).repeat(n, 1)
+    scales = torch.arange(n).to(torch.uint8)[:, None].repeat(1, 8)
+    act = Z.Act8(codes.cuda(), scales.cuda(), 256, code)
+    dw = torch.empty(n, 256, device="cuda")
+    Z.act_wgrad(act, torch.eye(n, dtype=dtype, device="cuda"), dw)
+    values = AO.values(codes, scales, 256, code)
+    got, want = dw.cpu().double(), AO.rounded(values, dtype).double()
+    if dtype == BF16:
+        small = values.abs() < 2.0 ** -126
+        assert bool((got[small].abs() <= 2.0 ** -126).all())
+        got, want = got[~small], want[~small]
+    bad = (got != want).nonzero()
+    assert len(bad) == 0, (len(bad), bad[0].tolist(), float(got[tuple(bad[0])]), float(want[tuple(bad[0])]))
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_wgrad_of_an_fp16_norms_checkpoint(Z, code):
+    """fp16 y8, taken from y before its rounding: values that are not on fp16's grid are rounded to it,
+    by at most half of fp16's smallest step, and the weight gradient is that of the rounded values."""
+    rows, cols, outs = 200, 96, 40
+    # small enough that scales go below fp16's smallest step (e4m3's least code is 2^-9 of one)
+    x, w = _matrix(rows, cols, FP16, 61), _matrix(1, cols, FP16, 62, sigma=2.0 ** (-9 if code == "e4m3" else -20))[0]
+    y8 = Z.Act8.empty(rows, cols, code)
+    Z.rmsnorm(x, w, y8=y8)
+    dy = _matrix(rows, outs, FP16, 63, sigma=0.1)
+    dw = torch.empty(outs, cols, device="cuda")
+    Z.act_wgrad(y8, dy, dw)
+    values = y8.unpack(FP32).double()
+    seen = values.half().double()
+    assert float((values - seen).abs().max()) <= 2.0 ** -25
+    assert not torch.equal(values, seen)
+    want, mags = dy.double().t().contiguous() @ seen, dy.double().abs().t().contiguous() @ seen.abs()
+    # sums of 200 terms in fp32, two u a step on the matrix cores
+    _assert_within(dw, want, 2 * U * (rows + 8) * mags, "dw")

@@ -238,7 +238,8 @@ def act_pack(x, act):
 
 
 def act_unpack(act, out):
-    """Read a checkpoint back into matrix `out` (bf16, fp16 or fp32; any row stride)."""
+    """Read a checkpoint back into matrix `out` (bf16, fp16 or fp32; any row stride), each value
+    rounded once; past fp16's range to its largest number."""
     rows, cols, dev, stride = _input(out, "out", _DTYPES)
     arrays = _checkpoint(act, "act", rows, cols, dev)
     _enqueue("zs_act_unpack", dev, arrays, rows, cols, out.data_ptr(), _DTYPES[out.dtype], stride)
@@ -302,7 +303,9 @@ def act_wgrad(x8, dy, dw, base=None, in_major=False, workspace=None):
     """dw = base + dy^T x: the weight gradient of y = x W^T from the checkpoint of x and the
     gradient dy [rows, outs] of y.  dw is [outs, cols], or [cols, outs] with in_major (weights
     kept as (in, out)), in dy's dtype or fp32; base has dw's dtype, shape and stride and may be
-    dw itself: the gradient is then added to what is there."""
+    dw itself: the gradient is then added to what is there.  x8's values take part in dy's dtype:
+    exact in bf16, and in fp16 for checkpoints of fp16 values (others are rounded to fp16, past
+    its range to its largest number)."""
     rows, outs, dev, dys = _input(dy, "dy", HALF)
     arrays = _checkpoint(x8, "x8", rows, x8.cols, dev)
     shape = (x8.cols, outs) if in_major else (outs, x8.cols)

@@ -6,7 +6,7 @@
 // the matrix instruction needs consecutive tokens of one column.  Tiles are staged in LDS as
 // they lie in memory (a row per token) and read back through gfx950's transposing LDS loads,
 // four tokens of one column per lane and load.  The checkpoint's codes become 2-byte values
-// (code * 2^k, exact) on the way into LDS, once per workgroup instead of once per wave.
+// on the way into LDS, once per workgroup instead of once per wave.
 //
 // The matrix cores bound it: 2 * rows * cols * outs operations, at 1.15 to 1.25 PFLOP/s where
 // there are enough tiles (8192 tokens, 4096 -> 14336 with a bf16 base: 0.82 ms), what the library
@@ -52,9 +52,11 @@ __device__ __forceinline__ uint32_t fp16_range(uint32_t x) {
       uint32_t, __builtin_elementwise_maximum(__builtin_elementwise_minimum(__builtin_bit_cast(v2h, x), top), -top));
 }
 
-// Sixteen codes under scale byte b as 2-byte values in memory order.  gfx950 converts a pair of
-// e4m3 codes with a power-of-two scale in one instruction, which takes the scale from the exponent
-// field alone: exact for every code and scale byte, 0 (2^-127) and 255 (NaN) included.
+// Sixteen codes under scale byte b as 2-byte values in memory order, each rounded once to nearest
+// even.  gfx950 converts a pair of e4m3 codes with a power-of-two scale in one instruction, which
+// takes the scale from the exponent field alone, 0 (2^-127) and 255 (NaN) included.  The rounding
+// changes nothing in bf16 down to its smallest normal number (a code has four significant bits, or
+// seven), nor in fp16 for values that were fp16 numbers.
 template <int DT, int CODE>
 __device__ __forceinline__ void values16(const v4u& c, int b, v4u& lo, v4u& hi) {
   if constexpr (CODE == ZS_E4M3) {
