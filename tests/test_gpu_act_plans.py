@@ -68,8 +68,8 @@ def test_large_checkpoints(Z, cols, pad, dtype, code):
 
 # rows and columns that take: a wave to a row, two chunks to a lane; two rows to a lane; 512 threads to a row
 # (with a residual); 256 threads of two chunks; 512 of two; 1024 of two
-NORMS = [(4097, 1003), (5000, 544), (33001, 100), (33001, 512), (8201, 2600), (8201, 4096), (4100, 2049), (300, 8191),
-         (300, 16383)]
+NORMS = [(4097, 1003), (5000, 544), (33001, 100), (33001, 512), (8201, 2600), (8201, 3201), (8201, 4096), (4100, 2049),
+         (300, 8191), (300, 16383)]
 
 
 @pytest.mark.parametrize("with_residual", [True, False])

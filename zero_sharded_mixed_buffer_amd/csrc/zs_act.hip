@@ -551,8 +551,11 @@ hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
 // against 24.0 with a workgroup to a row, half its lanes idle) where the rows fill the card that way
 // (777 x 1003: 6.2 us against 5.7).  From there a workgroup takes a row:
 // of 256 threads with two chunks each, except that with a residual, whose outputs too are twice as
-// many, and rows enough, 512 threads with one chunk are faster (16384 x 4096, all outputs: 109.9 us
-// against 117.4; without a residual 64.9 against 57.1; 2048 rows 16.7 against 14.2).
+// many, rows enough and most of the threads busy, 512 threads with one chunk are faster (16384 rows,
+// all outputs: 4096 columns 110.6 us against 117.5, 3584 99.0 against 100.3, 3200 89.6 against
+// 91.0, but 2688 77.5 against 76.3; with 16-bit outputs alone 85.9 against 88.1, 76.5 against 77.0,
+// 70.5 against 68.1, 62.5 against 57.5; 4096 columns without a residual 64.9 against 57.1, 2048 rows
+// 16.7 against 14.2).
 template <int DT>
 hipError_t norm_cols(const NormArgs& a, hipStream_t s) {
   const bool many = a.rows >= 32768;
@@ -561,7 +564,7 @@ hipError_t norm_cols(const NormArgs& a, hipStream_t s) {
   if (a.cols <= 1024 && a.rows >= 4096) return norm_launch<DT, 64, 2>(a, s);
   if (a.cols <= 2048) return norm_launch<DT, 256, 1>(a, s);
   if (a.cols <= 4096)
-    return a.residual != nullptr && a.rows >= 8192 && a.cols > 2560 ? norm_launch<DT, 512, 1>(a, s)
+    return a.residual != nullptr && a.rows >= 8192 && a.cols > 3200 ? norm_launch<DT, 512, 1>(a, s)
                                                                     : norm_launch<DT, 256, 2>(a, s);
   if (a.cols <= 8192) return norm_launch<DT, 512, 2>(a, s);
   return norm_launch<DT, 1024, 2>(a, s);
