@@ -39,12 +39,15 @@ class Act8:
     `scales`, uint8 [rows, groups of 32], both contiguous on one GPU; `code` is "e4m3" or
     "int8".  The arrays are the caller's, or Act8.empty's."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "code", "device", "arrays", "address", "source", "versions")
+    __slots__ = ("codes", "scales", "rows", "cols", "code", "device", "arrays", "address", "marks", "fills", "source",
+                 "versions")
 
     # `arrays` is the struct that the C calls read; every call writes the tensors' present
     # addresses into it, so that storage which was freed and allocated again is found.
-    # `source` is the storage (weakly held) of the tensor that the checkpoint was last taken of, if
-    # that is known, `versions` that tensor's and the codes' version then
+    # `marks` are the arrays that a write gives a new version, `fills` where fills are counted for
+    # codes that are part of a larger tensor.  `source` is the storage (weakly held) of the tensor
+    # that the checkpoint was last taken of, if that is known, `versions` that tensor's and the
+    # codes' version then
 
     def __init__(self, codes, scales, cols, code="e4m3"):
         if code not in CODES:
@@ -69,12 +72,25 @@ class Act8:
         self.device = device
         self.arrays = A.ActArrays(0, 0, CODES[code], 0)
         self.address = ctypes.addressof(self.arrays)
+        # Arrays that are parts of a larger tensor share its version with all other parts, other
+        # checkpoints' among them: the fills of such codes are counted beside their storage instead
+        self.marks = [t for t in (codes, scales) if _has_own_version(t)]
+        self.fills = None if self.marks and self.marks[0] is codes else _fills(codes)
         self.source, self.versions = None, None
+
+    def _wrote(self):
+        if self.fills is not None:
+            self.fills[0] += 1
+        return self.marks
 
     def _taken_of(self, t):
         self.source = None
-        if t is not None and not t.is_inference() and _has_own_version(t) and not self.codes.is_inference():
-            self.source, self.versions = weakref.ref(t.untyped_storage()), (t._version, self.codes._version)
+        if t is not None and _has_own_version(t):
+            try:
+                self.versions = t._version, self.codes._version
+            except RuntimeError:  # tensors made in inference mode carry none
+                return
+            self.source = weakref.ref(t.untyped_storage())
 
     def _outlived(self, t):
         """Whether t is known to have been changed since the checkpoint was taken of it.  Versions
@@ -130,11 +146,13 @@ def _enqueue(name, device, *args):
         A._check(status, name)
 
 
-def _wrote(*tensors):
+def _wrote(tensors):
     """Mark what a call has written as changed, as torch's own writes are: autograd then refuses a
-    backward pass that would read a saved tensor's later contents.  (Tensors made in inference
-    mode carry no version.)"""
-    torch.autograd.graph.increment_version([t for t in tensors if t is not None and not t.is_inference()])
+    backward pass that would read a saved tensor's later contents."""
+    try:
+        torch._C._increment_version(tensors)
+    except RuntimeError:  # tensors made in inference mode carry no version outside of it
+        torch._C._increment_version([t for t in tensors if not t.is_inference()])
 
 
 def _has_own_version(t):
@@ -142,21 +160,11 @@ def _has_own_version(t):
     return not t._is_view() or t.numel() * t.element_size() == t.untyped_storage().nbytes()
 
 
-def _wrote_act(act):
-    """The arrays of a written checkpoint that get a new version.  Arrays that are parts of a larger
-    tensor share its version with all other parts, other checkpoints' among them: the fills of such
-    codes are counted beside their storage instead."""
-    if act is None:
-        return ()
-    if not _has_own_version(act.codes):
-        fills = act.codes.untyped_storage().__dict__.setdefault("_act8_fills", {})
-        at = act.codes.storage_offset()
-        fills[at] = fills.get(at, 0) + 1
-    return [t for t in (act.codes, act.scales) if _has_own_version(t)]
-
-
 def _fills(codes):
-    return codes.untyped_storage().__dict__.get("_act8_fills", {}).get(codes.storage_offset(), 0)
+    """How often checkpoint codes that are part of a larger tensor have been filled, as a list of one
+    number that all checkpoints in this place share."""
+    places = codes.untyped_storage().__dict__.setdefault("_act8_fills", {})
+    return places.setdefault(codes.storage_offset(), [0])
 
 
 def _at(t):
@@ -233,7 +241,7 @@ def act_pack(x, act):
     rows, cols, dev, stride = _input(x, "x", _DTYPES)
     arrays = _checkpoint(act, "act", rows, cols, dev)
     _enqueue("zs_act_pack", dev, x.data_ptr(), _DTYPES[x.dtype], stride, rows, cols, arrays)
-    _wrote(*_wrote_act(act))
+    _wrote(act._wrote())
     act._taken_of(x)
 
 
@@ -243,7 +251,7 @@ def act_unpack(act, out):
     rows, cols, dev, stride = _input(out, "out", _DTYPES)
     arrays = _checkpoint(act, "act", rows, cols, dev)
     _enqueue("zs_act_unpack", dev, arrays, rows, cols, out.data_ptr(), _DTYPES[out.dtype], stride)
-    _wrote(out)
+    _wrote((out,))
 
 
 def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, y8=None, h8=None, rstd=None):
@@ -262,7 +270,11 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, h=None, y=None, y8=None, h8=None
     ha = _checkpoint(h8, "h8", rows, cols, dev) if h8 is not None else None
     _enqueue("zs_rmsnorm", dev, x.data_ptr(), xs, _at(residual), rs, weight.data_ptr(), _DTYPES[dt], rows, cols, eps,
              _at(h), hs, _at(y), ys, ya, ha, _at(rstd))
-    _wrote(h, y, rstd, *_wrote_act(y8), *_wrote_act(h8))
+    wrote = [t for t in (h, y, rstd) if t is not None]
+    for act in (y8, h8):
+        if act is not None:
+            wrote += act._wrote()
+    _wrote(wrote)
     if y8 is not None:
         y8._taken_of(y)
     if h8 is not None:
@@ -296,7 +308,7 @@ def rmsnorm_backward(dy, saved, weight, rstd, dx, dh=None, dweight=None, base=No
     _enqueue("zs_rmsnorm_backward", dev, dy.data_ptr(), dys, _at(dh), dhs, _at(h), hs, h8, weight.data_ptr(),
              rstd.data_ptr(), _DTYPES[dt], rows, cols, dx.data_ptr(), dxs, _at(dweight),
              _DTYPES[dweight.dtype] if dweight is not None else A.ZS_FP32, _at(base), _at(workspace), size)
-    _wrote(dx, dweight, workspace if dweight is not None else None)
+    _wrote((dx, dweight, workspace) if dweight is not None else (dx,))
 
 
 def act_wgrad(x8, dy, dw, base=None, in_major=False, workspace=None):
@@ -317,7 +329,7 @@ def act_wgrad(x8, dy, dw, base=None, in_major=False, workspace=None):
     workspace, size = _workspace(workspace, A.zs_act_wgrad_workspace(rows, x8.cols, outs), dev)
     _enqueue("zs_act_wgrad", dev, arrays, rows, x8.cols, dy.data_ptr(), _DTYPES[dy.dtype], dys, outs, dw.data_ptr(),
              _DTYPES[dw.dtype], dws, int(bool(in_major)), _at(base), _at(workspace), size)
-    _wrote(dw, workspace)
+    _wrote((dw, workspace))
 
 
 # ------------------------------------------------------------------------------ autograd
@@ -472,14 +484,15 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, x8, grad_into):
         ctx.save_for_backward(weight, x8.codes, x8.scales)
-        ctx.code, ctx.cols, ctx.grad_into, ctx.fills = x8.code, x8.cols, grad_into, _fills(x8.codes)
+        ctx.code, ctx.cols, ctx.grad_into = x8.code, x8.cols, grad_into
+        ctx.fills = x8.fills[:] if x8.fills is not None else None
         return torch.nn.functional.linear(x, weight)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         weight, codes, scales = ctx.saved_tensors
-        if _fills(codes) > ctx.fills:
+        if ctx.fills is not None and _fills(codes)[0] > ctx.fills[0]:
             raise RuntimeError("the checkpoint of a linear layer's input, needed for its weight's gradient, has been "
                                "modified by an inplace operation: it was filled anew before backward")
         dx = dw = None
