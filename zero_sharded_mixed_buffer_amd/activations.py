@@ -39,15 +39,12 @@ class Act8:
     `scales`, uint8 [rows, groups of 32], both contiguous on one GPU; `code` is "e4m3" or
     "int8".  The arrays are the caller's, or Act8.empty's."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "code", "device", "arrays", "address", "marks", "fills", "source",
-                 "versions")
+    __slots__ = ("codes", "scales", "rows", "cols", "code", "device", "arrays", "address", "source")
 
     # `arrays` is the struct that the C calls read; every call writes the tensors' present
     # addresses into it, so that storage which was freed and allocated again is found.
-    # `marks` are the arrays that a write gives a new version, `fills` where fills are counted for
-    # codes that are part of a larger tensor.  `source` is the storage (weakly held) of the tensor
-    # that the checkpoint was last taken of, if that is known, `versions` that tensor's and the
-    # codes' version then
+    # `source` is what the checkpoint was last taken of, if that is known: a tensor's storage (weakly
+    # held), the tensor's version and the codes' version then
 
     def __init__(self, codes, scales, cols, code="e4m3"):
         if code not in CODES:
@@ -72,34 +69,37 @@ class Act8:
         self.device = device
         self.arrays = A.ActArrays(0, 0, CODES[code], 0)
         self.address = ctypes.addressof(self.arrays)
-        # Arrays that are parts of a larger tensor share its version with all other parts, other
-        # checkpoints' among them: the fills of such codes are counted beside their storage instead
-        self.marks = [t for t in (codes, scales) if _has_own_version(t)]
-        self.fills = None if self.marks and self.marks[0] is codes else _fills(codes)
-        self.source, self.versions = None, None
+        self.source = None
 
     def _wrote(self):
-        if self.fills is not None:
-            self.fills[0] += 1
-        return self.marks
+        """The arrays that a write gives a new version.  Those that are parts of a larger tensor share
+        its version with all other parts, other checkpoints' among them: the fills of such codes are
+        counted beside their storage instead."""
+        codes, scales = self.codes, self.scales
+        if not (codes._is_view() or scales._is_view()):
+            return [codes, scales]
+        own = [t for t in (codes, scales) if _has_own_version(t)]
+        if not own or own[0] is not codes:
+            _fills(codes)[0] += 1
+        return own
 
     def _taken_of(self, t):
-        self.source = None
-        if t is not None and _has_own_version(t):
-            try:
-                self.versions = t._version, self.codes._version
-            except RuntimeError:  # tensors made in inference mode carry none
-                return
-            self.source = weakref.ref(t.untyped_storage())
+        if t is None or not _has_own_version(t):
+            self.source = None
+            return
+        try:
+            self.source = weakref.ref(t.untyped_storage()), t._version, self.codes._version
+        except RuntimeError:  # tensors made in inference mode carry no version
+            self.source = None
 
     def _outlived(self, t):
         """Whether t is known to have been changed since the checkpoint was taken of it.  Versions
         only grow; a smaller one is counted apart (t.data's) and says nothing, and neither does that
         of a part of a larger tensor.  Codes written by other means since then may be anyone's."""
-        if self.source is None or t.is_inference() or self.source() is not t.untyped_storage():
+        if self.source is None or t.is_inference():
             return False
-        of_t, of_codes = self.versions
-        return t._version > of_t and self.codes._version == of_codes
+        storage, of_t, of_codes = self.source
+        return storage() is t.untyped_storage() and t._version > of_t and self.codes._version == of_codes
 
     @classmethod
     def empty(cls, rows, cols, code="e4m3", device="cuda"):
@@ -485,14 +485,14 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, weight, x8, grad_into):
         ctx.save_for_backward(weight, x8.codes, x8.scales)
         ctx.code, ctx.cols, ctx.grad_into = x8.code, x8.cols, grad_into
-        ctx.fills = x8.fills[:] if x8.fills is not None else None
+        ctx.fills = None if _has_own_version(x8.codes) else _fills(x8.codes)[0]
         return torch.nn.functional.linear(x, weight)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         weight, codes, scales = ctx.saved_tensors
-        if ctx.fills is not None and _fills(codes)[0] > ctx.fills[0]:
+        if ctx.fills is not None and _fills(codes)[0] > ctx.fills:
             raise RuntimeError("the checkpoint of a linear layer's input, needed for its weight's gradient, has been "
                                "modified by an inplace operation: it was filled anew before backward")
         dx = dw = None
