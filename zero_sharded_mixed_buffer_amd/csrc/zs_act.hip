@@ -315,7 +315,7 @@ template <int DT, int SAVED, int LPR, int V>
 __global__ __launch_bounds__(backward_block<LPR>(), 4) void k_rmsnorm_backward(NormBackwardArgs a) {
   constexpr int kBlock = backward_block<LPR>();
   constexpr int kRows = kBlock / LPR;
-    __shared__ float slot[2][kRows][LPR > 64 ? LPR / 64 : 1];
+  __shared__ float slot[2][kRows][LPR > 64 ? LPR / 64 : 1];
   __shared__ float fold[kRows > 1 ? kRows : 1][kRows > 1 ? LPR * V * 8 : 1];
   const int sub = threadIdx.x / LPR;
   const int lane = threadIdx.x % LPR;

@@ -8,11 +8,14 @@
 // four tokens of one column per lane and load.  The checkpoint's codes become 2-byte values
 // on the way into LDS, once per workgroup instead of once per wave.
 //
-// The matrix cores bound it: 2 * rows * cols * outs operations, at 1.15 to 1.25 PFLOP/s where
-// there are enough tiles (8192 tokens, 4096 -> 14336 with a bf16 base: 0.82 ms), what the library
-// reaches with operands laid out the way it likes best (1.23), and 1.3 times its rate on the
-// token-major operands that a backward pass has (0.90).  Codes in int8 need five vector
-// instructions for two values where e4m3 has one: 0.89 ms.
+// Where there are enough tiles the operations bound it, 2 * rows * cols * outs: 8192 tokens, 4096 ->
+// 14336 in 0.80 ms (1.20 PFLOP/s; 0.82 added to a bf16 base), 4096 -> 4096 in 0.22 ms (1.24).  In
+// turn with these, the library's bf16 product takes 0.94 ms (1.02) and 0.23 ms (1.21) on the
+// token-major operands that a backward pass has, 0.63 ms (1.53) and 0.17 ms (1.67) if both are
+// transposed before it.  The matrix cores are busy 60 % of the time and LDS 46 %, at the 1.7 to 1.8
+// GHz that the card holds under this load.  Codes in int8 need five vector instructions for two
+// values where e4m3 has one: 0.89 ms with a base.  With few tokens the launch's start and end are
+// most of it: 512 tokens, 4096 -> 14336 take 0.10 ms where the bytes take 0.04, 64 tokens 0.06.
 //
 // Where the tiles do not fill the last round of CUs, those of it are split over the tokens; each
 // split leaves its fp32 sums in the workspace and k_wgrad_fold adds them in token order: no
@@ -505,10 +508,9 @@ __global__ __launch_bounds__(kThreads) void k_wgrad_fold(WgradArgs g, WgradGrid 
 // ------------------------------------------------------------------ launch choices
 
 // Both tiles take stages of 64 tokens.  The large one, one workgroup of eight waves to a CU, reads
-// half as many operand bytes from L2 and LDS for each product: 8192 x 4096 -> 4096 in 219 us (1.25
-// PFLOP/s) against 303.  The small one, two workgroups of four waves to a CU, serves outputs with
-// few large tiles: 16384 x 1024 -> 1024 in 52 us against 54, 1024 x 1024 -> 4096 in 16 against 28
-// (four splits).  Four waves of 4 x 4 instructions, with less LDS traffic still, were slower than
+// half as many operand bytes from L2 and LDS for each product: 8192 x 4096 -> 4096 in 218 us against
+// 314.  The small one, two workgroups of four waves to a CU, serves outputs with few large tiles:
+// 1024 x 1024 -> 4096 in 18 us against 33, 16384 x 1024 -> 1024 in 50 against 53.  Four waves of 4 x 4 instructions, with less LDS traffic still, were slower than
 // eight of 4 x 2 (298 us against 270, both before the interleaving below was in place).
 using SmallTile = Tile<2, 2, 2, 2, 64, false>;  // 128 x 128
 using LargeTile = Tile<2, 4, 4, 2, 64, true>;   // 256 x 256
@@ -522,8 +524,11 @@ struct WgradChoice {
 // Time of a launch in microseconds as a function of the tile, the tiles done directly and the
 // splits of the others, from what the kernels measure on MI355X (256 CUs): a stage of the large
 // tile, one workgroup to a CU, and of the small one, one or two to a CU; the start and end of
-// a workgroup; the partial sums and the launch that folds them.  Within 10 % of the best choice
-// on fourteen shapes from 128 x 64 -> 256 to 8192 x 4096 -> 14336.
+// a workgroup; the partial sums and the launch that folds them.  Of fourteen sizes from 128 x 64 ->
+// 256 to 8192 x 4096 -> 14336 its choice is within 3 % of the best of all tiles and splits on twelve,
+// 6 % off at 16384 x 1024 -> 1024 (53.5 us, 50.2 are possible) and 20 % at 1024 x 1024 -> 1024 (19.9,
+// 16.6).  The bytes of dw and base are the same for every choice and not in it, so that it is no
+// estimate of a short batch's time.
 template <class TL>
 double launch_cost(int64_t tiles, int64_t direct, int64_t splits, int64_t stages) {
   auto rounds = [&](int64_t units, int64_t n) {
