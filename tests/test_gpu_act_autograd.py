@@ -254,3 +254,39 @@ def test_several_host_threads_finish(Z):
         t.join(30)
     assert not any(t.is_alive() for t in threads)
     assert count == [rounds] * 4 and not wrong
+
+
+# ------------------------------------------------------------------------------ recomputation
+
+@pytest.mark.parametrize("reentrant", [True, False])
+def test_recomputed_layers(Z, reentrant):
+    """A norm and two layers under torch's activation checkpointing, alone and one inside the other's
+    pass, with gradients in one flat buffer and by autograd: the same gradients as without."""
+    from torch.utils.checkpoint import checkpoint
+    x0 = _randn((4, 24, 64), BF16, 91)
+    nw = (1 + _randn((64,), BF16, 92, 0.1)).requires_grad_()
+    ws = [_randn((64, 64), BF16, 93 + i, 0.1).requires_grad_() for i in range(2)]
+    flat = torch.zeros(64 + 64 * 64, device="cuda")
+    intos = [flat[:64], flat[64:].view(64, 64)]
+    dy = _randn((4, 24, 64), BF16, 99)
+
+    def block(x):
+        out = Z.norm(x, nw, residual=x, y8="int8", grad_into=intos[0])
+        return Z.linear(Z.linear(out.y, ws[0], x8=out.y8, grad_into=intos[1]), ws[1]) + out.h
+
+    def run(wrapped):
+        flat.zero_()
+        ws[1].grad = None
+        x = x0.clone().requires_grad_()
+        y = x * 1
+        for _ in range(2):
+            y = checkpoint(block, y, use_reentrant=reentrant) if wrapped else block(y)
+        y.backward(dy)
+        assert nw.grad is None and ws[0].grad is None
+        return x.grad, ws[1].grad.clone(), flat.clone()
+
+    want = run(False)
+    for _ in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(run(True), want))
+    adds = flat.untyped_storage()._adds
+    assert adds.last is None and adds.under_way == 0
