@@ -89,8 +89,9 @@ zs_status zs_act_unpack(const zs_act* act, int64_t rows, int64_t cols, void* dst
  *       of h.
  *   rstd: NULL or rows fp32.
  * cols is 1 .. 16384.
- * Errors: ZS_EINVAL on NULL x or weight, no output at all, h and y or y8 and h8 in one place, a
- * bad dtype, size, stride, alignment or code, or an eps that is no normal fp32 number above 0. */
+ * Errors: ZS_EINVAL on NULL x or weight, no output at all, h and y or y8 and h8 in one place, h
+ * in place at another stride, a bad dtype, size, stride, alignment or code, or an eps that is
+ * no normal fp32 number above 0. */
 zs_status zs_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                      const void* weight, zs_dtype dtype, int64_t rows, int64_t cols, double eps, void* h,
                      int64_t h_stride, void* y, int64_t y_stride, const zs_act* y8, const zs_act* h8, float* rstd,
@@ -112,8 +113,8 @@ zs_status zs_rmsnorm_workspace(int64_t rows, int64_t cols, int64_t* bytes);
  *       dweight itself adds to what is there.  The sum is rounded once.
  *   workspace: device memory of at least zs_rmsnorm_workspace bytes, 16-byte aligned; may be NULL
  *       when dweight is.
- * Errors: ZS_EINVAL on NULL dy, weight, rstd or dx, neither or both of h and h8, a base without
- * dweight, a missing, small or misaligned workspace, or as zs_rmsnorm. */
+ * Errors: ZS_EINVAL on NULL dy, weight, rstd or dx, neither or both of h and h8, dx in place at
+ * another stride, a base without dweight, a missing, small or misaligned workspace, or as zs_rmsnorm. */
 zs_status zs_rmsnorm_backward(const void* dy, int64_t dy_stride, const void* dh, int64_t dh_stride, const void* h,
                               int64_t h_stride, const zs_act* h8, const void* weight, const float* rstd,
                               zs_dtype dtype, int64_t rows, int64_t cols, void* dx, int64_t dx_stride, void* dweight,

@@ -39,3 +39,15 @@ def test_norm_outputs_in_one_place_are_refused(Z):
     _refused(Z, "y8 and h8", Z.zs_rmsnorm, **call, y8=Z.ActArrays(P, 2 * P, 0, 0), h8=Z.ActArrays(P, 3 * P, 0, 0))
     _refused(Z, "y8 and h8", Z.zs_rmsnorm, **call, y8=Z.ActArrays(P, 2 * P, 0, 0), h8=Z.ActArrays(3 * P, 2 * P, 1, 0))
     _refused(Z, "h and y", Z.zs_rmsnorm, **call, h=2 * P, h_stride=64, y=2 * P, y_stride=64)
+
+
+def test_in_place_with_another_stride_is_refused(Z):
+    """h in x's or the residual's memory, dx in dy's or dh's, has to have its rows where theirs are; one
+    row lies the same way at any stride."""
+    call = dict(x=P, x_stride=64, residual=2 * P, residual_stride=96, weight=P, dtype=0, rows=4, cols=64, eps=1e-6)
+    _refused(Z, "in place", Z.zs_rmsnorm, **call, h=P, h_stride=96)
+    _refused(Z, "in place", Z.zs_rmsnorm, **call, h=2 * P, h_stride=64)
+    call = dict(dy=P, dy_stride=64, dh=2 * P, dh_stride=96, h=3 * P, h_stride=64, h8=None, weight=P, rstd=P, dtype=0, rows=4,
+                cols=64)
+    _refused(Z, "in place", Z.zs_rmsnorm_backward, **call, dx=P, dx_stride=96)
+    _refused(Z, "in place", Z.zs_rmsnorm_backward, **call, dx=2 * P, dx_stride=64)

@@ -936,6 +936,11 @@ zs_status check_matrix(const void* p, int64_t stride, int dt, int64_t rows, int6
   return ok();
 }
 
+// An output in an input's memory has to have its rows where the input's are.
+bool moved(const void* out, int64_t out_stride, const void* in, int64_t in_stride, int64_t rows) {
+  return rows > 1 && out != nullptr && out == in && out_stride != in_stride;
+}
+
 zs_status check_act(const zs_act* a, int64_t rows, const char* what) {
   if (a == nullptr) return fail(ZS_EINVAL, "%s is NULL", what);
   if (a->code != ZS_E4M3 && a->code != ZS_INT8) return fail(ZS_EINVAL, "%s: unknown code %d", what, a->code);
@@ -1038,6 +1043,8 @@ extern "C" zs_status zs_rmsnorm(const void* x, int64_t x_stride, const void* res
   if (!grad_aligned(rstd, ZS_FP32)) return fail(ZS_EINVAL, "rstd must be aligned to its elements");
   if (h == nullptr && y == nullptr && y8 == nullptr && h8 == nullptr && rstd == nullptr)
     return fail(ZS_EINVAL, "no output: h, y, y8, h8 and rstd are all NULL");
+  if (moved(h, h_stride, x, x_stride, rows) || moved(h, h_stride, residual, residual_stride, rows))
+    return fail(ZS_EINVAL, "h in place of x or residual must have its stride");
   if (rows > 0 && h != nullptr && h == y) return fail(ZS_EINVAL, "h and y are the same memory");
   if (rows > 0 && y8 != nullptr && h8 != nullptr && (y8->codes == h8->codes || y8->scales == h8->scales))
     return fail(ZS_EINVAL, "y8 and h8 are the same memory");
@@ -1086,6 +1093,8 @@ extern "C" zs_status zs_rmsnorm_backward(const void* dy, int64_t dy_stride, cons
   if (st != ZS_OK) return st;
   if ((h == nullptr) == (h8 == nullptr) && (rows > 0 || h != nullptr))
     return fail(ZS_EINVAL, "exactly one of h and h8 must be given");
+  if (moved(dx, dx_stride, dy, dy_stride, rows) || moved(dx, dx_stride, dh, dh_stride, rows))
+    return fail(ZS_EINVAL, "dx in place of dy or dh must have its stride");
   if (weight == nullptr || (rstd == nullptr && rows > 0)) return fail(ZS_EINVAL, "weight and rstd must not be NULL");
   if (!grad_aligned(weight, dtype)) return fail(ZS_EINVAL, "weight must be aligned to its elements");
   if (!grad_aligned(rstd, ZS_FP32)) return fail(ZS_EINVAL, "rstd must be aligned to its elements");
