@@ -59,6 +59,11 @@ class ActArrays(ctypes.Structure):
     _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("code", c_int32), ("reserved", c_int32)]
 
 
+class Weight8Arrays(ctypes.Structure):
+    """zs_weight8: an 8-bit weight's arrays."""
+    _fields_ = [("codes", c_void_p), ("codes_t", c_void_p), ("scales", c_void_p)]
+
+
 _lib = None
 
 _SIGS = {
@@ -106,6 +111,20 @@ _SIGS = {
     "zs_act_wgrad_workspace": [c_int64, c_int64, c_int64, c_void_p],
     "zs_act_wgrad": [c_void_p, c_int64, c_int64, c_void_p, c_int32, c_int64, c_int64, c_void_p, c_int32, c_int64,
                      c_int32, c_void_p, c_void_p, c_int64, c_void_p],
+    "zs_weight8_size": [c_int64, c_int64, c_void_p, c_void_p, c_void_p],
+    "zs_weight8_pack": [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p],
+    "zs_product8": [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int32, c_void_p, c_int32, c_int64, c_void_p],
+    "zs_expert_product": [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int32, c_void_p, c_int32, c_int64, c_int64,
+                          c_int64, c_int32, c_void_p, c_int64, c_int32, c_void_p],
+    "zs_expert_wgrad": [c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p, c_int32, c_int64, c_int64, c_int64,
+                        c_void_p, c_int32, c_int64, c_int64, c_int32, c_void_p, c_void_p],
+    "zs_route_workspace": [c_int64, c_int32, c_void_p],
+    "zs_route": [c_void_p, c_int32, c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p],
+    "zs_expert_gather": [c_void_p, c_int64, c_int32, c_void_p, c_int64, c_int32, c_int64, c_void_p, c_int64, c_void_p],
+    "zs_expert_combine": [c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_int64, c_int32, c_int64, c_void_p, c_int64,
+                          c_void_p],
+    "zs_expert_combine_backward": [c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_int64, c_int32,
+                                   c_int64, c_void_p, c_int64, c_void_p, c_void_p],
     "zs_offload_adamw_step": [c_void_p, c_void_p, c_int32, c_void_p, POINTER(AdamwHParams), c_void_p, c_void_p,
                               c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p],
 }
@@ -504,3 +523,80 @@ def zs_act_wgrad(x8, rows, cols, dy, dy_dtype, dy_stride, outs, dw, dw_dtype, dw
                               _dptr(dw, "dw", w), dtype_code(dw_dtype), dw_stride, int(bool(in_major)),
                               _dptr(base, "base", w), _dptr(workspace, "workspace", w), workspace_bytes,
                               _stream(stream)), w)
+
+
+# ---------------------------------------------------------------------------- products and experts
+# (include/zs_product.h; an 8-bit weight argument is a Weight8Arrays)
+
+def zs_weight8_size(outs, cols):
+    """Returns (codes_bytes, codes_t_bytes, scales_bytes) of an outs x cols weight."""
+    a, b, c = c_int64(), c_int64(), c_int64()
+    _check(lib().zs_weight8_size(outs, cols, ctypes.addressof(a), ctypes.addressof(b), ctypes.addressof(c)),
+           "zs_weight8_size")
+    return a.value, b.value, c.value
+
+
+def zs_weight8_pack(src, src_dtype, src_stride, outs, cols, w8, stream=None):
+    w = "zs_weight8_pack"
+    _check(lib().zs_weight8_pack(_dptr(src, "src", w), dtype_code(src_dtype), src_stride, outs, cols, _act(w8),
+                                 _stream(stream)), w)
+
+
+def zs_product8(x8, rows, w8, outs, cols, transposed, y, y_dtype, y_stride, stream=None):
+    w = "zs_product8"
+    _check(lib().zs_product8(_act(x8), rows, _act(w8), outs, cols, int(bool(transposed)), _dptr(y, "y", w),
+                             dtype_code(y_dtype), y_stride, _stream(stream)), w)
+
+
+def zs_expert_product(x, x_stride, weight, w_stride, w_expert_stride, dtype, ends, experts, rows, cols, outs, in_major, y,
+                      y_stride, zero_rest=False, stream=None):
+    w = "zs_expert_product"
+    _check(lib().zs_expert_product(_dptr(x, "x", w), x_stride, _dptr(weight, "w", w), w_stride, w_expert_stride,
+                                   dtype_code(dtype), _dptr(ends, "ends", w), experts, rows, cols, outs,
+                                   int(bool(in_major)), _dptr(y, "y", w), y_stride, int(bool(zero_rest)),
+                                   _stream(stream)), w)
+
+
+def zs_expert_wgrad(x, x_stride, dy, dy_stride, dtype, ends, experts, rows, cols, outs, dw, dw_dtype, dw_stride,
+                    dw_expert_stride, in_major=False, base=None, stream=None):
+    w = "zs_expert_wgrad"
+    _check(lib().zs_expert_wgrad(_dptr(x, "x", w), x_stride, _dptr(dy, "dy", w), dy_stride, dtype_code(dtype),
+                                 _dptr(ends, "ends", w), experts, rows, cols, outs, _dptr(dw, "dw", w),
+                                 dtype_code(dw_dtype), dw_stride, dw_expert_stride, int(bool(in_major)),
+                                 _dptr(base, "base", w), _stream(stream)), w)
+
+
+def zs_route_workspace(slots, experts):
+    """Bytes of zs_route's workspace."""
+    n = c_int64()
+    _check(lib().zs_route_workspace(slots, experts, ctypes.addressof(n)), "zs_route_workspace")
+    return n.value
+
+
+def zs_route(ids, id_bytes, slots, experts, ends, slot, place, workspace, workspace_bytes, stream=None):
+    w = "zs_route"
+    _check(lib().zs_route(_dptr(ids, "ids", w), id_bytes, slots, experts, _dptr(ends, "ends", w), _dptr(slot, "slot", w),
+                          _dptr(place, "place", w), _dptr(workspace, "workspace", w), workspace_bytes,
+                          _stream(stream)), w)
+
+
+def zs_expert_gather(x, x_stride, dtype, slot, tokens, choices, cols, out, out_stride, stream=None):
+    w = "zs_expert_gather"
+    _check(lib().zs_expert_gather(_dptr(x, "x", w), x_stride, dtype_code(dtype), _dptr(slot, "slot", w), tokens, choices,
+                                  cols, _dptr(out, "out", w), out_stride, _stream(stream)), w)
+
+
+def zs_expert_combine(y, y_stride, dtype, place, weights, tokens, choices, cols, out, out_stride, stream=None):
+    w = "zs_expert_combine"
+    _check(lib().zs_expert_combine(_dptr(y, "y", w), y_stride, dtype_code(dtype), _dptr(place, "place", w),
+                                   _dptr(weights, "weights", w), tokens, choices, cols, _dptr(out, "out", w), out_stride,
+                                   _stream(stream)), w)
+
+
+def zs_expert_combine_backward(dout, dout_stride, y, y_stride, dtype, slot, weights, tokens, choices, cols, dy=None,
+                               dy_stride=0, dweights=None, stream=None):
+    w = "zs_expert_combine_backward"
+    _check(lib().zs_expert_combine_backward(_dptr(dout, "dout", w), dout_stride, _dptr(y, "y", w), y_stride,
+                                            dtype_code(dtype), _dptr(slot, "slot", w), _dptr(weights, "weights", w),
+                                            tokens, choices, cols, _dptr(dy, "dy", w), dy_stride,
+                                            _dptr(dweights, "dweights", w), _stream(stream)), w)

@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libzs.so")
 
-SOURCES = ["zs_abi.cpp", "zs_kernels.hip", "zs_probe.hip", "zs_act.hip", "zs_wgrad.hip"]
+SOURCES = ["zs_abi.cpp", "zs_kernels.hip", "zs_probe.hip", "zs_act.hip", "zs_wgrad.hip", "zs_product.hip",
+           "zs_expert.hip"]
 HOST_SOURCES = ["zs_host.cpp", "zs_plan.cpp"]  # plain C++ (host step, planner), built by the host compiler
 HEADERS = ["zs_internal.h", "zs_host.h", "zs_plan.h", "zs_act_dev.h"]
 

@@ -16,6 +16,7 @@
 
 #include "zs.h"
 #include "zs_act.h"
+#include "zs_product.h"
 #include "zs_host.h"
 #include "zs_probe.h"
 #include "zs_internal.h"
@@ -1180,4 +1181,333 @@ extern "C" zs_status zs_act_wgrad(const zs_act* x8, int64_t rows, int64_t cols, 
   a.in_major = in_major != 0;
   hipError_t e = zs::launch_wgrad(a, as_stream(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "launching the weight gradient");
+}
+
+// ---------------------------------------------------------------------------- products and experts
+
+namespace {
+
+zs_status check_weight8_sizes(int64_t outs, int64_t cols) {
+  zs_status st = check_sizes(outs, cols);
+  if (st != ZS_OK) return st;
+  if (outs < 1) return fail(ZS_EINVAL, "outs must be positive");
+  if (outs > (int64_t(1) << 30) || cols > (int64_t(1) << 30) ||
+      ((outs + 127) / 128) * ((cols + 127) / 128) > zs::kProductMaxUnits)
+    return fail(ZS_EINVAL, "outs x cols exceeds one launch");
+  return ok();
+}
+
+zs_status check_weight8(const zs_weight8* w, bool turned) {
+  if (w == nullptr) return fail(ZS_EINVAL, "w8 is NULL");
+  if (w->codes == nullptr || w->scales == nullptr) return fail(ZS_EINVAL, "w8: codes or scales is NULL");
+  if (turned && w->codes_t == nullptr) return fail(ZS_EINVAL, "w8: the transposed codes are missing");
+  if (!aligned16(w->codes) || !aligned16(w->codes_t)) return fail(ZS_EINVAL, "w8: codes must be 16-byte aligned");
+  return ok();
+}
+
+zs_status check_experts(const int32_t* ends, int32_t experts, int64_t rows, int64_t cols, int64_t outs) {
+  if (experts < 1 || experts > zs::kMaxExperts)
+    return fail(ZS_EINVAL, "experts must be within 1 .. %lld", static_cast<long long>(zs::kMaxExperts));
+  if (ends == nullptr) return fail(ZS_EINVAL, "ends is NULL");
+  if ((reinterpret_cast<uintptr_t>(ends) & 3) != 0) return fail(ZS_EINVAL, "ends must be aligned to its elements");
+  zs_status st = check_sizes(rows, cols);
+  if (st == ZS_OK) st = check_sizes(rows, outs);
+  if (st == ZS_OK) st = check_sizes(outs, cols);
+  if (st != ZS_OK) return st;
+  if (rows > zs::kMaxSlots) return fail(ZS_EINVAL, "rows exceeds 2^31 - 4096");
+  if (cols > (int64_t(1) << 30) || outs > (int64_t(1) << 30)) return fail(ZS_EINVAL, "cols and outs are at most 2^30");
+  return ok();
+}
+
+// The experts' matrices rows x cols, `apart` elements from one to the next.
+zs_status check_expert_matrices(const void* p, int64_t stride, int64_t apart, int32_t experts, int dt, int64_t rows,
+                                int64_t cols, bool written, const char* what) {
+  zs_status st = check_matrix(p, stride, dt, rows, cols, what);
+  if (st != ZS_OK) return st;
+  if (experts > 1 && (apart < 0 || apart > kMaxBytes / 4 / experts))
+    return fail(ZS_EINVAL, "%s: the expert stride is out of range", what);
+  const int64_t extent = rows > 0 ? (rows - 1) * (rows > 1 ? stride : 0) + cols : 0;
+  if (written && experts > 1 && apart < extent) return fail(ZS_EINVAL, "%s: the experts' matrices overlap", what);
+  return ok();
+}
+
+zs_status check_routing(int64_t tokens, int32_t choices, int64_t cols, int dt) {
+  if (!is_grad_dtype(dt)) return fail(ZS_EINVAL, "dtype must be bf16, fp16 or fp32");
+  if (choices < 1) return fail(ZS_EINVAL, "choices must be positive");
+  zs_status st = check_sizes(tokens, cols);
+  if (st != ZS_OK) return st;
+  if (tokens > zs::kMaxSlots / choices) return fail(ZS_EINVAL, "tokens x choices exceeds 2^31 - 4096");
+  // a launch holds fewer than 2^32 threads, up to 256 for a row
+  if (tokens * choices > zs::kProductMaxUnits * 2 && cols > 64)
+    return fail(ZS_EINVAL, "tokens x choices exceeds one launch");
+  return check_sizes(tokens * choices, cols);
+}
+
+zs_status check_words(const void* p, int64_t n, const char* what) {
+  if (p == nullptr && n > 0) return fail(ZS_EINVAL, "%s is NULL", what);
+  if ((reinterpret_cast<uintptr_t>(p) & 3) != 0) return fail(ZS_EINVAL, "%s must be aligned to its elements", what);
+  return ok();
+}
+
+}  // namespace
+
+extern "C" zs_status zs_weight8_size(int64_t outs, int64_t cols, int64_t* codes_bytes, int64_t* codes_t_bytes,
+                                     int64_t* scales_bytes) {
+  if (codes_bytes == nullptr || codes_t_bytes == nullptr || scales_bytes == nullptr)
+    return fail(ZS_EINVAL, "an output is NULL");
+  zs_status st = check_weight8_sizes(outs, cols);
+  if (st != ZS_OK) return st;
+  const int64_t po = round_up(outs, zs::kWeightBlock), pc = round_up(cols, zs::kWeightBlock);
+  *codes_bytes = outs * pc;
+  *codes_t_bytes = cols * po;
+  *scales_bytes = (po / zs::kWeightBlock) * (pc / zs::kWeightBlock);
+  return ok();
+}
+
+extern "C" zs_status zs_weight8_pack(const void* src, zs_dtype src_dtype, int64_t src_stride, int64_t outs, int64_t cols,
+                                     const zs_weight8* w8, void* stream) {
+  const TraceRange trace("zs_weight8_pack");
+  if (!is_grad_dtype(src_dtype)) return fail(ZS_EINVAL, "src_dtype must be bf16, fp16 or fp32");
+  zs_status st = check_weight8_sizes(outs, cols);
+  if (st == ZS_OK) st = check_matrix(src, src_stride, src_dtype, outs, cols, "src");
+  if (st == ZS_OK) st = check_weight8(w8, false);
+  if (st != ZS_OK) return st;
+  hipError_t e = zs::launch_weight8(src, src_dtype, src_stride, outs, cols, static_cast<uint8_t*>(w8->codes),
+                                    static_cast<uint8_t*>(w8->codes_t), static_cast<uint8_t*>(w8->scales), as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the 8-bit weight");
+}
+
+extern "C" zs_status zs_product8(const zs_act* x8, int64_t rows, const zs_weight8* w8, int64_t outs, int64_t cols,
+                                 int32_t transposed, void* y, zs_dtype y_dtype, int64_t y_stride, void* stream) {
+  const TraceRange trace("zs_product8");
+  if (!is_half_dtype(y_dtype)) return fail(ZS_EINVAL, "y_dtype must be bf16 or fp16");
+  zs_status st = check_weight8_sizes(outs, cols);
+  const int64_t k = transposed ? outs : cols, n = transposed ? cols : outs;
+  if (st == ZS_OK) st = check_sizes(rows, k);
+  if (st == ZS_OK) st = check_act(x8, rows, "x8");
+  if (st == ZS_OK && x8->code != ZS_E4M3) return fail(ZS_EINVAL, "x8 must hold e4m3 codes");
+  if (st == ZS_OK) st = check_weight8(w8, transposed != 0);
+  if (st == ZS_OK) st = check_matrix(y, y_stride, y_dtype, rows, n, "y");
+  if (st != ZS_OK) return st;
+  zs::ProductArgs a{};
+  a.a = x8->codes;
+  a.a_scales = static_cast<const uint8_t*>(x8->scales);
+  a.b = transposed ? w8->codes_t : w8->codes;
+  a.b_scales = static_cast<const uint8_t*>(w8->scales);
+  a.c = y;
+  a.m = rows;
+  a.n = n;
+  a.k = k;
+  a.a_padded = a.a_stride = zs::act_padded(k);
+  a.b_padded = a.b_stride = round_up(k, zs::kWeightBlock);
+  a.b_blocks = round_up(cols, zs::kWeightBlock) / zs::kWeightBlock;
+  a.b_turned = transposed != 0;
+  a.c_stride = y_stride;
+  a.c_dt = y_dtype;
+  a.groups = 1;
+  if (rows > zs::kMaxSlots || zs::product_units(a, false, zs::kProductTile, zs::kProductTile) > zs::kProductMaxUnits)
+    return fail(ZS_EINVAL, "rows x outs exceeds one launch");
+  if (rows == 0) return ok();
+  hipError_t e = zs::launch_product8(a, as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the 8-bit product");
+}
+
+extern "C" zs_status zs_expert_product(const void* x, int64_t x_stride, const void* w, int64_t w_stride,
+                                       int64_t w_expert_stride, zs_dtype dtype, const int32_t* ends, int32_t experts,
+                                       int64_t rows, int64_t cols, int64_t outs, int32_t in_major, void* y,
+                                       int64_t y_stride, int32_t zero_rest, void* stream) {
+  const TraceRange trace("zs_expert_product");
+  if (!is_half_dtype(dtype)) return fail(ZS_EINVAL, "dtype must be bf16 or fp16");
+  zs_status st = check_experts(ends, experts, rows, cols, outs);
+  if (st == ZS_OK) st = check_matrix(x, x_stride, dtype, rows, cols, "x");
+  if (st == ZS_OK)
+    st = check_expert_matrices(w, w_stride, w_expert_stride, experts, dtype, in_major ? cols : outs, in_major ? outs : cols,
+                               false, "w");
+  if (st == ZS_OK) st = check_matrix(y, y_stride, dtype, rows, outs, "y");
+  if (st != ZS_OK) return st;
+  zs::ProductArgs a{};
+  a.a = x;
+  a.b = w;
+  a.c = y;
+  a.ends = ends;
+  a.groups = experts;
+  a.m = rows;
+  a.n = outs;
+  a.k = cols;
+  a.a_stride = x_stride;
+  a.b_stride = w_stride;
+  a.b_group = experts > 1 ? w_expert_stride : 0;
+  a.c_stride = y_stride;
+  a.c_dt = dtype;
+  a.zero_rest = zero_rest != 0;
+  if (zs::product_units(a, false, zs::kProductTile, zs::kProductTile) > zs::kProductMaxUnits)
+    return fail(ZS_EINVAL, "rows x outs exceeds one launch");
+  if (rows == 0) return ok();
+  hipError_t e = zs::launch_expert_product(a, dtype, in_major != 0, as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the experts' products");
+}
+
+extern "C" zs_status zs_expert_wgrad(const void* x, int64_t x_stride, const void* dy, int64_t dy_stride, zs_dtype dtype,
+                                     const int32_t* ends, int32_t experts, int64_t rows, int64_t cols, int64_t outs,
+                                     void* dw, zs_dtype dw_dtype, int64_t dw_stride, int64_t dw_expert_stride,
+                                     int32_t in_major, const void* base, void* stream) {
+  const TraceRange trace("zs_expert_wgrad");
+  if (!is_half_dtype(dtype)) return fail(ZS_EINVAL, "dtype must be bf16 or fp16");
+  if (!is_grad_dtype(dw_dtype)) return fail(ZS_EINVAL, "dw_dtype must be bf16, fp16 or fp32");
+  if (dw_dtype != dtype && dw_dtype != ZS_FP32) return fail(ZS_EUNSUPPORTED, "dw_dtype must be dtype or fp32");
+  zs_status st = check_experts(ends, experts, rows, cols, outs);
+  const int64_t dw_rows = in_major ? cols : outs, dw_cols = in_major ? outs : cols;
+  if (st == ZS_OK) st = check_matrix(x, x_stride, dtype, rows, cols, "x");
+  if (st == ZS_OK) st = check_matrix(dy, dy_stride, dtype, rows, outs, "dy");
+  if (st == ZS_OK)
+    st = check_expert_matrices(dw, dw_stride, dw_expert_stride, experts, dw_dtype, dw_rows, dw_cols, true, "dw");
+  if (st == ZS_OK && base != nullptr)
+    st = check_expert_matrices(base, dw_stride, dw_expert_stride, experts, dw_dtype, dw_rows, dw_cols, true, "base");
+  if (st != ZS_OK) return st;
+  zs::ProductArgs a{};
+  a.a = in_major ? x : dy;
+  a.b = in_major ? dy : x;
+  a.c = dw;
+  a.base = base;
+  a.ends = ends;
+  a.groups = experts;
+  a.m = dw_rows;
+  a.n = dw_cols;
+  a.k = rows;
+  a.a_stride = in_major ? x_stride : dy_stride;
+  a.b_stride = in_major ? dy_stride : x_stride;
+  a.c_stride = dw_stride;
+  a.c_group = experts > 1 ? dw_expert_stride : 0;
+  a.c_dt = dw_dtype;
+  if (dw_rows == 0) return ok();
+  if (zs::product_units(a, true, zs::kProductTile, zs::kProductTile) > zs::kProductMaxUnits)
+    return fail(ZS_EINVAL, "experts x outs x cols exceeds one launch");
+  hipError_t e = zs::launch_expert_wgrad(a, dtype, as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the experts' weight gradients");
+}
+
+namespace {
+
+zs_status check_slots(int64_t slots, int32_t experts) {
+  if (slots < 0 || slots > zs::kMaxSlots) return fail(ZS_EINVAL, "slots must be within 0 .. 2^31 - 4096");
+  if (experts < 1 || experts > zs::kMaxExperts)
+    return fail(ZS_EINVAL, "experts must be within 1 .. %lld", static_cast<long long>(zs::kMaxExperts));
+  return ok();
+}
+
+}  // namespace
+
+extern "C" zs_status zs_route_workspace(int64_t slots, int32_t experts, int64_t* bytes) {
+  if (bytes == nullptr) return fail(ZS_EINVAL, "bytes is NULL");
+  zs_status st = check_slots(slots, experts);
+  if (st != ZS_OK) return st;
+  *bytes = zs::route_workspace(slots, experts);
+  return ok();
+}
+
+extern "C" zs_status zs_route(const void* ids, int32_t id_bytes, int64_t slots, int32_t experts, int32_t* ends,
+                              int32_t* slot, int32_t* place, void* workspace, int64_t workspace_bytes, void* stream) {
+  const TraceRange trace("zs_route");
+  zs_status st = check_slots(slots, experts);
+  if (st != ZS_OK) return st;
+  if (id_bytes != 4 && id_bytes != 8) return fail(ZS_EINVAL, "id_bytes must be 4 or 8");
+  if ((ids == nullptr && slots > 0) || (reinterpret_cast<uintptr_t>(ids) & (id_bytes - 1)) != 0)
+    return fail(ZS_EINVAL, "ids is NULL or not aligned to its elements");
+  st = check_words(ends, experts, "ends");
+  if (st == ZS_OK) st = check_words(slot, slots, "slot");
+  if (st == ZS_OK) st = check_words(place, slots, "place");
+  if (st == ZS_OK) st = check_workspace(workspace, workspace_bytes, zs::route_workspace(slots, experts));
+  if (st != ZS_OK) return st;
+  zs::RouteArgs a{};
+  a.ids = ids;
+  a.ends = ends;
+  a.slot = slot;
+  a.place = place;
+  a.slots = slots;
+  a.experts = experts;
+  a.id_bytes = id_bytes;
+  hipError_t e = zs::launch_route(a, workspace, as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the routing");
+}
+
+extern "C" zs_status zs_expert_gather(const void* x, int64_t x_stride, zs_dtype dtype, const int32_t* slot, int64_t tokens,
+                                      int32_t choices, int64_t cols, void* out, int64_t out_stride, void* stream) {
+  const TraceRange trace("zs_expert_gather");
+  zs_status st = check_routing(tokens, choices, cols, dtype);
+  const int64_t rows = st == ZS_OK ? tokens * choices : 0;
+  if (st == ZS_OK) st = check_matrix(x, x_stride, dtype, tokens, cols, "x");
+  if (st == ZS_OK) st = check_words(slot, rows, "slot");
+  if (st == ZS_OK) st = check_matrix(out, out_stride, dtype, rows, cols, "out");
+  if (st != ZS_OK) return st;
+  zs::RowsArgs a{};
+  a.x = x;
+  a.out = out;
+  a.slot = slot;
+  a.rows = rows;
+  a.cols = cols;
+  a.x_stride = x_stride;
+  a.out_stride = out_stride;
+  a.choices = choices;
+  hipError_t e = zs::launch_expert_gather(a, dtype, as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the gather");
+}
+
+extern "C" zs_status zs_expert_combine(const void* y, int64_t y_stride, zs_dtype dtype, const int32_t* place,
+                                       const float* weights, int64_t tokens, int32_t choices, int64_t cols, void* out,
+                                       int64_t out_stride, void* stream) {
+  const TraceRange trace("zs_expert_combine");
+  zs_status st = check_routing(tokens, choices, cols, dtype);
+  const int64_t rows = st == ZS_OK ? tokens * choices : 0;
+  if (st == ZS_OK) st = check_matrix(y, y_stride, dtype, rows, cols, "y");
+  if (st == ZS_OK) st = check_words(place, rows, "place");
+  if (st == ZS_OK) st = check_words(weights, 0, "weights");
+  if (st == ZS_OK) st = check_matrix(out, out_stride, dtype, tokens, cols, "out");
+  if (st != ZS_OK) return st;
+  zs::RowsArgs a{};
+  a.x = y;
+  a.out = out;
+  a.place = place;
+  a.weights = weights;
+  a.rows = rows;
+  a.cols = cols;
+  a.x_stride = y_stride;
+  a.out_stride = out_stride;
+  a.choices = choices;
+  hipError_t e = zs::launch_expert_combine(a, dtype, as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the combination");
+}
+
+extern "C" zs_status zs_expert_combine_backward(const void* dout, int64_t dout_stride, const void* y, int64_t y_stride,
+                                                zs_dtype dtype, const int32_t* slot, const float* weights, int64_t tokens,
+                                                int32_t choices, int64_t cols, void* dy, int64_t dy_stride,
+                                                float* dweights, void* stream) {
+  const TraceRange trace("zs_expert_combine_backward");
+  zs_status st = check_routing(tokens, choices, cols, dtype);
+  const int64_t rows = st == ZS_OK ? tokens * choices : 0;
+  if (st != ZS_OK) return st;
+  if (rows > 0 && dy == nullptr && dweights == nullptr) return fail(ZS_EINVAL, "no output is given");
+  st = check_matrix(dout, dout_stride, dtype, tokens, cols, "dout");
+  if (st == ZS_OK && dweights != nullptr) st = check_matrix(y, y_stride, dtype, rows, cols, "y");
+  if (st == ZS_OK) st = check_words(slot, rows, "slot");
+  if (st == ZS_OK) st = check_words(weights, 0, "weights");
+  if (st == ZS_OK) st = check_words(dweights, 0, "dweights");
+  if (st == ZS_OK && dy != nullptr) st = check_matrix(dy, dy_stride, dtype, rows, cols, "dy");
+  if (st != ZS_OK) return st;
+  if (dweights != nullptr && moved(dy, dy_stride, y, y_stride, rows))
+    return fail(ZS_EINVAL, "dy is in place of y at another stride");
+  zs::CombineBackwardArgs a{};
+  a.dout = dout;
+  a.y = y;
+  a.slot = slot;
+  a.weights = weights;
+  a.dy = dy;
+  a.dweights = dweights;
+  a.rows = rows;
+  a.cols = cols;
+  a.dout_stride = dout_stride;
+  a.y_stride = y_stride;
+  a.dy_stride = dy_stride;
+  a.choices = choices;
+  hipError_t e = zs::launch_expert_combine_backward(a, dtype, as_stream(stream));
+  return e == hipSuccess ? ok() : hip_fail(e, "launching the combination's backward");
 }

@@ -191,4 +191,73 @@ struct WgradArgs {
 int64_t wgrad_workspace(int64_t rows, int64_t cols, int64_t outs);  // bytes; < 0: past one launch
 hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s);
 
+// Products (zs_product.hip): c[m][n] = base + sum over k of a[m][k] * b[n][k], over groups of m
+// (each with a b of its own) or of k (each with a c of its own).  Strides in elements.
+struct ProductArgs {
+  const void* a;
+  const void* b;
+  void* c;
+  const void* base;         // or null
+  const uint8_t* a_scales;  // of 8-bit operands
+  const uint8_t* b_scales;
+  const int32_t* ends;  // the groups' ends, or null: one group
+  int64_t m, n, k;
+  int64_t a_stride, b_stride, c_stride, b_group, c_group;
+  int64_t a_padded, b_padded;  // codes of a row of 8-bit operands
+  int64_t b_blocks;            // scales of a row of blocks
+  int32_t groups;
+  int32_t c_dt;
+  bool b_turned;   // b holds the transposed codes
+  bool zero_rest;  // rows behind the last group become zeros
+};
+// Workgroups of a launch with such tiles.
+int64_t product_units(const ProductArgs& a, bool sum_groups, int64_t tile_m, int64_t tile_n);
+constexpr int64_t kProductMaxUnits = (int64_t(1) << 23) - 64;  // workgroups of 512 threads of one launch
+constexpr int64_t kProductTile = 128;                          // the smallest tile's sides
+hipError_t launch_product8(const ProductArgs& a, hipStream_t s);
+hipError_t launch_expert_product(const ProductArgs& a, int dt, bool in_major, hipStream_t s);
+hipError_t launch_expert_wgrad(const ProductArgs& a, int dt, hipStream_t s);
+constexpr int64_t kWeightBlock = 128;
+hipError_t launch_weight8(const void* src, int dt, int64_t stride, int64_t outs, int64_t cols, uint8_t* codes, uint8_t* codes_t,
+                          uint8_t* scales, hipStream_t s);
+
+// Routing (zs_expert.hip).
+constexpr int kRouteChunk = 1024;     // choices of a workgroup
+constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxSlots = (int64_t(1) << 31) - 4096;
+struct RouteArgs {
+  const void* ids;
+  int32_t* ends;
+  int32_t* slot;
+  int32_t* place;
+  int32_t* totals;  // workspace: experts + 1, then as many for each chunk
+  int32_t* counts;
+  int64_t slots, chunks;
+  int32_t experts, id_bytes, bits;
+};
+int64_t route_workspace(int64_t slots, int experts);
+hipError_t launch_route(RouteArgs a, void* workspace, hipStream_t s);
+struct RowsArgs {
+  const void* x;
+  void* out;
+  const int32_t* slot;   // the gather's
+  const int32_t* place;  // the combination's
+  const float* weights;  // or null: ones
+  int64_t rows, cols, x_stride, out_stride;  // rows: tokens * choices
+  int32_t choices, rows_log2;
+};
+hipError_t launch_expert_gather(RowsArgs a, int dt, hipStream_t s);
+hipError_t launch_expert_combine(RowsArgs a, int dt, hipStream_t s);
+struct CombineBackwardArgs {
+  const void* dout;
+  const void* y;         // or null: no dweights
+  const int32_t* slot;
+  const float* weights;  // or null: ones
+  void* dy;              // or null
+  float* dweights;       // or null
+  int64_t rows, cols, dout_stride, y_stride, dy_stride;
+  int32_t choices, rows_log2;
+};
+hipError_t launch_expert_combine_backward(CombineBackwardArgs a, int dt, hipStream_t s);
+
 }  // namespace zs

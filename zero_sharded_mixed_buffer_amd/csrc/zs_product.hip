@@ -1,0 +1,697 @@
+// gfx950 kernels of the matrix products: a layer's products with an 8-bit weight (zs_product8), and
+// the experts' products over groups of rows (zs_expert_product, zs_expert_wgrad):
+//   c[m][n] = sum over k of a[m][k] * b[n][k]
+// on the matrix cores, summed in fp32.
+//
+// An operand lies in memory with consecutive k (rows of m or n, "by rows"), or with consecutive m
+// or n (rows of k, "by k").  A stage of the sum is 128 bytes of every row: 64 values of k in 16
+// bits, 128 in 8.  Stages go from memory straight into LDS, 16 bytes to a lane, two buffers in
+// turn.  Such a load puts a wave's 64 pieces one after the other, so rows cannot be padded against
+// bank conflicts: instead a lane fetches another piece of its row than its place says.  Operands by
+// rows are read back 16 bytes to a lane (eight lanes: eight rows, eight different pieces), operands
+// by k through gfx950's transposing loads.
+
+#include <algorithm>
+#include <type_traits>
+
+#include "zs_act_dev.h"
+
+namespace zs {
+namespace {
+
+using namespace act;
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8hf __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+
+// A workgroup's tile: WM x WN waves, each FM x FN matrix instructions of 32 x 32.
+template <int WM_, int WN_, int FM_, int FN_>
+struct Tile {
+  static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_;
+  static constexpr int kThreads = WM * WN * 64;
+  static constexpr int kM = WM * FM * 32, kN = WN * FN * 32;
+  static constexpr int kLoadsM = kM * 8 / kThreads, kLoadsN = kN * 8 / kThreads;  // 16-byte pieces per thread and stage
+  static constexpr int kBuffer = (kM + kN) * 128;
+  static constexpr int kStripPitch = FN * 32 + 8;  // the epilogue's strips, as in the weight gradient
+  static constexpr int kStrips = WM * WN * 32 * kStripPitch * 4;
+  static constexpr int kLds = 2 * kBuffer > kStrips ? 2 * kBuffer : kStrips;
+  static_assert(kLds <= 163840, "LDS of a CU");
+  static_assert(kLoadsM * kThreads == kM * 8 && kLoadsN * kThreads == kN * 8, "whole loads");
+  static_assert(kThreads % 64 == 0 && kM >= 128 && kN >= 128, "blocks that change places");
+};
+
+// ------------------------------------------------------------------ groups of rows
+
+__device__ __forceinline__ int wave_max_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d && o > v) v = o;
+  }
+  return v;
+}
+__device__ __forceinline__ int wave_sum_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// Ends that run backwards or past the rows would lead out of the matrices: an end counts as the
+// largest one up to it, within 0 .. rows.
+struct Span {
+  int64_t first, last;
+  int group;
+};
+
+// The span of rows of group e.
+__device__ __forceinline__ Span group_span(const int32_t* ends, int e, int64_t rows) {
+  const int lane = threadIdx.x & 63;
+  int before = 0, upto = 0;
+  for (int c = 0; c <= e; c += 64) {
+    int v = c + lane <= e ? ends[c + lane] : 0;
+    v = v < 0 ? 0 : v > rows ? static_cast<int>(rows) : v;
+    const int all = __shfl(wave_max_scan(v, lane), 63);
+    const int less = __shfl(wave_max_scan(c + lane < e ? v : 0, lane), 63);
+    before = less > before ? less : before;
+    upto = all > upto ? all : upto;
+  }
+  return {before, upto > before ? upto : before, e};
+}
+
+// Tiles of `tile` rows of all groups, one group after the other, and, where `rest`, of the rows
+// behind the last one as one more group.  Returns how many there are; where 0 <= unit < that, *s
+// is the tile's group with the rows from the tile's first to the group's last.
+__device__ __forceinline__ int find_tile(const int32_t* ends, int groups, bool rest, int64_t rows, int tile, int unit, Span* s) {
+  if (ends == nullptr) {
+    *s = {int64_t(unit) * tile, rows, 0};
+    return static_cast<int>((rows + tile - 1) / tile);
+  }
+  const int lane = threadIdx.x & 63;
+  int top = 0, tiles = 0;
+  const int all = groups + (rest ? 1 : 0);
+  for (int c = 0; c < all; c += 64) {
+    int v = c + lane < groups ? ends[c + lane] : c + lane == groups && rest ? static_cast<int>(rows) : 0;
+    v = v < 0 ? 0 : v > rows ? static_cast<int>(rows) : v;
+    v = wave_max_scan(v, lane);
+    v = v > top ? v : top;
+    const int prev = __shfl_up(v, 1);
+    const int start = lane == 0 ? top : prev;
+    const int n = (v - start + tile - 1) / tile;
+    const int sum = wave_sum_scan(n, lane);
+    const int mine = unit - tiles - (sum - n);
+    const uint64_t hit = __ballot(mine >= 0 && mine < n);
+    if (hit != 0) {
+      const int at = __ffsll(static_cast<unsigned long long>(hit)) - 1;
+      s->first = int64_t(__shfl(start, at)) + int64_t(__shfl(mine, at)) * tile;
+      s->last = __shfl(v, at);
+      s->group = c + at;
+    }
+    tiles += __shfl(sum, 63);
+    top = __shfl(v, 63);
+  }
+  return tiles;
+}
+
+// ------------------------------------------------------------------ operands
+
+template <int DT>
+__device__ __forceinline__ v16f mfma(const v8s& a, const v8s& b, const v16f& c) {
+  if constexpr (DT == ZS_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8hf, a), __builtin_bit_cast(v8hf, b), c, 0, 0, 0);
+}
+
+constexpr int kEight = 3;  // the operands' type beside ZS_BF16 and ZS_FP16: e4m3 codes
+
+// One operand of a workgroup: R rows of m or n, `left` of them inside the matrix (the others repeat
+// the last one and reach outputs that are never stored), k from 0 to `depth` (elements).  BY_K: k
+// runs over memory rows.  `stride` and offsets in bytes.
+template <bool BY_K, int R, int THREADS, int SIZE>
+struct Operand {
+  static constexpr int kLoads = R * 8 / THREADS;
+  static constexpr int kPerRow = BY_K ? R / 8 : 8;        // pieces of a memory row
+  static constexpr int kRows = THREADS / kPerRow;         // memory rows of one load of the workgroup
+  static constexpr int kPitch = BY_K ? R * 2 : 128;
+  static constexpr int kDepth = BY_K ? 64 : 128 / SIZE;   // k of a stage
+  static_assert(!BY_K || SIZE == 2, "8-bit operands lie by rows");
+  static_assert(kRows % 8 == 0, "a thread's rows are alike modulo 8");
+  const char* base;
+  int64_t stride, depth, padded;
+  int left;
+  uint32_t off[kLoads];
+
+  // which piece of its memory row a thread fetches
+  static __device__ __forceinline__ int piece() {
+    const int row = threadIdx.x / kPerRow, at = threadIdx.x % kPerRow;
+    return BY_K ? ((at >> 2) ^ (row & 3)) << 2 | (at & 3) : at ^ (row & 7);
+  }
+  // padded: bytes of a memory row that may be read (8-bit operands by rows)
+  __device__ __forceinline__ Operand(const char* base_, int64_t stride_, int left_, int64_t depth_, int64_t padded_)
+      : base(base_), stride(stride_), depth(depth_), padded(padded_), left(left_) {
+    int p = piece();
+    if (BY_K && p * 8 + 8 > left) p = left / 8 > 0 ? left / 8 - 1 : 0;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      int row = u * kRows + threadIdx.x / kPerRow;
+      if (!BY_K && row >= left) row = left - 1;
+      off[u] = static_cast<uint32_t>(row * stride) + p * 16;
+    }
+  }
+  __device__ __forceinline__ const char* at(int64_t stage) const {
+    return base + stage * (BY_K ? stride * kDepth : int64_t(128));
+  }
+  // a whole stage from memory to LDS
+  __device__ __forceinline__ void direct(int64_t stage, char* lds, int wave) const {
+    const char* p = at(stage);
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+      __builtin_amdgcn_global_load_lds((global_void*)(p + off[u]), (lds_void*)(lds + (u * THREADS + wave * 64) * 16), 16, 0, 0);
+  }
+  // a stage into registers, at any alignment, with zeros outside; its addresses are worked out here
+  __device__ __forceinline__ void fetch(int64_t stage, v4u (&r)[kLoads]) const {
+    int id = threadIdx.x;
+    asm volatile("" : "+v"(id));
+    const int row0 = id / kPerRow, p = piece();
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      int64_t row = row0 + u * kRows;
+      if constexpr (SIZE == 1) {  // past the row's end: a piece of the same row, which meets zeros
+        if (row >= left) row = left - 1;
+        const int64_t byte = stage * 128 + p * 16;
+        r[u] = *reinterpret_cast<const v4u*>(base + row * stride + (byte < padded ? byte : padded - 16));
+      } else if constexpr (BY_K) {
+        row += stage * kDepth;
+        const int64_t cnt = row < depth ? left - p * 8 : 0;
+        r[u] = load8h(reinterpret_cast<const uint16_t*>(base + row * stride) + p * 8, cnt >= 8 ? 8 : cnt > 0 ? static_cast<int>(cnt) : 0);
+      } else {
+        if (row >= left) row = left - 1;
+        const int64_t k = stage * kDepth + p * 8, cnt = depth - k;
+        r[u] = load8h(reinterpret_cast<const uint16_t*>(base + row * stride) + k, cnt >= 8 ? 8 : cnt > 0 ? static_cast<int>(cnt) : 0);
+      }
+    }
+  }
+  static __device__ __forceinline__ void leave(const v4u (&r)[kLoads], char* lds) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) *reinterpret_cast<v4u*>(lds + (u * THREADS + threadIdx.x) * 16) = r[u];
+  }
+};
+
+// How a lane reads the fragments of one operand from a buffer: fragment f holds 32 rows of m or n,
+// step s 16 values of k in 16 bits (32 in 8): lanes 0 .. 31 the first half, 32 .. 63 the second.
+template <bool BY_K, int R, int F>
+struct Reader {
+  static constexpr int kPitch = BY_K ? R * 2 : 128;
+  int at[BY_K ? F : 4];
+  __device__ __forceinline__ Reader(int first) {  // the wave's first row
+    const int lane = threadIdx.x & 63;
+    if constexpr (BY_K) {
+      const int row = (lane >> 5) * 8 + ((lane & 15) >> 2), col = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+#pragma unroll
+      for (int f = 0; f < F; ++f) at[f] = row * kPitch + (((first + f * 32 + col) * 2) ^ ((row & 3) * 64));
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) at[s] = (first + (lane & 31)) * 128 + (((2 * s + (lane >> 5)) ^ (lane & 7)) * 16);
+    }
+  }
+  __device__ __forceinline__ v8s operator()(const char* buf, int f, int s) const {
+    if constexpr (BY_K) {
+      const char* p = buf + at[f] + s * 16 * kPitch;
+      const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
+      const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * kPitch));
+      return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      return *reinterpret_cast<const v8s*>(buf + at[s] + f * 4096);
+    }
+  }
+};
+
+// ------------------------------------------------------------------ the product
+
+// Eight sums of row `row` of c, from column col on, cnt of them inside: added to the base and
+// rounded once.
+__device__ __forceinline__ void write8(const ProductArgs& g, int64_t at, int cnt, float (&f)[8]) {
+  if (g.c_dt == ZS_FP32) {
+    float* p = static_cast<float*>(g.c) + at;
+    const float* base = static_cast<const float*>(g.base);
+    if (base != nullptr) base += at;
+    if (cnt == 8) {
+      v4u lo, hi;
+      if (base != nullptr) {
+        const v4u x = *reinterpret_cast<const v4u_a4*>(base), y = *reinterpret_cast<const v4u_a4*>(base + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[j] += bits_f(x[j]);
+          f[4 + j] += bits_f(y[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        lo[j] = f_bits(f[j]);
+        hi[j] = f_bits(f[4 + j]);
+      }
+      *reinterpret_cast<v4u_a4*>(p) = lo;
+      *reinterpret_cast<v4u_a4*>(p + 4) = hi;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (j < cnt) p[j] = f[j] + (base != nullptr ? base[j] : 0.0f);
+    }
+    return;
+  }
+  uint16_t* p = static_cast<uint16_t*>(g.c) + at;
+  if (g.base != nullptr) {
+    float x[8];
+    const v4u b = load8h(static_cast<const uint16_t*>(g.base) + at, cnt);
+    if (g.c_dt == ZS_BF16) widen8<ZS_BF16>(b, x);
+    else widen8<ZS_FP16>(b, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] += x[j];
+  }
+  const v4u w = g.c_dt == ZS_BF16 ? narrow8<ZS_BF16>(f) : narrow8<ZS_FP16>(f);
+  if (cnt >= 8) {
+    *reinterpret_cast<v4u_a2*>(p) = w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < cnt) p[j] = static_cast<uint16_t>(w[j >> 1] >> ((j & 1) * 16));
+  }
+}
+
+// Unit u of a tiles_m x tiles_n grid in bands of eight rows of tiles, column by column: workgroups
+// that run at the same time share rows of both operands in their XCD's L2.
+__device__ __forceinline__ void banded(int u, int tiles_m, int tiles_n, int* m, int* n) {
+  constexpr int kBand = 8;
+  const int band = u / (kBand * tiles_n), in = u - band * kBand * tiles_n;
+  const int high = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
+  *n = in / high;
+  *m = band * kBand + in - *n * high;
+}
+
+// KIND: ZS_BF16, ZS_FP16 or kEight.  AK, BK: operand a, b lies by k.  SUM_GROUPS: the groups divide
+// k, and each has an output of its own (the weight gradient); otherwise they divide m, and each has
+// a b of its own.  STAGED: stages pass through registers, for operands that are not aligned to 16
+// bytes.
+template <int KIND, bool AK, bool BK, bool SUM_GROUPS, bool STAGED, class TL>
+__global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  constexpr int kSize = KIND == kEight ? 1 : 2;
+  using OpA = Operand<AK, TL::kM, TL::kThreads, kSize>;
+  using OpB = Operand<BK, TL::kN, TL::kThreads, kSize>;
+  constexpr int kDepth = OpA::kDepth;
+
+  // one contiguous run of units per XCD
+  const int tiles_n = static_cast<int>((g.n + TL::kN - 1) / TL::kN);
+  Span s{0, 0, 0};
+  int64_t m0, n0, k0 = 0, depth = g.k;
+  {
+    int units, tiles_m = 0;
+    if constexpr (SUM_GROUPS) {
+      tiles_m = static_cast<int>((g.m + TL::kM - 1) / TL::kM);
+      units = tiles_m * tiles_n * g.groups;
+    } else {
+      tiles_m = find_tile(g.ends, g.groups, g.zero_rest, g.m, TL::kM, -1, &s);
+      units = tiles_m * tiles_n;
+    }
+    const int run = (units + kXcds - 1) / kXcds, in_run = blockIdx.x / kXcds;
+    int unit = blockIdx.x % kXcds * run + in_run;
+    if (in_run >= run || unit >= units) return;
+    int tm, tn;
+    if constexpr (SUM_GROUPS) {
+      const int e = unit / (tiles_m * tiles_n);
+      unit -= e * tiles_m * tiles_n;
+      s = group_span(g.ends, e, g.k);
+      banded(unit, tiles_m, tiles_n, &tm, &tn);
+      m0 = int64_t(tm) * TL::kM;
+      k0 = s.first;
+      depth = s.last - s.first;
+    } else {
+      banded(unit, tiles_m, tiles_n, &tm, &tn);
+      find_tile(g.ends, g.groups, g.zero_rest, g.m, TL::kM, tm, &s);
+      m0 = s.first;
+      if (g.ends != nullptr && s.group == g.groups) depth = 0;  // rows behind the last group: zeros
+    }
+    n0 = int64_t(tn) * TL::kN;
+  }
+  const int64_t m_end = SUM_GROUPS ? g.m : s.last;
+  const int left_m = static_cast<int>(m_end - m0 < TL::kM ? m_end - m0 : TL::kM);
+  const int left_n = static_cast<int>(g.n - n0 < TL::kN ? g.n - n0 : TL::kN);
+  // a group behind the last one has no b
+  const int64_t b_at = SUM_GROUPS || depth == 0 ? 0 : s.group * g.b_group;
+  const OpA op_a(static_cast<const char*>(g.a) + (AK ? k0 * g.a_stride + m0 : m0 * g.a_stride + k0) * kSize, g.a_stride * kSize,
+                 left_m, depth, g.a_padded);
+  const OpB op_b(static_cast<const char*>(g.b) + (b_at + (BK ? k0 * g.b_stride + n0 : n0 * g.b_stride + k0)) * kSize,
+                 g.b_stride * kSize, left_n, depth, g.b_padded);
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / TL::WN * TL::FM * 32, wn = wave % TL::WN * TL::FN * 32;
+  constexpr int kOperandA = TL::kM * 128;
+  const Reader<AK, TL::kM, TL::FM> read_a(wm);
+  const Reader<BK, TL::kN, TL::FN> read_b(wn);
+
+  v16f acc[TL::FM][TL::FN];
+#pragma unroll
+  for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < TL::FN; ++j) acc[i][j] = v16f(0.0f);
+
+  // scales of 8-bit operands: a dword of four groups of 32 for each of a's rows, a byte for b's
+  // block.  Lanes 32 .. 63 multiply the second and fourth group.
+  constexpr int kScales = KIND == kEight ? TL::FM : 1;
+  struct Scales {
+    int a[kScales], b;
+  };
+  auto fetch_scales = [&](int64_t stage, Scales& sc) {
+    if constexpr (KIND == kEight) {
+      const int64_t groups = g.a_padded / kActGroup;
+#pragma unroll
+      for (int i = 0; i < TL::FM; ++i) {
+        int row = wm + i * 32 + (lane & 31);
+        if (row >= left_m) row = left_m - 1;
+        const uint8_t* p = g.a_scales + (m0 + row) * groups;
+        if (stage * 4 + 4 <= groups) {
+          sc.a[i] = *reinterpret_cast<const __attribute__((aligned(1))) int*>(p + stage * 4);
+        } else {  // groups past the row's end count as its last one: they meet zeros
+          int w = 0;
+          for (int q = 0; q < 4; ++q) {
+            const int64_t at = stage * 4 + q;
+            w |= p[at < groups ? at : groups - 1] << (8 * q);
+          }
+          sc.a[i] = w;
+        }
+      }
+      int64_t row = n0 + wn, col = stage;
+      if (row >= g.n) row = g.n - 1;
+      // transposed codes: the blocks' rows run along k
+      sc.b = g.b_turned ? g.b_scales[col * g.b_blocks + row / 128] : g.b_scales[row / 128 * g.b_blocks + col];
+    }
+  };
+  auto settle = [&](Scales& sc) {  // the loads have landed
+    if constexpr (KIND == kEight) {
+#pragma unroll
+      for (int i = 0; i < TL::FM; ++i) {
+        sc.a[i] = static_cast<int>(static_cast<uint32_t>(sc.a[i]) >> (lane >> 5) * 8);
+        asm volatile("" : "+v"(sc.a[i]));
+      }
+      asm volatile("" : "+v"(sc.b));
+    }
+  };
+
+  // A stage is multiplied in four steps (in two of double depth for 8-bit operands).
+  constexpr int kSteps = KIND == kEight ? 2 : 4, kParts = 4 / kSteps;
+  struct Operands {
+    v8s a[TL::FM][kParts], b[TL::FN][kParts];
+  };
+  auto read = [&](Operands& f, const char* buf, int step) {
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) {
+#pragma unroll
+      for (int i = 0; i < TL::FM; ++i) f.a[i][q] = read_a(buf, i, step * kParts + q);
+#pragma unroll
+      for (int j = 0; j < TL::FN; ++j) f.b[j][q] = read_b(buf + kOperandA, j, step * kParts + q);
+    }
+  };
+  auto multiply = [&](const Operands& f, const Scales& sc, auto step) {
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < TL::FN; ++j) {
+        if constexpr (KIND == kEight) {
+          typedef short v16s __attribute__((ext_vector_type(16)));
+          const v16s a = __builtin_shufflevector(f.a[i][0], f.a[i][1], 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+          const v16s b = __builtin_shufflevector(f.b[j][0], f.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(__builtin_bit_cast(v8i, a), __builtin_bit_cast(v8i, b),
+                                                                      acc[i][j], 0, 0, 2 * decltype(step)::value, sc.a[i], 0, sc.b);
+        } else {
+          acc[i][j] = mfma<KIND>(f.a[i][0], f.b[j][0], acc[i][j]);
+        }
+      }
+  };
+
+  const int64_t stages = (depth + kDepth - 1) / kDepth;
+  // stages that lie inside both operands; the others pass through registers
+  const int64_t whole = STAGED ? 0 : KIND == kEight ? std::min(g.a_padded, g.b_padded) / 128 : depth / kDepth;
+  v4u ra[STAGED ? OpA::kLoads : 1], rb[STAGED ? OpB::kLoads : 1];
+  auto begin = [&](int64_t stage, char* buf) {
+    if constexpr (STAGED) {
+      op_a.fetch(stage, ra);
+      op_b.fetch(stage, rb);
+    } else if (stage < whole) {
+      op_a.direct(stage, buf, wave);
+      op_b.direct(stage, buf + kOperandA, wave);
+    } else {
+      v4u ta[OpA::kLoads], tb[OpB::kLoads];
+      op_a.fetch(stage, ta);
+      op_b.fetch(stage, tb);
+      OpA::leave(ta, buf);
+      OpB::leave(tb, buf + kOperandA);
+    }
+  };
+  auto finish = [&](char* buf) {
+    if constexpr (STAGED) {
+      OpA::leave(ra, buf);
+      OpB::leave(rb, buf + kOperandA);
+    }
+  };
+  if (stages > 0) {
+    Scales sc[2];
+    Operands f[2];
+    char* cur = lds;
+    char* other = lds + TL::kBuffer;
+    begin(0, cur);
+    fetch_scales(0, sc[0]);
+    finish(cur);
+    __syncthreads();
+    settle(sc[0]);
+    for (int64_t i = 0; i < stages; ++i) {
+      if (i + 1 < stages) {
+        begin(i + 1, other);
+        fetch_scales(i + 1, sc[1]);
+      }
+      read(f[0], cur, 0);
+      if constexpr (kSteps == 4) {
+        read(f[1], cur, 1);
+        multiply(f[0], sc[0], std::integral_constant<int, 0>{});
+        read(f[0], cur, 2);
+        multiply(f[1], sc[0], std::integral_constant<int, 0>{});
+        read(f[1], cur, 3);
+        multiply(f[0], sc[0], std::integral_constant<int, 0>{});
+        multiply(f[1], sc[0], std::integral_constant<int, 0>{});
+      } else {
+        read(f[1], cur, 1);
+        multiply(f[0], sc[0], std::integral_constant<int, 0>{});
+        multiply(f[1], sc[0], std::integral_constant<int, 1>{});
+      }
+      if (i + 1 < stages) finish(other);
+      __syncthreads();
+      sc[0] = sc[1];
+      settle(sc[0]);
+      char* x = cur;
+      cur = other;
+      other = x;
+    }
+  }
+
+  // The sums leave through LDS, a strip of 32 rows of the wave at a time, so that a lane stores
+  // eight consecutive elements of a row.  Accumulator r of a lane is row 8 * (r / 4) + 4 * (lane / 32)
+  // + r % 4, column lane % 32.
+  float* strip = reinterpret_cast<float*>(lds) + wave * 32 * TL::kStripPitch;
+  const int64_t c_at = SUM_GROUPS ? s.group * g.c_group : 0;
+#pragma unroll
+  for (int i = 0; i < TL::FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        strip[(8 * (r / 4) + 4 * (lane >> 5) + r % 4) * TL::kStripPitch + j * 32 + (lane & 31)] = acc[i][j][r];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    for (int q = lane; q < 32 * TL::FN * 4; q += 64) {
+      const int r = q / (TL::FN * 4), c = q % (TL::FN * 4) * 8;
+      const v4u x = *reinterpret_cast<const v4u*>(strip + r * TL::kStripPitch + c);
+      const v4u y = *reinterpret_cast<const v4u*>(strip + r * TL::kStripPitch + c + 4);
+      const int tm = wm + i * 32 + r, left = left_n - (wn + c);
+      if (tm >= left_m || left <= 0) continue;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = bits_f(x[j]);
+        v[4 + j] = bits_f(y[j]);
+      }
+      write8(g, c_at + (m0 + tm) * g.c_stride + n0 + wn + c, left >= 8 ? 8 : left, v);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+using SmallTile = Tile<2, 2, 2, 2>;  // 128 x 128
+using LargeTile = Tile<2, 4, 4, 2>;  // 256 x 256
+
+// ------------------------------------------------------------------ launch choices
+
+template <int KIND, bool AK, bool BK, bool SUM_GROUPS, bool STAGED, class TL>
+hipError_t launch_tile(const ProductArgs& a, hipStream_t s) {
+  auto kernel = &k_product<KIND, AK, BK, SUM_GROUPS, STAGED, TL>;
+  if (TL::kLds > 65536) {
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, TL::kLds);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t units = product_units(a, SUM_GROUPS, TL::kM, TL::kN);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(launch_units(units, kXcdWhole))), dim3(TL::kThreads), TL::kLds, s, a);
+  return hipGetLastError();
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Whether an operand's stages can go straight to LDS: 16-byte pieces at 16-byte addresses, offsets
+// within a tile of 32 bits; by k also whole pieces at a row's end.
+bool direct_rows(const void* p, int64_t stride, int64_t group) {
+  return aligned16(p) && stride % 8 == 0 && group % 8 == 0 && stride < (1 << 22);
+}
+
+template <int KIND, bool AK, bool BK, bool SUM_GROUPS>
+hipError_t launch_sizes(const ProductArgs& a, hipStream_t s) {
+  const bool direct = direct_rows(a.a, a.a_stride, 0) && direct_rows(a.b, a.b_stride, a.b_group) && (!AK || a.m % 8 == 0) &&
+                      (!BK || a.n % 8 == 0);
+  if (!direct) return launch_tile<KIND, AK, BK, SUM_GROUPS, true, SmallTile>(a, s);
+  const int64_t per_group = SUM_GROUPS ? a.m : a.m / std::max(1, a.groups);
+  if (per_group >= 192 && a.n >= 192 && product_units(a, SUM_GROUPS, LargeTile::kM, LargeTile::kN) >= 200)
+    return launch_tile<KIND, AK, BK, SUM_GROUPS, false, LargeTile>(a, s);
+  return launch_tile<KIND, AK, BK, SUM_GROUPS, false, SmallTile>(a, s);
+}
+
+}  // namespace
+
+int64_t product_units(const ProductArgs& a, bool sum_groups, int64_t tile_m, int64_t tile_n) {
+  const int64_t tn = (a.n + tile_n - 1) / tile_n;
+  if (sum_groups) return a.groups * ((a.m + tile_m - 1) / tile_m) * tn;
+  // every group may end with a part of a tile
+  return ((a.m + tile_m - 1) / tile_m + (a.ends != nullptr ? a.groups : 0)) * tn;
+}
+
+hipError_t launch_product8(const ProductArgs& a, hipStream_t s) {
+  if (product_units(a, false, LargeTile::kM, LargeTile::kN) >= 200)
+    return launch_tile<kEight, false, false, false, false, LargeTile>(a, s);
+  return launch_tile<kEight, false, false, false, false, SmallTile>(a, s);
+}
+
+hipError_t launch_expert_product(const ProductArgs& a, int dt, bool in_major, hipStream_t s) {
+  if (dt == ZS_BF16)
+    return in_major ? launch_sizes<ZS_BF16, false, true, false>(a, s) : launch_sizes<ZS_BF16, false, false, false>(a, s);
+  return in_major ? launch_sizes<ZS_FP16, false, true, false>(a, s) : launch_sizes<ZS_FP16, false, false, false>(a, s);
+}
+
+hipError_t launch_expert_wgrad(const ProductArgs& a, int dt, hipStream_t s) {
+  return dt == ZS_BF16 ? launch_sizes<ZS_BF16, true, true, true>(a, s) : launch_sizes<ZS_FP16, true, true, true>(a, s);
+}
+
+// ------------------------------------------------------------------ weights in 8 bits
+
+namespace {
+
+// The codes of a weight, its transposed codes and its scales, one 128 x 128 block to a workgroup.  A
+// thread holds two patches of four rows by eight columns, so that the four codes of a column leave
+// as one word of the transposed block, which is turned in LDS.
+template <int DT>
+__global__ __launch_bounds__(256) void k_weight8(const void* src, int64_t stride, int64_t outs, int64_t cols, uint8_t* codes,
+                                                 uint8_t* codes_t, uint8_t* scales, int64_t blocks_n) {
+  __shared__ __attribute__((aligned(16))) uint32_t turned[128 * 36];  // a column's 128 codes at a pitch of 144 bytes
+  __shared__ uint32_t tops[4];
+  const int64_t bo = blockIdx.x / blocks_n, bc = blockIdx.x % blocks_n;
+  const int64_t pc = blocks_n * 128, pr = (outs + 127) / 128 * 128;
+  const int patch_c = threadIdx.x % 16, patch_r = threadIdx.x / 16;  // rows patch_r * 4 and 64 + patch_r * 4
+  const int64_t col = bc * 128 + patch_c * 8;
+  const int64_t left = cols - col;
+  const int cnt = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
+  float f[2][4][8];
+  float top = 0.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t row = bo * 128 + h * 64 + patch_r * 4 + r;
+      const int n = row < outs ? cnt : 0;
+      if constexpr (DT == ZS_FP32) {
+        const float* p = static_cast<const float*>(src) + row * stride + col;
+        if (n == 8) {
+          const v4u x = *reinterpret_cast<const v4u_a4*>(p), y = *reinterpret_cast<const v4u_a4*>(p + 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[h][r][j] = bits_f(x[j]);
+            f[h][r][4 + j] = bits_f(y[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[h][r][j] = j < n ? p[j] : 0.0f;
+        }
+      } else {
+        widen8<DT>(load8h(static_cast<const uint16_t*>(src) + row * stride + col, n), f[h][r]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = __builtin_elementwise_maximum(top, fabsf(f[h][r][j]));  // a NaN wins
+    }
+  uint32_t m = f_bits(top) & 0x7FFFFFFFu;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    const uint32_t o = __shfl_xor(m, d);
+    m = o > m ? o : m;
+  }
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) m = tops[w] > m ? tops[w] : m;
+  const int b = scale_byte<ZS_E4M3>(m);
+  if (threadIdx.x == 0) scales[bo * blocks_n + bc] = static_cast<uint8_t>(b);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    v2u c[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      c[r] = encode8<ZS_E4M3>(f[h][r], b);
+      const int64_t row = bo * 128 + h * 64 + patch_r * 4 + r;
+      if (row < outs) *reinterpret_cast<v2u*>(codes + row * pc + col) = c[r];
+    }
+    if (codes_t != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w |= ((c[r][j >> 2] >> (j % 4 * 8)) & 0xFFu) << (8 * r);
+        turned[(patch_c * 8 + j) * 36 + h * 16 + patch_r] = w;
+      }
+    }
+  }
+  if (codes_t == nullptr) return;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int id = q * 256 + threadIdx.x, row = id / 8, at = id % 8;
+    const int64_t c = bc * 128 + row;
+    if (c < cols) *reinterpret_cast<v4u*>(codes_t + c * pr + bo * 128 + at * 16) = *reinterpret_cast<const v4u*>(turned + row * 36 + at * 4);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_weight8(const void* src, int dt, int64_t stride, int64_t outs, int64_t cols, uint8_t* codes, uint8_t* codes_t,
+                          uint8_t* scales, hipStream_t s) {
+  const int64_t blocks_n = (cols + 127) / 128, blocks = (outs + 127) / 128 * blocks_n;
+  if (blocks == 0) return hipSuccess;
+  auto kernel = dt == ZS_BF16 ? &k_weight8<ZS_BF16> : dt == ZS_FP16 ? &k_weight8<ZS_FP16> : &k_weight8<ZS_FP32>;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, src, stride, outs, cols, codes, codes_t, scales,
+                     blocks_n);
+  return hipGetLastError();
+}
+
+}  // namespace zs
