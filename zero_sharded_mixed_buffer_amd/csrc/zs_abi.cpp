@@ -1300,8 +1300,9 @@ extern "C" zs_status zs_product8(const zs_act* x8, int64_t rows, const zs_weight
   a.k = k;
   a.a_padded = a.a_stride = zs::act_padded(k);
   a.b_padded = a.b_stride = round_up(k, zs::kWeightBlock);
-  a.b_blocks = round_up(cols, zs::kWeightBlock) / zs::kWeightBlock;
-  a.b_turned = transposed != 0;
+  const int64_t blocks = round_up(cols, zs::kWeightBlock) / zs::kWeightBlock;  // of a row of w8's blocks
+  a.b_scale_row = transposed ? 1 : blocks;
+  a.b_scale_step = transposed ? blocks : 1;
   a.c_stride = y_stride;
   a.c_dt = y_dtype;
   a.groups = 1;

@@ -204,10 +204,9 @@ struct ProductArgs {
   int64_t m, n, k;
   int64_t a_stride, b_stride, c_stride, b_group, c_group;
   int64_t a_padded, b_padded;  // codes of a row of 8-bit operands
-  int64_t b_blocks;            // scales of a row of blocks
+  int64_t b_scale_row, b_scale_step;  // from one of b's blocks to the next, along its rows and along k
   int32_t groups;
   int32_t c_dt;
-  bool b_turned;   // b holds the transposed codes
   bool zero_rest;  // rows behind the last group become zeros
 };
 // Workgroups of a launch with such tiles.

@@ -4,12 +4,12 @@
 // on the matrix cores, summed in fp32.
 //
 // An operand lies in memory with consecutive k (rows of m or n, "by rows"), or with consecutive m
-// or n (rows of k, "by k").  A stage of the sum is 128 bytes of every row: 64 values of k in 16
-// bits, 128 in 8.  Stages go from memory straight into LDS, 16 bytes to a lane, two buffers in
-// turn.  Such a load puts a wave's 64 pieces one after the other, so rows cannot be padded against
-// bank conflicts: instead a lane fetches another piece of its row than its place says.  Operands by
-// rows are read back 16 bytes to a lane (eight lanes: eight rows, eight different pieces), operands
-// by k through gfx950's transposing loads.
+// or n (rows of k, "by k").  A stage of the sum is 128 bytes of every row, a cache line: 64 values of
+// k in 16 bits, 128 in 8.  Stages go from memory straight into LDS, 16 bytes to a lane, into two
+// buffers in turn.  Such a load puts a wave's 64 pieces one after the other, so rows cannot be padded
+// against bank conflicts: instead a lane fetches another piece of its row than its place says.
+// Operands by rows are read back 16 bytes to a lane (sixteen lanes that read at once: sixteen rows,
+// whose pieces lie on all 64 banks), operands by k through gfx950's transposing loads.
 
 #include <algorithm>
 #include <type_traits>
@@ -29,7 +29,7 @@ typedef _Float16 v8hf __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(1))) const void global_void;
+typedef v4u v4u_a1 __attribute__((aligned(1)));
 
 // A workgroup's tile: WM x WN waves, each FM x FN matrix instructions of 32 x 32.
 template <int WM_, int WN_, int FM_, int FN_>
@@ -37,14 +37,18 @@ struct Tile {
   static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_;
   static constexpr int kThreads = WM * WN * 64;
   static constexpr int kM = WM * FM * 32, kN = WN * FN * 32;
-  static constexpr int kLoadsM = kM * 8 / kThreads, kLoadsN = kN * 8 / kThreads;  // 16-byte pieces per thread and stage
-  static constexpr int kBuffer = (kM + kN) * 128;
+  // bytes of a stage of half of a's rows, and of b's
+  static constexpr int kHalfM = kM / 2 * 128, kBufferN = kN * 128;
+  static constexpr int kBuffers = 4 * kHalfM + 2 * kBufferN;
+  static constexpr int kSegment = kM * 64;  // a's scales (8-bit operands): 64 bytes of each row, twice
   static constexpr int kStripPitch = FN * 32 + 8;  // the epilogue's strips, as in the weight gradient
   static constexpr int kStrips = WM * WN * 32 * kStripPitch * 4;
-  static constexpr int kLds = 2 * kBuffer > kStrips ? 2 * kBuffer : kStrips;
-  static_assert(kLds <= 163840, "LDS of a CU");
-  static_assert(kLoadsM * kThreads == kM * 8 && kLoadsN * kThreads == kN * 8, "whole loads");
-  static_assert(kThreads % 64 == 0 && kM >= 128 && kN >= 128, "blocks that change places");
+  static constexpr int lds(bool eight) {
+    const int all = kBuffers + (eight ? 2 * kSegment : 0);
+    return all > kStrips ? all : kStrips;
+  }
+  static_assert(lds(true) <= 163840, "LDS of a CU");
+  static_assert(FM % 2 == 0 && kThreads % 64 == 0 && kM >= 128 && kN >= 128, "halves, and blocks that change places");
 };
 
 // ------------------------------------------------------------------ groups of rows
@@ -73,6 +77,8 @@ struct Span {
   int group;
 };
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // The span of rows of group e.
 __device__ __forceinline__ Span group_span(const int32_t* ends, int e, int64_t rows) {
   const int lane = threadIdx.x & 63;
@@ -85,6 +91,8 @@ __device__ __forceinline__ Span group_span(const int32_t* ends, int e, int64_t r
     before = less > before ? less : before;
     upto = all > upto ? all : upto;
   }
+  before = uniform(before);
+  upto = uniform(upto);
   return {before, upto > before ? upto : before, e};
 }
 
@@ -112,12 +120,12 @@ __device__ __forceinline__ int find_tile(const int32_t* ends, int groups, bool r
     const uint64_t hit = __ballot(mine >= 0 && mine < n);
     if (hit != 0) {
       const int at = __ffsll(static_cast<unsigned long long>(hit)) - 1;
-      s->first = int64_t(__shfl(start, at)) + int64_t(__shfl(mine, at)) * tile;
-      s->last = __shfl(v, at);
+      s->first = __builtin_amdgcn_readlane(start, at) + int64_t(__builtin_amdgcn_readlane(mine, at)) * tile;
+      s->last = __builtin_amdgcn_readlane(v, at);
       s->group = c + at;
     }
-    tiles += __shfl(sum, 63);
-    top = __shfl(v, 63);
+    tiles += __builtin_amdgcn_readlane(sum, 63);
+    top = __builtin_amdgcn_readlane(v, 63);
   }
   return tiles;
 }
@@ -134,49 +142,59 @@ __device__ __forceinline__ v16f mfma(const v8s& a, const v8s& b, const v16f& c) 
 
 constexpr int kEight = 3;  // the operands' type beside ZS_BF16 and ZS_FP16: e4m3 codes
 
-// One operand of a workgroup: R rows of m or n, `left` of them inside the matrix (the others repeat
-// the last one and reach outputs that are never stored), k from 0 to `depth` (elements).  BY_K: k
-// runs over memory rows.  `stride` and offsets in bytes.
-template <bool BY_K, int R, int THREADS, int SIZE>
+// One operand of a workgroup, or half of one: R rows of m or n, k from 0 to `depth` (elements).
+// BY_K: k runs over memory rows.  Row r is the tile's row r, or, of a half, the r % RUN-th of the
+// half's rows of wave row r / RUN: each wave finds half of its rows in either half.  `left` rows of
+// the tile lie inside the matrix; the others repeat the last one and reach outputs that are never
+// stored.  `stride` and offsets in bytes.
+template <bool BY_K, int R, int RUN, int THREADS, int SIZE>
 struct Operand {
-  static constexpr int kLoads = R * 8 / THREADS;
-  static constexpr int kPerRow = BY_K ? R / 8 : 8;        // pieces of a memory row
-  static constexpr int kRows = THREADS / kPerRow;         // memory rows of one load of the workgroup
-  static constexpr int kPitch = BY_K ? R * 2 : 128;
-  static constexpr int kDepth = BY_K ? 64 : 128 / SIZE;   // k of a stage
+  static constexpr int kLoads = R * 8 / THREADS;         // 16-byte pieces per thread and stage
+  static constexpr int kPerRow = BY_K ? R / 8 : 8;       // pieces of a memory row
+  static constexpr int kRows = THREADS / kPerRow;        // memory rows of one load of the workgroup
+  static constexpr int kDepth = BY_K ? 64 : 128 / SIZE;  // k of a stage
+  static constexpr int kBlocks = R >= 128 ? 4 : 2;       // by k: blocks of 64 bytes that change places
   static_assert(!BY_K || SIZE == 2, "8-bit operands lie by rows");
-  static_assert(kRows % 8 == 0, "a thread's rows are alike modulo 8");
+  static_assert(kLoads * THREADS == R * 8, "whole loads");
+  static_assert(kRows % (BY_K ? 4 : 16) == 0, "a thread's pieces change places alike");
   const char* base;
   int64_t stride, depth, padded;
-  int left;
+  int left, half;  // half: 0 or 1, -1 for a whole operand
   uint32_t off[kLoads];
 
   // which piece of its memory row a thread fetches
   static __device__ __forceinline__ int piece() {
     const int row = threadIdx.x / kPerRow, at = threadIdx.x % kPerRow;
-    return BY_K ? ((at >> 2) ^ (row & 3)) << 2 | (at & 3) : at ^ (row & 7);
+    return BY_K ? ((at >> 2) ^ (row & (kBlocks - 1))) << 2 | (at & 3) : at ^ ((row >> 1) & 7);
   }
+  __device__ __forceinline__ int tile_row(int r) const { return half < 0 ? r : r / RUN * (2 * RUN) + half * RUN + r % RUN; }
   // padded: bytes of a memory row that may be read (8-bit operands by rows)
-  __device__ __forceinline__ Operand(const char* base_, int64_t stride_, int left_, int64_t depth_, int64_t padded_)
-      : base(base_), stride(stride_), depth(depth_), padded(padded_), left(left_) {
-    int p = piece();
-    if (BY_K && p * 8 + 8 > left) p = left / 8 > 0 ? left / 8 - 1 : 0;
+  __device__ __forceinline__ Operand(const char* base_, int64_t stride_, int left_, int64_t depth_, int64_t padded_, int half_ = -1)
+      : base(base_), stride(stride_), depth(depth_), padded(padded_), left(left_), half(half_) {
+    int col = tile_row(piece() * 8);  // by k
+    if (BY_K && col + 8 > left) col = left >= 8 ? left - 8 : 0;
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       int row = u * kRows + threadIdx.x / kPerRow;
-      if (!BY_K && row >= left) row = left - 1;
-      off[u] = static_cast<uint32_t>(row * stride) + p * 16;
+      if (!BY_K) {
+        row = tile_row(row);
+        if (row >= left) row = left - 1;
+      }
+      off[u] = static_cast<uint32_t>(row) * static_cast<uint32_t>(stride) + (BY_K ? col * 2 : piece() * 16);
+      asm volatile("" : "+v"(off[u]));  // one register, not half of a 64-bit product
     }
   }
   __device__ __forceinline__ const char* at(int64_t stage) const {
     return base + stage * (BY_K ? stride * kDepth : int64_t(128));
   }
-  // a whole stage from memory to LDS
-  __device__ __forceinline__ void direct(int64_t stage, char* lds, int wave) const {
-    const char* p = at(stage);
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-      __builtin_amdgcn_global_load_lds((global_void*)(p + off[u]), (lds_void*)(lds + (u * THREADS + wave * 64) * 16), 16, 0, 0);
+  // Piece u of a whole stage, which begins at p, from memory to LDS.  (A buffer's base is scalar and
+  // moves with the stage; the offsets stay.  Beside global loads to LDS the compiler would wait for all
+  // LDS reads under way wherever one is needed.)
+  __device__ __forceinline__ void direct(int u, const char* p, char* lds, int wave) const {
+#ifdef __HIP_DEVICE_COMPILE__  // the host compiler knows no buffers
+    const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, -1, 0x00027000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (u * THREADS + wave * 64) * 16), 16, off[u], 0, 0, 0);
+#endif
   }
   // a stage into registers, at any alignment, with zeros outside; its addresses are worked out here
   __device__ __forceinline__ void fetch(int64_t stage, v4u (&r)[kLoads]) const {
@@ -186,16 +204,19 @@ struct Operand {
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       int64_t row = row0 + u * kRows;
+      if constexpr (BY_K) {
+        const int col = tile_row(p * 8);
+        row += stage * kDepth;
+        const int cnt = row < depth ? left - col : 0;
+        r[u] = load8h(reinterpret_cast<const uint16_t*>(base + row * stride) + col, cnt >= 8 ? 8 : cnt > 0 ? cnt : 0);
+        continue;
+      }
+      row = tile_row(static_cast<int>(row));
+      if (row >= left) row = left - 1;
       if constexpr (SIZE == 1) {  // past the row's end: a piece of the same row, which meets zeros
-        if (row >= left) row = left - 1;
         const int64_t byte = stage * 128 + p * 16;
         r[u] = *reinterpret_cast<const v4u*>(base + row * stride + (byte < padded ? byte : padded - 16));
-      } else if constexpr (BY_K) {
-        row += stage * kDepth;
-        const int64_t cnt = row < depth ? left - p * 8 : 0;
-        r[u] = load8h(reinterpret_cast<const uint16_t*>(base + row * stride) + p * 8, cnt >= 8 ? 8 : cnt > 0 ? static_cast<int>(cnt) : 0);
       } else {
-        if (row >= left) row = left - 1;
         const int64_t k = stage * kDepth + p * 8, cnt = depth - k;
         r[u] = load8h(reinterpret_cast<const uint16_t*>(base + row * stride) + k, cnt >= 8 ? 8 : cnt > 0 ? static_cast<int>(cnt) : 0);
       }
@@ -208,20 +229,22 @@ struct Operand {
 };
 
 // How a lane reads the fragments of one operand from a buffer: fragment f holds 32 rows of m or n,
-// step s 16 values of k in 16 bits (32 in 8): lanes 0 .. 31 the first half, 32 .. 63 the second.
+// quarter s of a stage 16 values of k in 16 bits (32 in 8): lanes 0 .. 31 the first of its two pieces,
+// 32 .. 63 the second.
 template <bool BY_K, int R, int F>
 struct Reader {
   static constexpr int kPitch = BY_K ? R * 2 : 128;
-  int at[BY_K ? F : 4];
+  int at[BY_K ? F : 4], wave_at;
   __device__ __forceinline__ Reader(int first) {  // the wave's first row
     const int lane = threadIdx.x & 63;
+    wave_at = BY_K ? 0 : first * 128;
     if constexpr (BY_K) {
       const int row = (lane >> 5) * 8 + ((lane & 15) >> 2), col = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
 #pragma unroll
-      for (int f = 0; f < F; ++f) at[f] = row * kPitch + (((first + f * 32 + col) * 2) ^ ((row & 3) * 64));
+      for (int f = 0; f < F; ++f) at[f] = row * kPitch + (((first + f * 32 + col) * 2) ^ ((row & (R >= 128 ? 3 : 1)) * 64));
     } else {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) at[s] = (first + (lane & 31)) * 128 + (((2 * s + (lane >> 5)) ^ (lane & 7)) * 16);
+      for (int s = 0; s < 4; ++s) at[s] = (lane & 31) * 128 + (((2 * s + (lane >> 5)) ^ ((lane >> 1) & 7)) * 16);
     }
   }
   __device__ __forceinline__ v8s operator()(const char* buf, int f, int s) const {
@@ -231,10 +254,30 @@ struct Reader {
       const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * kPitch));
       return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
-      return *reinterpret_cast<const v8s*>(buf + at[s] + f * 4096);
+      return *reinterpret_cast<const v8s*>(buf + wave_at + at[s] + f * 4096);
     }
   }
 };
+
+// Waits until at most N of the wave's loads are under way, and for its LDS reads and writes; the
+// workgroup's barrier.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+#endif
+}
+__device__ __forceinline__ void wait_lds() {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#endif
+}
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
 
 // ------------------------------------------------------------------ the product
 
@@ -306,8 +349,8 @@ template <int KIND, bool AK, bool BK, bool SUM_GROUPS, bool STAGED, class TL>
 __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   constexpr int kSize = KIND == kEight ? 1 : 2;
-  using OpA = Operand<AK, TL::kM, TL::kThreads, kSize>;
-  using OpB = Operand<BK, TL::kN, TL::kThreads, kSize>;
+  using OpA = Operand<AK, TL::kM / 2, TL::FM * 16, TL::kThreads, kSize>;
+  using OpB = Operand<BK, TL::kN, TL::kN, TL::kThreads, kSize>;
   constexpr int kDepth = OpA::kDepth;
 
   // one contiguous run of units per XCD
@@ -348,15 +391,14 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
   const int left_n = static_cast<int>(g.n - n0 < TL::kN ? g.n - n0 : TL::kN);
   // a group behind the last one has no b
   const int64_t b_at = SUM_GROUPS || depth == 0 ? 0 : s.group * g.b_group;
-  const OpA op_a(static_cast<const char*>(g.a) + (AK ? k0 * g.a_stride + m0 : m0 * g.a_stride + k0) * kSize, g.a_stride * kSize,
-                 left_m, depth, g.a_padded);
+  const char* const a_base = static_cast<const char*>(g.a) + (AK ? k0 * g.a_stride + m0 : m0 * g.a_stride + k0) * kSize;
+  const OpA op_a[2] = {{a_base, g.a_stride * kSize, left_m, depth, g.a_padded, 0}, {a_base, g.a_stride * kSize, left_m, depth, g.a_padded, 1}};
   const OpB op_b(static_cast<const char*>(g.b) + (b_at + (BK ? k0 * g.b_stride + n0 : n0 * g.b_stride + k0)) * kSize,
                  g.b_stride * kSize, left_n, depth, g.b_padded);
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / TL::WN * TL::FM * 32, wn = wave % TL::WN * TL::FN * 32;
-  constexpr int kOperandA = TL::kM * 128;
-  const Reader<AK, TL::kM, TL::FM> read_a(wm);
+  const Reader<AK, TL::kM / 2, TL::FM / 2> read_a(wm / 2);
   const Reader<BK, TL::kN, TL::FN> read_b(wn);
 
   v16f acc[TL::FM][TL::FN];
@@ -365,141 +407,222 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
 #pragma unroll
     for (int j = 0; j < TL::FN; ++j) acc[i][j] = v16f(0.0f);
 
-  // scales of 8-bit operands: a dword of four groups of 32 for each of a's rows, a byte for b's
-  // block.  Lanes 32 .. 63 multiply the second and fourth group.
+  // Scales of 8-bit operands for a stage: a dword of four groups of 32 for each of a's rows, a byte for
+  // b's block.  Lanes 32 .. 63 name those of the second and fourth group.  Those of a come through LDS,
+  // a segment of sixteen stages (64 bytes of a row) at a time: read by each wave for its fragments, the
+  // scattered dwords took as long as both operands.  The four pieces of a segment's row change places
+  // by (row / 4) % 4.
   constexpr int kScales = KIND == kEight ? TL::FM : 1;
+  constexpr int kPieces = TL::kM * 4 / TL::kThreads;
   struct Scales {
     int a[kScales], b;
   };
-  auto fetch_scales = [&](int64_t stage, Scales& sc) {
+  char* const segments = lds + TL::kBuffers;
+  const int64_t a_groups = g.a_padded / kActGroup;
+  const uint8_t* b_scale = nullptr;
+  if constexpr (KIND == kEight) b_scale = g.b_scales + (n0 + wn < g.n ? n0 + wn : g.n - 1) / 128 * g.b_scale_row;
+  auto begin_segment = [&](int64_t segment) {
     if constexpr (KIND == kEight) {
-      const int64_t groups = g.a_padded / kActGroup;
+      char* into = segments + (segment & 1) * TL::kSegment;
+      const uint8_t* p = g.a_scales + m0 * a_groups + segment * 64;
+      const int64_t left = a_groups - segment * 64;  // groups of the rows from here on
+      int id = threadIdx.x;
+      asm volatile("" : "+v"(id));
 #pragma unroll
-      for (int i = 0; i < TL::FM; ++i) {
-        int row = wm + i * 32 + (lane & 31);
+      for (int u = 0; u < kPieces; ++u) {
+        int row = (u * TL::kThreads + id) / 4;
+        const int at = ((id & 3) ^ ((row >> 2) & 3)) * 16;
         if (row >= left_m) row = left_m - 1;
-        const uint8_t* p = g.a_scales + (m0 + row) * groups;
-        if (stage * 4 + 4 <= groups) {
-          sc.a[i] = *reinterpret_cast<const __attribute__((aligned(1))) int*>(p + stage * 4);
+        v4u w;
+        if (at + 16 <= left) {
+          w = *reinterpret_cast<const v4u_a1*>(p + row * a_groups + at);
         } else {  // groups past the row's end count as its last one: they meet zeros
-          int w = 0;
+#pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int64_t at = stage * 4 + q;
-            w |= p[at < groups ? at : groups - 1] << (8 * q);
+            w[q] = 0;
+            for (int e = 0; e < 4; ++e) {
+              const int64_t i = at + q * 4 + e < left ? at + q * 4 + e : left - 1;
+              w[q] |= static_cast<uint32_t>(p[row * a_groups + i]) << (8 * e);
+            }
           }
-          sc.a[i] = w;
         }
+        *reinterpret_cast<v4u*>(into + (u * TL::kThreads + id) * 16) = w;
       }
-      int64_t row = n0 + wn, col = stage;
-      if (row >= g.n) row = g.n - 1;
-      // transposed codes: the blocks' rows run along k
-      sc.b = g.b_turned ? g.b_scales[col * g.b_blocks + row / 128] : g.b_scales[row / 128 * g.b_blocks + col];
     }
   };
-  auto settle = [&](Scales& sc) {  // the loads have landed
+  const int scale_row = (wm + (lane & 31)) * 64, scale_turn = ((lane >> 2) & 3) * 16;
+  auto read_scales = [&](int64_t stage, Scales& sc) {
     if constexpr (KIND == kEight) {
+      const int q = static_cast<int>(stage) & 15;
+      const char* p = segments + (static_cast<int>(stage >> 4) & 1) * TL::kSegment + scale_row + (((q >> 2) * 16) ^ scale_turn) + (q & 3) * 4;
 #pragma unroll
-      for (int i = 0; i < TL::FM; ++i) {
-        sc.a[i] = static_cast<int>(static_cast<uint32_t>(sc.a[i]) >> (lane >> 5) * 8);
-        asm volatile("" : "+v"(sc.a[i]));
-      }
-      asm volatile("" : "+v"(sc.b));
+      for (int i = 0; i < TL::FM; ++i)
+        sc.a[i] = static_cast<int>(*reinterpret_cast<const uint32_t*>(p + i * 2048) >> (lane >> 5) * 8);
     }
   };
 
-  // A stage is multiplied in four steps (in two of double depth for 8-bit operands).
-  constexpr int kSteps = KIND == kEight ? 2 : 4, kParts = 4 / kSteps;
-  struct Operands {
-    v8s a[TL::FM][kParts], b[TL::FN][kParts];
-  };
-  auto read = [&](Operands& f, const char* buf, int step) {
+  // A stage is multiplied in four clusters: half h of the wave's rows of a with half q of the stage's
+  // k, (0, 0), (0, 1), (1, 0), (1, 1).  b's fragments are read with the first two and kept.
+  constexpr int kHalf = TL::FM / 2;
+  v8s fa[kHalf][2], fb[2][TL::FN][2];
+  auto multiply = [&](int h, int q, const Scales& sc, auto odd) {
+    if constexpr (KIND == kEight) {
+      typedef short v16s __attribute__((ext_vector_type(16)));
 #pragma unroll
-    for (int q = 0; q < kParts; ++q) {
+      for (int i = 0; i < kHalf; ++i)
 #pragma unroll
-      for (int i = 0; i < TL::FM; ++i) f.a[i][q] = read_a(buf, i, step * kParts + q);
-#pragma unroll
-      for (int j = 0; j < TL::FN; ++j) f.b[j][q] = read_b(buf + kOperandA, j, step * kParts + q);
-    }
-  };
-  auto multiply = [&](const Operands& f, const Scales& sc, auto step) {
-#pragma unroll
-    for (int i = 0; i < TL::FM; ++i)
-#pragma unroll
-      for (int j = 0; j < TL::FN; ++j) {
-        if constexpr (KIND == kEight) {
-          typedef short v16s __attribute__((ext_vector_type(16)));
-          const v16s a = __builtin_shufflevector(f.a[i][0], f.a[i][1], 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
-          const v16s b = __builtin_shufflevector(f.b[j][0], f.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(__builtin_bit_cast(v8i, a), __builtin_bit_cast(v8i, b),
-                                                                      acc[i][j], 0, 0, 2 * decltype(step)::value, sc.a[i], 0, sc.b);
-        } else {
-          acc[i][j] = mfma<KIND>(f.a[i][0], f.b[j][0], acc[i][j]);
+        for (int j = 0; j < TL::FN; ++j) {
+          const v16s a = __builtin_shufflevector(fa[i][0], fa[i][1], 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+          const v16s b = __builtin_shufflevector(fb[q][j][0], fb[q][j][1], 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+          v16f& c = acc[h * kHalf + i][j];
+          c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(__builtin_bit_cast(v8i, a), __builtin_bit_cast(v8i, b), c, 0, 0,
+                                                              2 * decltype(odd)::value, sc.a[h * kHalf + i], 0, sc.b);
         }
-      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i)
+#pragma unroll
+          for (int j = 0; j < TL::FN; ++j)
+            acc[h * kHalf + i][j] = mfma<KIND>(fa[i][e], fb[q][j][e], acc[h * kHalf + i][j]);
+    }
   };
 
   const int64_t stages = (depth + kDepth - 1) / kDepth;
   // stages that lie inside both operands; the others pass through registers
-  const int64_t whole = STAGED ? 0 : KIND == kEight ? std::min(g.a_padded, g.b_padded) / 128 : depth / kDepth;
-  v4u ra[STAGED ? OpA::kLoads : 1], rb[STAGED ? OpB::kLoads : 1];
-  auto begin = [&](int64_t stage, char* buf) {
-    if constexpr (STAGED) {
-      op_a.fetch(stage, ra);
-      op_b.fetch(stage, rb);
-    } else if (stage < whole) {
-      op_a.direct(stage, buf, wave);
-      op_b.direct(stage, buf + kOperandA, wave);
+  const int64_t whole = STAGED ? 0 : KIND == kEight ? g.a_padded / 128 : depth / kDepth;
+  auto buffer_a = [&](int h, int64_t stage) { return lds + (2 * h + (static_cast<int>(stage) & 1)) * TL::kHalfM; };
+  auto buffer_b = [&](int64_t stage) { return lds + 4 * TL::kHalfM + (static_cast<int>(stage) & 1) * TL::kBufferN; };
+  // a stage of an operand into LDS: under way, or done where it takes registers
+  auto begin = [&](const auto& op, int64_t stage, char* buf) {
+    using Op = std::remove_cv_t<std::remove_reference_t<decltype(op)>>;
+    if (stage < whole) {
+      const char* p = op.at(stage);
+#pragma unroll
+      for (int u = 0; u < Op::kLoads; ++u) op.direct(u, p, buf, wave);
     } else {
-      v4u ta[OpA::kLoads], tb[OpB::kLoads];
-      op_a.fetch(stage, ta);
-      op_b.fetch(stage, tb);
-      OpA::leave(ta, buf);
-      OpB::leave(tb, buf + kOperandA);
+      v4u t[Op::kLoads];
+      op.fetch(stage, t);
+      Op::leave(t, buf);
     }
   };
-  auto finish = [&](char* buf) {
-    if constexpr (STAGED) {
-      OpA::leave(ra, buf);
-      OpB::leave(rb, buf + kOperandA);
-    }
-  };
+  // Two groups of waves take turns: while one reads its fragments and sends for later stages, the other,
+  // one barrier ahead or behind, multiplies; each SIMD has a wave of both.  (Where waves are four to a
+  // workgroup, two workgroups on a CU do that for each other, and the barriers within a half of a
+  // stage are left out.)
+  // A half of a, and b, are free once their clusters have been read, and stage i + 2 goes there: b and
+  // the first half from cluster 2 of stage i on, the second half in cluster 0 of stage i + 1.  Each has
+  // a stage and a half of time.  A wave waits for its own pieces one cluster before they are read;
+  // the barrier behind that makes it all waves'.
+  constexpr bool kTurns = TL::kThreads == 512;
   if (stages > 0) {
-    Scales sc[2];
-    Operands f[2];
-    char* cur = lds;
-    char* other = lds + TL::kBuffer;
-    begin(0, cur);
-    fetch_scales(0, sc[0]);
-    finish(cur);
-    __syncthreads();
-    settle(sc[0]);
-    for (int64_t i = 0; i < stages; ++i) {
-      if (i + 1 < stages) {
-        begin(i + 1, other);
-        fetch_scales(i + 1, sc[1]);
+    constexpr std::integral_constant<int, 0> kZero{};
+    constexpr std::integral_constant<int, 1> kOne{};
+    Scales sc;
+    int next_b_scale = 0;
+    auto none = [] {};
+    auto cluster = [&](int h, auto odd, const char* buf_a, const char* buf_b, auto around) {
+      constexpr int q = decltype(odd)::value;
+      if (h == 0) {
+#pragma unroll
+        for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) fb[q][j][e] = read_b(buf_b, j, 2 * q + e);
       }
-      read(f[0], cur, 0);
-      if constexpr (kSteps == 4) {
-        read(f[1], cur, 1);
-        multiply(f[0], sc[0], std::integral_constant<int, 0>{});
-        read(f[0], cur, 2);
-        multiply(f[1], sc[0], std::integral_constant<int, 0>{});
-        read(f[1], cur, 3);
-        multiply(f[0], sc[0], std::integral_constant<int, 0>{});
-        multiply(f[1], sc[0], std::integral_constant<int, 0>{});
-      } else {
-        read(f[1], cur, 1);
-        multiply(f[0], sc[0], std::integral_constant<int, 0>{});
-        multiply(f[1], sc[0], std::integral_constant<int, 1>{});
-      }
-      if (i + 1 < stages) finish(other);
-      __syncthreads();
-      sc[0] = sc[1];
-      settle(sc[0]);
-      char* x = cur;
-      cur = other;
-      other = x;
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) fa[i][e] = read_a(buf_a, i, 2 * q + e);
+      around();
+      wait_lds();
+      if (kTurns) meet();
+      __builtin_amdgcn_s_setprio(1);
+      multiply(h, q, sc, odd);
+      __builtin_amdgcn_s_setprio(0);
+      if (kTurns || q == 1) meet();
+    };
+    begin_segment(0);
+    begin(op_a[0], 0, buffer_a(0, 0));
+    begin(op_b, 0, buffer_b(0));
+    begin(op_a[1], 0, buffer_a(1, 0));
+    if (stages > 1) {
+      begin(op_a[0], 1, buffer_a(0, 1));
+      begin(op_b, 1, buffer_b(1));
     }
+    if constexpr (KIND == kEight) next_b_scale = b_scale[0];
+    wait_loads<0>();
+    wait_lds();
+    meet();
+    if (kTurns && wave >= 4) meet();
+    // MAIN: the new stages go straight to LDS
+    v4u ra0[STAGED ? OpA::kLoads : 1], ra1[STAGED ? OpA::kLoads : 1], rb[STAGED ? OpB::kLoads : 1];
+    auto one_stage = [&](int64_t i, auto main) {
+      constexpr bool kMain = decltype(main)::value;
+      constexpr int kA = OpA::kLoads, kB = OpB::kLoads;
+      char* a0 = buffer_a(0, i);
+      char* a1 = buffer_a(1, i);
+      char* b = buffer_b(i);
+      if constexpr (KIND == kEight) {
+        if ((i & 15) == 8 && (i / 16 + 1) * 16 < stages) begin_segment(i / 16 + 1);
+        read_scales(i, sc);
+        sc.b = next_b_scale;
+        if (kMain || i + 1 < stages) next_b_scale = b_scale[(i + 1) * g.b_scale_step];
+      }
+      const char* pa = op_a[0].at(i + 2);
+      const char* pb = op_b.at(i + 2);
+      cluster(0, kZero, a0, b, [&] {
+        if constexpr (kMain) {
+          const char* p = op_a[1].at(i + 1);
+#pragma unroll
+          for (int u = 0; u < kA; ++u) op_a[1].direct(u, p, buffer_a(1, i + 1), wave);
+        } else if constexpr (STAGED) {
+          if (i + 1 < stages) op_a[1].fetch(i + 1, ra1);
+        } else {
+          if (i + 1 < stages) begin(op_a[1], i + 1, buffer_a(1, i + 1));
+        }
+      });
+      cluster(0, kOne, a0, b, [&] {
+        if constexpr (STAGED) {
+          if (i > 0 && i + 1 < stages) {
+            OpA::leave(ra0, buffer_a(0, i + 1));
+            OpB::leave(rb, buffer_b(i + 1));
+          }
+        }
+        wait_loads<kMain ? 2 * kA + kB : 0>();  // the second half of a
+      });
+      cluster(1, kZero, a1, b, [&] {
+        if constexpr (kMain) {
+#pragma unroll
+          for (int u = 0; u < kA; ++u) op_a[0].direct(u, pa, a0, wave);
+#pragma unroll
+          for (int u = 0; u < kB / 2; ++u) op_b.direct(u, pb, b, wave);
+        } else if constexpr (STAGED) {
+          if (i + 2 < stages) {
+            op_a[0].fetch(i + 2, ra0);
+            op_b.fetch(i + 2, rb);
+          }
+        } else if (i + 2 < stages) {
+          begin(op_a[0], i + 2, a0);
+          begin(op_b, i + 2, b);
+        }
+      });
+      cluster(1, kOne, a1, b, [&] {
+        if constexpr (STAGED) {
+          if (i + 1 < stages) OpA::leave(ra1, buffer_a(1, i + 1));
+        }
+        wait_loads<kMain ? 2 * kA + kB / 2 : 0>();  // the next stage's first half of a, and b
+        if constexpr (kMain) {
+#pragma unroll
+          for (int u = kB / 2; u < kB; ++u) op_b.direct(u, pb, b, wave);
+        }
+      });
+    };
+    int64_t i = 0;
+    for (; i + 2 < whole; ++i) one_stage(i, std::true_type{});
+    for (; i < stages; ++i) one_stage(i, std::false_type{});
+    if (kTurns && wave < 4) meet();
+    meet();  // the strips below reuse the buffers
   }
 
   // The sums leave through LDS, a strip of 32 rows of the wave at a time, so that a lane stores
@@ -543,12 +666,13 @@ using LargeTile = Tile<2, 4, 4, 2>;  // 256 x 256
 template <int KIND, bool AK, bool BK, bool SUM_GROUPS, bool STAGED, class TL>
 hipError_t launch_tile(const ProductArgs& a, hipStream_t s) {
   auto kernel = &k_product<KIND, AK, BK, SUM_GROUPS, STAGED, TL>;
-  if (TL::kLds > 65536) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, TL::kLds);
+  constexpr int kLds = TL::lds(KIND == kEight);
+  if (kLds > 65536) {
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (e != hipSuccess) return e;
   }
   const int64_t units = product_units(a, SUM_GROUPS, TL::kM, TL::kN);
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(launch_units(units, kXcdWhole))), dim3(TL::kThreads), TL::kLds, s, a);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(launch_units(units, kXcdWhole))), dim3(TL::kThreads), kLds, s, a);
   return hipGetLastError();
 }
 
