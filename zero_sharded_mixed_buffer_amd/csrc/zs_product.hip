@@ -464,8 +464,9 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
   // A stage is multiplied in four clusters: half h of the wave's rows of a with half q of the stage's
   // k, (0, 0), (0, 1), (1, 0), (1, 1).  b's fragments are read with the first two and kept.
   constexpr int kHalf = TL::FM / 2;
-  v8s fa[kHalf][2], fb[2][TL::FN][2];
-  auto multiply = [&](int h, int q, const Scales& sc, auto odd) {
+  constexpr bool kJoined = KIND != kEight;
+  v8s fa[kJoined ? 2 : 1][kHalf][2], fb[2][TL::FN][2];
+  auto multiply = [&](int h, int q, const v8s (&fa)[kHalf][2], const Scales& sc, auto odd) {
     if constexpr (KIND == kEight) {
       typedef short v16s __attribute__((ext_vector_type(16)));
 #pragma unroll
@@ -523,24 +524,28 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
     int next_b_scale = 0;
     auto none = [] {};
     auto cluster = [&](int h, auto odd, const char* buf_a, const char* buf_b, auto around) {
-      constexpr int q = decltype(odd)::value;
-      if (h == 0) {
+      constexpr int kFirst = decltype(odd)::value, kLast = kJoined ? 1 : kFirst;
 #pragma unroll
-        for (int j = 0; j < TL::FN; ++j)
+      for (int q = kFirst; q <= kLast; ++q) {
+        if (h == 0) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) fb[q][j][e] = read_b(buf_b, j, 2 * q + e);
+          for (int j = 0; j < TL::FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) fb[q][j][e] = read_b(buf_b, j, 2 * q + e);
+        }
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) fa[q - kFirst][i][e] = read_a(buf_a, i, 2 * q + e);
       }
-#pragma unroll
-      for (int i = 0; i < kHalf; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) fa[i][e] = read_a(buf_a, i, 2 * q + e);
       around();
       wait_lds();
       if (kTurns) meet();
       __builtin_amdgcn_s_setprio(1);
-      multiply(h, q, sc, odd);
+#pragma unroll
+      for (int q = kFirst; q <= kLast; ++q) multiply(h, q, fa[q - kFirst], sc, odd);
       __builtin_amdgcn_s_setprio(0);
-      if (kTurns || q == 1) meet();
+      if (kTurns || kLast == 1) meet();
     };
     begin_segment(0);
     begin(op_a[0], 0, buffer_a(0, 0));
@@ -571,7 +576,7 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
       }
       const char* pa = op_a[0].at(i + 2);
       const char* pb = op_b.at(i + 2);
-      cluster(0, kZero, a0, b, [&] {
+      auto send_a1 = [&] {
         if constexpr (kMain) {
           const char* p = op_a[1].at(i + 1);
 #pragma unroll
@@ -581,42 +586,64 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
         } else {
           if (i + 1 < stages) begin(op_a[1], i + 1, buffer_a(1, i + 1));
         }
-      });
-      cluster(0, kOne, a0, b, [&] {
+      };
+      auto leave_a0_b = [&] {
         if constexpr (STAGED) {
           if (i > 0 && i + 1 < stages) {
             OpA::leave(ra0, buffer_a(0, i + 1));
             OpB::leave(rb, buffer_b(i + 1));
           }
         }
-        wait_loads<kMain ? 2 * kA + kB : 0>();  // the second half of a
-      });
-      cluster(1, kZero, a1, b, [&] {
+      };
+      auto send_a0_b = [&](int from, int to) {  // pieces of b
         if constexpr (kMain) {
+          if (from == 0) {
 #pragma unroll
-          for (int u = 0; u < kA; ++u) op_a[0].direct(u, pa, a0, wave);
+            for (int u = 0; u < kA; ++u) op_a[0].direct(u, pa, a0, wave);
+          }
 #pragma unroll
-          for (int u = 0; u < kB / 2; ++u) op_b.direct(u, pb, b, wave);
-        } else if constexpr (STAGED) {
-          if (i + 2 < stages) {
+          for (int u = from; u < to; ++u) op_b.direct(u, pb, b, wave);
+        } else if (from == 0 && i + 2 < stages) {
+          if constexpr (STAGED) {
             op_a[0].fetch(i + 2, ra0);
             op_b.fetch(i + 2, rb);
+          } else {
+            begin(op_a[0], i + 2, a0);
+            begin(op_b, i + 2, b);
           }
-        } else if (i + 2 < stages) {
-          begin(op_a[0], i + 2, a0);
-          begin(op_b, i + 2, b);
         }
-      });
-      cluster(1, kOne, a1, b, [&] {
+      };
+      auto leave_a1 = [&] {
         if constexpr (STAGED) {
           if (i + 1 < stages) OpA::leave(ra1, buffer_a(1, i + 1));
         }
-        wait_loads<kMain ? 2 * kA + kB / 2 : 0>();  // the next stage's first half of a, and b
-        if constexpr (kMain) {
-#pragma unroll
-          for (int u = kB / 2; u < kB; ++u) op_b.direct(u, pb, b, wave);
-        }
-      });
+      };
+      // how many pieces may be under way behind those that are waited for: the second half of a, then
+      // the next stage's first half and b
+      if constexpr (kJoined) {
+        cluster(0, kZero, a0, b, [&] {
+          leave_a0_b();
+          wait_loads<kMain ? kA + kB : 0>();
+          send_a1();
+        });
+        cluster(1, kZero, a1, b, [&] {
+          wait_loads<kMain ? kA : 0>();
+          send_a0_b(0, kB);
+          leave_a1();
+        });
+      } else {
+        cluster(0, kZero, a0, b, send_a1);
+        cluster(0, kOne, a0, b, [&] {
+          leave_a0_b();
+          wait_loads<kMain ? 2 * kA + kB : 0>();
+        });
+        cluster(1, kZero, a1, b, [&] { send_a0_b(0, kB / 2); });
+        cluster(1, kOne, a1, b, [&] {
+          leave_a1();
+          wait_loads<kMain ? 2 * kA + kB / 2 : 0>();
+          send_a0_b(kB / 2, kB);
+        });
+      }
     };
     int64_t i = 0;
     for (; i + 2 < whole; ++i) one_stage(i, std::true_type{});
