@@ -27,6 +27,7 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8hf __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef v4u v4u_a1 __attribute__((aligned(1)));
@@ -140,6 +141,7 @@ __device__ __forceinline__ v16f mfma(const v8s& a, const v8s& b, const v16f& c) 
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8hf, a), __builtin_bit_cast(v8hf, b), c, 0, 0, 0);
 }
 
+constexpr int64_t kFewRows = 32;  // of a group: see few_rows
 constexpr int kEight = 3;  // the operands' type beside ZS_BF16 and ZS_FP16: e4m3 codes
 
 // One operand of a workgroup, or half of one: R rows of m or n, k from 0 to `depth` (elements).
@@ -685,6 +687,155 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
   }
 }
 
+// ------------------------------------------------------------------ few rows
+
+// Products of at most 16 rows of a at a time, where reading b is most of it: a workgroup takes
+// 16 * NF rows of b, its eight waves every eighth piece of 128 bytes of k, and the waves' sums meet in
+// LDS.  Operands go from memory into the matrix instructions' registers without LDS: a lane's row is
+// lane % 16, and the order of k within a piece is free as long as both operands have the same, so
+// that a lane takes 32 consecutive bytes (16-bit operands; for 8-bit ones the instruction's scales
+// fix which).  Any alignment will do.
+template <int KIND, int NF>
+__global__ __launch_bounds__(512) void k_few(ProductArgs g) {
+  constexpr int kSize = KIND == kEight ? 1 : 2, kDepth = 128 / kSize, kWaves = 8, kAhead = NF == 1 ? 4 : 2;
+  __shared__ __attribute__((aligned(16))) v4f sums[kWaves][NF][64];
+  const int tiles_n = static_cast<int>((g.n + 16 * NF - 1) / (16 * NF));
+  Span s{0, 0, 0};
+  const int tiles_m = find_tile(g.ends, g.groups, g.zero_rest, g.m, 16, -1, &s), units = tiles_m * tiles_n;
+  const int run = (units + kXcds - 1) / kXcds, in_run = blockIdx.x / kXcds, unit = blockIdx.x % kXcds * run + in_run;
+  if (in_run >= run || unit >= units) return;
+  find_tile(g.ends, g.groups, g.zero_rest, g.m, 16, unit % tiles_m, &s);  // tiles of one n are neighbours
+  const int64_t m0 = s.first, n0 = int64_t(unit / tiles_m) * (16 * NF);
+  const bool none = g.ends != nullptr && s.group == g.groups;  // rows behind the last group: zeros
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), row = lane & 15, part = lane >> 4;
+  const int left_m = static_cast<int>(s.last - m0 < 16 ? s.last - m0 : 16);
+
+  v4f acc[NF];
+#pragma unroll
+  for (int j = 0; j < NF; ++j) acc[j] = v4f(0.0f);
+  if (!none) {
+    const int64_t am = m0 + (row < left_m ? row : left_m - 1);
+    const char* pa = static_cast<const char*>(g.a) + am * g.a_stride * kSize;
+    const char* pb[NF];
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      const int64_t n = n0 + j * 16 + row;
+      pb[j] = static_cast<const char*>(g.b) + ((KIND == kEight ? 0 : s.group * g.b_group) + (n < g.n ? n : g.n - 1) * g.b_stride) * kSize;
+    }
+    const int first = part * (KIND == kEight ? 16 : 32), second = first + (KIND == kEight ? 64 : 16);  // bytes
+    struct Piece {
+      v4u a[2], b[NF][2];
+      int a_scale, b_scale;
+    };
+    const int64_t a_groups = g.a_padded / kActGroup;
+    const uint8_t* a_scale = KIND == kEight ? g.a_scales + am * a_groups + part : nullptr;
+    const uint8_t* b_scale = KIND == kEight ? g.b_scales + n0 / kWeightBlock * g.b_scale_row : nullptr;
+    auto fetch = [&](int64_t at, Piece& p) {  // a whole piece
+      const int64_t byte = at * 128;
+      p.a[0] = *reinterpret_cast<const v4u_a2*>(pa + byte + first);
+      p.a[1] = *reinterpret_cast<const v4u_a2*>(pa + byte + second);
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        p.b[j][0] = __builtin_nontemporal_load(reinterpret_cast<const v4u_a2*>(pb[j] + byte + first));
+        p.b[j][1] = __builtin_nontemporal_load(reinterpret_cast<const v4u_a2*>(pb[j] + byte + second));
+      }
+      if constexpr (KIND == kEight) {
+        p.a_scale = a_scale[at * 4];
+        p.b_scale = b_scale[at * g.b_scale_step];
+      }
+    };
+    auto fetch_last = [&](int64_t at, Piece& p) {
+      if constexpr (KIND == kEight) {  // past the row of a: a piece of the same row, which meets zeros
+        const int64_t byte = at * 128, top = g.a_padded - 16;
+        p.a[0] = *reinterpret_cast<const v4u*>(pa + (byte + first < top ? byte + first : top));
+        p.a[1] = *reinterpret_cast<const v4u*>(pa + (byte + second < top ? byte + second : top));
+        const int64_t group = at * 4 + part < a_groups ? at * 4 : a_groups - 1 - part;
+        p.a_scale = a_scale[group];
+        p.b_scale = b_scale[at * g.b_scale_step];
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          p.b[j][0] = *reinterpret_cast<const v4u*>(pb[j] + byte + first);
+          p.b[j][1] = *reinterpret_cast<const v4u*>(pb[j] + byte + second);
+        }
+      } else {
+        const int64_t k = at * kDepth + first / 2, left = g.k - k;
+        auto cnt = [&](int64_t v) { return v >= 8 ? 8 : v > 0 ? static_cast<int>(v) : 0; };
+        p.a[0] = load8h(reinterpret_cast<const uint16_t*>(pa) + k, cnt(left));
+        p.a[1] = load8h(reinterpret_cast<const uint16_t*>(pa) + k + 8, cnt(left - 8));
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          p.b[j][0] = load8h(reinterpret_cast<const uint16_t*>(pb[j]) + k, cnt(left));
+          p.b[j][1] = load8h(reinterpret_cast<const uint16_t*>(pb[j]) + k + 8, cnt(left - 8));
+        }
+      }
+    };
+    auto multiply = [&](const Piece& p) {  // rows of the sums: b's, columns: a's
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        if constexpr (KIND == kEight) {
+          typedef unsigned int v8u __attribute__((ext_vector_type(8)));
+          const v8u a = __builtin_shufflevector(p.a[0], p.a[1], 0, 1, 2, 3, 4, 5, 6, 7);
+          const v8u b = __builtin_shufflevector(p.b[j][0], p.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+          acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(v8i, b), __builtin_bit_cast(v8i, a), acc[j], 0, 0,
+                                                                    0, p.b_scale, 0, p.a_scale);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if constexpr (KIND == ZS_BF16)
+              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, p.b[j][e]), __builtin_bit_cast(v8bf, p.a[e]),
+                                                               acc[j], 0, 0, 0);
+            else
+              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8hf, p.b[j][e]), __builtin_bit_cast(v8hf, p.a[e]),
+                                                              acc[j], 0, 0, 0);
+          }
+        }
+      }
+    };
+    const int64_t pieces = (g.k + kDepth - 1) / kDepth, whole = KIND == kEight ? g.a_padded / 128 : g.k / kDepth;
+    int64_t at = wave;
+    Piece p[kAhead];
+    for (; at + (kAhead - 1) * kWaves < whole; at += kAhead * kWaves) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) fetch(at + u * kWaves, p[u]);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) multiply(p[u]);
+    }
+    for (; at < pieces; at += kWaves) {
+      if (at < whole) fetch(at, p[0]);
+      else fetch_last(at, p[0]);
+      multiply(p[0]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NF; ++j) sums[wave][j][lane] = acc[j];
+  __syncthreads();
+  if (wave >= NF) return;
+  v4f sum = sums[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) sum += sums[w][wave][lane];
+  // a lane has four consecutive columns of c's row `row`
+  const int64_t n = n0 + wave * 16 + part * 4, at = (m0 + row) * g.c_stride + n;
+  if (row >= left_m) return;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (n + r >= g.n) break;
+    uint16_t* c = static_cast<uint16_t*>(g.c) + at + r;
+    *c = static_cast<uint16_t>(g.c_dt == ZS_BF16 ? half_bits<ZS_BF16>(sum[r]) : half_bits<ZS_FP16>(sum[r]));
+  }
+}
+
+template <int KIND>
+hipError_t launch_few(const ProductArgs& a, hipStream_t s) {
+  const bool wide = product_units(a, false, 16, 32) >= 512;
+  const int64_t units = product_units(a, false, 16, wide ? 32 : 16);
+  auto kernel = wide ? &k_few<KIND, 2> : &k_few<KIND, 1>;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(launch_units(units, kXcdWhole))), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+// Whether the rows are so few that reading b once for each 16 of them is the better way.
+bool few_rows(const ProductArgs& a) { return a.m <= kFewRows * int64_t(a.groups); }
+
 using SmallTile = Tile<2, 2, 2, 2>;  // 128 x 128
 using LargeTile = Tile<2, 4, 4, 2>;  // 256 x 256
 
@@ -713,6 +864,9 @@ bool direct_rows(const void* p, int64_t stride, int64_t group) {
 
 template <int KIND, bool AK, bool BK, bool SUM_GROUPS>
 hipError_t launch_sizes(const ProductArgs& a, hipStream_t s) {
+  if constexpr (!AK && !BK && !SUM_GROUPS) {
+    if (few_rows(a)) return launch_few<KIND>(a, s);
+  }
   const bool direct = direct_rows(a.a, a.a_stride, 0) && direct_rows(a.b, a.b_stride, a.b_group) && (!AK || a.m % 8 == 0) &&
                       (!BK || a.n % 8 == 0);
   if (!direct) return launch_tile<KIND, AK, BK, SUM_GROUPS, true, SmallTile>(a, s);
@@ -732,6 +886,7 @@ int64_t product_units(const ProductArgs& a, bool sum_groups, int64_t tile_m, int
 }
 
 hipError_t launch_product8(const ProductArgs& a, hipStream_t s) {
+  if (few_rows(a)) return launch_few<kEight>(a, s);
   if (product_units(a, false, LargeTile::kM, LargeTile::kN) >= 200)
     return launch_tile<kEight, false, false, false, false, LargeTile>(a, s);
   return launch_tile<kEight, false, false, false, false, SmallTile>(a, s);
