@@ -32,15 +32,15 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef v4u v4u_a1 __attribute__((aligned(1)));
 
-// A workgroup's tile: WM x WN waves, each FM x FN matrix instructions of 32 x 32.
-template <int WM_, int WN_, int FM_, int FN_>
+// A workgroup's tile: WM x WN waves, each FM x FN matrix instructions of 32 x 32; DEPTH stages in LDS.
+template <int WM_, int WN_, int FM_, int FN_, int DEPTH_>
 struct Tile {
-  static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_;
+  static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_, kStages = DEPTH_;
   static constexpr int kThreads = WM * WN * 64;
   static constexpr int kM = WM * FM * 32, kN = WN * FN * 32;
   // bytes of a stage of half of a's rows, and of b's
   static constexpr int kHalfM = kM / 2 * 128, kBufferN = kN * 128;
-  static constexpr int kBuffers = 4 * kHalfM + 2 * kBufferN;
+  static constexpr int kBuffers = kStages * (2 * kHalfM + kBufferN);
   static constexpr int kSegment = kM * 64;  // a's scales (8-bit operands): 64 bytes of each row, twice
   static constexpr int kStripPitch = FN * 32 + 8;  // the epilogue's strips, as in the weight gradient
   static constexpr int kStrips = WM * WN * 32 * kStripPitch * 4;
@@ -49,7 +49,7 @@ struct Tile {
     return all > kStrips ? all : kStrips;
   }
   static_assert(lds(true) <= 163840, "LDS of a CU");
-  static_assert(FM % 2 == 0 && kThreads % 64 == 0 && kM >= 128 && kN >= 128, "halves, and blocks that change places");
+  static_assert((kStages & (kStages - 1)) == 0 && FM % 2 == 0 && kThreads % 64 == 0 && kM >= 128 && kN >= 128, "halves, and blocks that change places");
 };
 
 // ------------------------------------------------------------------ groups of rows
@@ -141,7 +141,8 @@ __device__ __forceinline__ v16f mfma(const v8s& a, const v8s& b, const v16f& c) 
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8hf, a), __builtin_bit_cast(v8hf, b), c, 0, 0, 0);
 }
 
-constexpr int64_t kFewRows = 32;  // of a group: see few_rows
+constexpr int64_t kFewUnits = 512;  // see few_rows
+constexpr int64_t kCus = 256;
 constexpr int kEight = 3;  // the operands' type beside ZS_BF16 and ZS_FP16: e4m3 codes
 
 // One operand of a workgroup, or half of one: R rows of m or n, k from 0 to `depth` (elements).
@@ -495,8 +496,11 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
   const int64_t stages = (depth + kDepth - 1) / kDepth;
   // stages that lie inside both operands; the others pass through registers
   const int64_t whole = STAGED ? 0 : KIND == kEight ? g.a_padded / 128 : depth / kDepth;
-  auto buffer_a = [&](int h, int64_t stage) { return lds + (2 * h + (static_cast<int>(stage) & 1)) * TL::kHalfM; };
-  auto buffer_b = [&](int64_t stage) { return lds + 4 * TL::kHalfM + (static_cast<int>(stage) & 1) * TL::kBufferN; };
+  constexpr int kBufs = TL::kStages;
+  auto buffer_a = [&](int h, int64_t stage) { return lds + (kBufs * h + (static_cast<int>(stage) & (kBufs - 1))) * TL::kHalfM; };
+  auto buffer_b = [&](int64_t stage) {
+    return lds + 2 * kBufs * TL::kHalfM + (static_cast<int>(stage) & (kBufs - 1)) * TL::kBufferN;
+  };
   // a stage of an operand into LDS: under way, or done where it takes registers
   auto begin = [&](const auto& op, int64_t stage, char* buf) {
     using Op = std::remove_cv_t<std::remove_reference_t<decltype(op)>>;
@@ -514,11 +518,12 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
   // one barrier ahead or behind, multiplies; each SIMD has a wave of both.  (Where waves are four to a
   // workgroup, two workgroups on a CU do that for each other, and the barriers within a half of a
   // stage are left out.)
-  // A half of a, and b, are free once their clusters have been read, and stage i + 2 goes there: b and
-  // the first half from cluster 2 of stage i on, the second half in cluster 0 of stage i + 1.  Each has
-  // a stage and a half of time.  A wave waits for its own pieces one cluster before they are read;
+  // A half of a, and b, are free once their clusters have been read, and a later stage goes there, i + 2
+  // with two buffers: b and the first half from cluster 2 of stage i on, the second half in cluster 0 of
+  // stage i + 1.  Each has a stage and a half of time, with four buffers three and a half.  A wave waits for its own pieces one cluster before they are read;
   // the barrier behind that makes it all waves'.
   constexpr bool kTurns = TL::kThreads == 512;
+  static_assert(!STAGED || kBufs == 2, "a stage in registers, one in LDS beside the present one");
   if (stages > 0) {
     constexpr std::integral_constant<int, 0> kZero{};
     constexpr std::integral_constant<int, 1> kOne{};
@@ -550,12 +555,10 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
       if (kTurns || kLast == 1) meet();
     };
     begin_segment(0);
-    begin(op_a[0], 0, buffer_a(0, 0));
-    begin(op_b, 0, buffer_b(0));
-    begin(op_a[1], 0, buffer_a(1, 0));
-    if (stages > 1) {
-      begin(op_a[0], 1, buffer_a(0, 1));
-      begin(op_b, 1, buffer_b(1));
+    for (int64_t i = 0; i < kBufs && i < stages; ++i) {
+      begin(op_a[0], i, buffer_a(0, i));
+      begin(op_b, i, buffer_b(i));
+      if (i < kBufs - 1) begin(op_a[1], i, buffer_a(1, i));
     }
     if constexpr (KIND == kEight) next_b_scale = b_scale[0];
     wait_loads<0>();
@@ -576,17 +579,17 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
         sc.b = next_b_scale;
         if (kMain || i + 1 < stages) next_b_scale = b_scale[(i + 1) * g.b_scale_step];
       }
-      const char* pa = op_a[0].at(i + 2);
-      const char* pb = op_b.at(i + 2);
+      const char* pa = op_a[0].at(i + kBufs);
+      const char* pb = op_b.at(i + kBufs);
       auto send_a1 = [&] {
         if constexpr (kMain) {
-          const char* p = op_a[1].at(i + 1);
+          const char* p = op_a[1].at(i + kBufs - 1);
 #pragma unroll
-          for (int u = 0; u < kA; ++u) op_a[1].direct(u, p, buffer_a(1, i + 1), wave);
+          for (int u = 0; u < kA; ++u) op_a[1].direct(u, p, buffer_a(1, i + kBufs - 1), wave);
         } else if constexpr (STAGED) {
           if (i + 1 < stages) op_a[1].fetch(i + 1, ra1);
         } else {
-          if (i + 1 < stages) begin(op_a[1], i + 1, buffer_a(1, i + 1));
+          if (i + kBufs - 1 < stages) begin(op_a[1], i + kBufs - 1, buffer_a(1, i + kBufs - 1));
         }
       };
       auto leave_a0_b = [&] {
@@ -605,13 +608,13 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
           }
 #pragma unroll
           for (int u = from; u < to; ++u) op_b.direct(u, pb, b, wave);
-        } else if (from == 0 && i + 2 < stages) {
+        } else if (from == 0 && i + kBufs < stages) {
           if constexpr (STAGED) {
-            op_a[0].fetch(i + 2, ra0);
-            op_b.fetch(i + 2, rb);
+            op_a[0].fetch(i + kBufs, ra0);
+            op_b.fetch(i + kBufs, rb);
           } else {
-            begin(op_a[0], i + 2, a0);
-            begin(op_b, i + 2, b);
+            begin(op_a[0], i + kBufs, a0);
+            begin(op_b, i + kBufs, b);
           }
         }
       };
@@ -625,11 +628,11 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
       if constexpr (kJoined) {
         cluster(0, kZero, a0, b, [&] {
           leave_a0_b();
-          wait_loads<kMain ? kA + kB : 0>();
+          wait_loads<kMain ? (kBufs - 1) * (kA + kB) + (kBufs - 2) * kA : 0>();
           send_a1();
         });
         cluster(1, kZero, a1, b, [&] {
-          wait_loads<kMain ? kA : 0>();
+          wait_loads<kMain ? (kBufs - 1) * kA + (kBufs - 2) * (kA + kB) : 0>();
           send_a0_b(0, kB);
           leave_a1();
         });
@@ -637,18 +640,18 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
         cluster(0, kZero, a0, b, send_a1);
         cluster(0, kOne, a0, b, [&] {
           leave_a0_b();
-          wait_loads<kMain ? 2 * kA + kB : 0>();
+          wait_loads<kMain ? (kBufs - 1) * (kA + kB) + (kBufs - 1) * kA : 0>();
         });
         cluster(1, kZero, a1, b, [&] { send_a0_b(0, kB / 2); });
         cluster(1, kOne, a1, b, [&] {
           leave_a1();
-          wait_loads<kMain ? 2 * kA + kB / 2 : 0>();
+          wait_loads<kMain ? kBufs * kA + kB / 2 + (kBufs - 2) * (kA + kB) : 0>();
           send_a0_b(kB / 2, kB);
         });
       }
     };
     int64_t i = 0;
-    for (; i + 2 < whole; ++i) one_stage(i, std::true_type{});
+    for (; i + kBufs < whole; ++i) one_stage(i, std::true_type{});
     for (; i < stages; ++i) one_stage(i, std::false_type{});
     if (kTurns && wave < 4) meet();
     meet();  // the strips below reuse the buffers
@@ -689,33 +692,42 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
 
 // ------------------------------------------------------------------ few rows
 
-// Products of at most 16 rows of a at a time, where reading b is most of it: a workgroup takes
-// 16 * NF rows of b, its eight waves every eighth piece of 128 bytes of k, and the waves' sums meet in
+// Products of 16 * MF rows of a at a time, where reading b is most of it: a workgroup takes 16 * NF
+// rows of b, its eight waves every eighth piece of 128 bytes of k, and the waves' sums meet in
 // LDS.  Operands go from memory into the matrix instructions' registers without LDS: a lane's row is
 // lane % 16, and the order of k within a piece is free as long as both operands have the same, so
 // that a lane takes 32 consecutive bytes (16-bit operands; for 8-bit ones the instruction's scales
 // fix which).  Any alignment will do.
-template <int KIND, int NF>
+template <int KIND, int MF, int NF>
 __global__ __launch_bounds__(512) void k_few(ProductArgs g) {
-  constexpr int kSize = KIND == kEight ? 1 : 2, kDepth = 128 / kSize, kWaves = 8, kAhead = NF == 1 ? 4 : 2;
-  __shared__ __attribute__((aligned(16))) v4f sums[kWaves][NF][64];
+  constexpr int kSize = KIND == kEight ? 1 : 2, kDepth = 128 / kSize, kWaves = 8, kAhead = MF * NF == 1 ? 4 : 2, kTileM = 16 * MF;
+  __shared__ __attribute__((aligned(16))) v4f sums[kWaves][MF * NF][64];
   const int tiles_n = static_cast<int>((g.n + 16 * NF - 1) / (16 * NF));
   Span s{0, 0, 0};
-  const int tiles_m = find_tile(g.ends, g.groups, g.zero_rest, g.m, 16, -1, &s), units = tiles_m * tiles_n;
+  const int tiles_m = find_tile(g.ends, g.groups, g.zero_rest, g.m, kTileM, -1, &s), units = tiles_m * tiles_n;
   const int run = (units + kXcds - 1) / kXcds, in_run = blockIdx.x / kXcds, unit = blockIdx.x % kXcds * run + in_run;
   if (in_run >= run || unit >= units) return;
-  find_tile(g.ends, g.groups, g.zero_rest, g.m, 16, unit % tiles_m, &s);  // tiles of one n are neighbours
+  find_tile(g.ends, g.groups, g.zero_rest, g.m, kTileM, unit % tiles_m, &s);  // tiles of one n are neighbours
   const int64_t m0 = s.first, n0 = int64_t(unit / tiles_m) * (16 * NF);
   const bool none = g.ends != nullptr && s.group == g.groups;  // rows behind the last group: zeros
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), row = lane & 15, part = lane >> 4;
-  const int left_m = static_cast<int>(s.last - m0 < 16 ? s.last - m0 : 16);
+  const int left_m = static_cast<int>(s.last - m0 < kTileM ? s.last - m0 : kTileM);
 
-  v4f acc[NF];
+  v4f acc[MF][NF];
 #pragma unroll
-  for (int j = 0; j < NF; ++j) acc[j] = v4f(0.0f);
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j) acc[i][j] = v4f(0.0f);
   if (!none) {
-    const int64_t am = m0 + (row < left_m ? row : left_m - 1);
-    const char* pa = static_cast<const char*>(g.a) + am * g.a_stride * kSize;
+    const int64_t a_groups = g.a_padded / kActGroup;
+    const char* pa[MF];
+    const uint8_t* a_scale[MF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      const int64_t m = m0 + (i * 16 + row < left_m ? i * 16 + row : left_m - 1);
+      pa[i] = static_cast<const char*>(g.a) + m * g.a_stride * kSize;
+      a_scale[i] = KIND == kEight ? g.a_scales + m * a_groups + part : nullptr;
+    }
     const char* pb[NF];
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
@@ -724,33 +736,35 @@ __global__ __launch_bounds__(512) void k_few(ProductArgs g) {
     }
     const int first = part * (KIND == kEight ? 16 : 32), second = first + (KIND == kEight ? 64 : 16);  // bytes
     struct Piece {
-      v4u a[2], b[NF][2];
-      int a_scale, b_scale;
+      v4u a[MF][2], b[NF][2];
+      int a_scale[MF], b_scale;
     };
-    const int64_t a_groups = g.a_padded / kActGroup;
-    const uint8_t* a_scale = KIND == kEight ? g.a_scales + am * a_groups + part : nullptr;
     const uint8_t* b_scale = KIND == kEight ? g.b_scales + n0 / kWeightBlock * g.b_scale_row : nullptr;
     auto fetch = [&](int64_t at, Piece& p) {  // a whole piece
       const int64_t byte = at * 128;
-      p.a[0] = *reinterpret_cast<const v4u_a2*>(pa + byte + first);
-      p.a[1] = *reinterpret_cast<const v4u_a2*>(pa + byte + second);
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        p.a[i][0] = *reinterpret_cast<const v4u_a2*>(pa[i] + byte + first);
+        p.a[i][1] = *reinterpret_cast<const v4u_a2*>(pa[i] + byte + second);
+        if constexpr (KIND == kEight) p.a_scale[i] = a_scale[i][at * 4];
+      }
 #pragma unroll
       for (int j = 0; j < NF; ++j) {
         p.b[j][0] = __builtin_nontemporal_load(reinterpret_cast<const v4u_a2*>(pb[j] + byte + first));
         p.b[j][1] = __builtin_nontemporal_load(reinterpret_cast<const v4u_a2*>(pb[j] + byte + second));
       }
-      if constexpr (KIND == kEight) {
-        p.a_scale = a_scale[at * 4];
-        p.b_scale = b_scale[at * g.b_scale_step];
-      }
+      if constexpr (KIND == kEight) p.b_scale = b_scale[at * g.b_scale_step];
     };
     auto fetch_last = [&](int64_t at, Piece& p) {
       if constexpr (KIND == kEight) {  // past the row of a: a piece of the same row, which meets zeros
         const int64_t byte = at * 128, top = g.a_padded - 16;
-        p.a[0] = *reinterpret_cast<const v4u*>(pa + (byte + first < top ? byte + first : top));
-        p.a[1] = *reinterpret_cast<const v4u*>(pa + (byte + second < top ? byte + second : top));
         const int64_t group = at * 4 + part < a_groups ? at * 4 : a_groups - 1 - part;
-        p.a_scale = a_scale[group];
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          p.a[i][0] = *reinterpret_cast<const v4u*>(pa[i] + (byte + first < top ? byte + first : top));
+          p.a[i][1] = *reinterpret_cast<const v4u*>(pa[i] + (byte + second < top ? byte + second : top));
+          p.a_scale[i] = a_scale[i][group];
+        }
         p.b_scale = b_scale[at * g.b_scale_step];
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
@@ -760,8 +774,11 @@ __global__ __launch_bounds__(512) void k_few(ProductArgs g) {
       } else {
         const int64_t k = at * kDepth + first / 2, left = g.k - k;
         auto cnt = [&](int64_t v) { return v >= 8 ? 8 : v > 0 ? static_cast<int>(v) : 0; };
-        p.a[0] = load8h(reinterpret_cast<const uint16_t*>(pa) + k, cnt(left));
-        p.a[1] = load8h(reinterpret_cast<const uint16_t*>(pa) + k + 8, cnt(left - 8));
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          p.a[i][0] = load8h(reinterpret_cast<const uint16_t*>(pa[i]) + k, cnt(left));
+          p.a[i][1] = load8h(reinterpret_cast<const uint16_t*>(pa[i]) + k + 8, cnt(left - 8));
+        }
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
           p.b[j][0] = load8h(reinterpret_cast<const uint16_t*>(pb[j]) + k, cnt(left));
@@ -771,25 +788,28 @@ __global__ __launch_bounds__(512) void k_few(ProductArgs g) {
     };
     auto multiply = [&](const Piece& p) {  // rows of the sums: b's, columns: a's
 #pragma unroll
-      for (int j = 0; j < NF; ++j) {
-        if constexpr (KIND == kEight) {
-          typedef unsigned int v8u __attribute__((ext_vector_type(8)));
-          const v8u a = __builtin_shufflevector(p.a[0], p.a[1], 0, 1, 2, 3, 4, 5, 6, 7);
-          const v8u b = __builtin_shufflevector(p.b[j][0], p.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-          acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(v8i, b), __builtin_bit_cast(v8i, a), acc[j], 0, 0,
-                                                                    0, p.b_scale, 0, p.a_scale);
-        } else {
+      for (int i = 0; i < MF; ++i)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if constexpr (KIND == ZS_BF16)
-              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, p.b[j][e]), __builtin_bit_cast(v8bf, p.a[e]),
-                                                               acc[j], 0, 0, 0);
-            else
-              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8hf, p.b[j][e]), __builtin_bit_cast(v8hf, p.a[e]),
-                                                              acc[j], 0, 0, 0);
+        for (int j = 0; j < NF; ++j) {
+          v4f& c = acc[i][j];
+          if constexpr (KIND == kEight) {
+            typedef unsigned int v8u __attribute__((ext_vector_type(8)));
+            const v8u a = __builtin_shufflevector(p.a[i][0], p.a[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            const v8u b = __builtin_shufflevector(p.b[j][0], p.b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+            c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(v8i, b), __builtin_bit_cast(v8i, a), c, 0, 0, 0,
+                                                                 p.b_scale, 0, p.a_scale[i]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if constexpr (KIND == ZS_BF16)
+                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, p.b[j][e]), __builtin_bit_cast(v8bf, p.a[i][e]), c,
+                                                            0, 0, 0);
+              else
+                c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8hf, p.b[j][e]), __builtin_bit_cast(v8hf, p.a[i][e]), c, 0,
+                                                           0, 0);
+            }
           }
         }
-      }
     };
     const int64_t pieces = (g.k + kDepth - 1) / kDepth, whole = KIND == kEight ? g.a_padded / 128 : g.k / kDepth;
     int64_t at = wave;
@@ -807,15 +827,18 @@ __global__ __launch_bounds__(512) void k_few(ProductArgs g) {
     }
   }
 #pragma unroll
-  for (int j = 0; j < NF; ++j) sums[wave][j][lane] = acc[j];
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j) sums[wave][i * NF + j][lane] = acc[i][j];
   __syncthreads();
-  if (wave >= NF) return;
+  if (wave >= MF * NF) return;
   v4f sum = sums[0][wave][lane];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) sum += sums[w][wave][lane];
-  // a lane has four consecutive columns of c's row `row`
-  const int64_t n = n0 + wave * 16 + part * 4, at = (m0 + row) * g.c_stride + n;
-  if (row >= left_m) return;
+  // a lane has four consecutive columns of one of c's rows
+  const int m = wave / NF * 16 + row;
+  const int64_t n = n0 + wave % NF * 16 + part * 4, at = (m0 + m) * g.c_stride + n;
+  if (m >= left_m) return;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if (n + r >= g.n) break;
@@ -824,20 +847,29 @@ __global__ __launch_bounds__(512) void k_few(ProductArgs g) {
   }
 }
 
-template <int KIND>
-hipError_t launch_few(const ProductArgs& a, hipStream_t s) {
-  const bool wide = product_units(a, false, 16, 32) >= 512;
-  const int64_t units = product_units(a, false, 16, wide ? 32 : 16);
-  auto kernel = wide ? &k_few<KIND, 2> : &k_few<KIND, 1>;
+template <int KIND, int MF>
+hipError_t launch_few_rows(const ProductArgs& a, hipStream_t s) {
+  const bool wide = product_units(a, false, 16 * MF, 32) >= 512;
+  const int64_t units = product_units(a, false, 16 * MF, wide ? 32 : 16);
+  auto kernel = wide ? &k_few<KIND, MF, 2> : &k_few<KIND, MF, 1>;
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(launch_units(units, kXcdWhole))), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
-// Whether the rows are so few that reading b once for each 16 of them is the better way.
-bool few_rows(const ProductArgs& a) { return a.m <= kFewRows * int64_t(a.groups); }
+template <int KIND>
+hipError_t launch_few(const ProductArgs& a, hipStream_t s) {
+  return a.m <= 16 * int64_t(a.groups) ? launch_few_rows<KIND, 1>(a, s) : launch_few_rows<KIND, 2>(a, s);
+}
 
-using SmallTile = Tile<2, 2, 2, 2>;  // 128 x 128
-using LargeTile = Tile<2, 4, 4, 2>;  // 256 x 256
+// Whether k_few is the better way: a unit of it takes k times 1.07 ns per 128 bytes (8 KB of operands),
+// a workgroup of the tiles below about 0.75 us for the same k as long as there are no more of them than
+// CUs.  Measured in 8 bits, k_few and tiles: 128 x 4096 -> 4096 (512 units) 22 and 26 us, 256 rows 40 and 26;
+// 512 x 1003 -> 517 (272 units) 8 and 12; 32 x 4096 -> 14336 (448 units) 34 and 36.
+bool few_rows(const ProductArgs& a) { return product_units(a, false, 32, 32) <= kFewUnits; }
+
+using SmallTile = Tile<2, 2, 2, 2, 2>;  // 128 x 128, two workgroups to a CU
+using DeepTile = Tile<2, 2, 2, 2, 4>;   // the same for launches that have a CU for each workgroup
+using LargeTile = Tile<2, 4, 4, 2, 2>;  // 256 x 256
 
 // ------------------------------------------------------------------ launch choices
 
@@ -873,6 +905,8 @@ hipError_t launch_sizes(const ProductArgs& a, hipStream_t s) {
   const int64_t per_group = SUM_GROUPS ? a.m : a.m / std::max(1, a.groups);
   if (per_group >= 192 && a.n >= 192 && product_units(a, SUM_GROUPS, LargeTile::kM, LargeTile::kN) >= 200)
     return launch_tile<KIND, AK, BK, SUM_GROUPS, false, LargeTile>(a, s);
+  if (product_units(a, SUM_GROUPS, DeepTile::kM, DeepTile::kN) <= kCus)
+    return launch_tile<KIND, AK, BK, SUM_GROUPS, false, DeepTile>(a, s);
   return launch_tile<KIND, AK, BK, SUM_GROUPS, false, SmallTile>(a, s);
 }
 
@@ -889,6 +923,8 @@ hipError_t launch_product8(const ProductArgs& a, hipStream_t s) {
   if (few_rows(a)) return launch_few<kEight>(a, s);
   if (product_units(a, false, LargeTile::kM, LargeTile::kN) >= 200)
     return launch_tile<kEight, false, false, false, false, LargeTile>(a, s);
+  if (product_units(a, false, DeepTile::kM, DeepTile::kN) <= kCus)
+    return launch_tile<kEight, false, false, false, false, DeepTile>(a, s);
   return launch_tile<kEight, false, false, false, false, SmallTile>(a, s);
 }
 
