@@ -132,17 +132,19 @@ zs_status zs_expert_combine(const void* y, int64_t y_stride, zs_dtype dtype, con
                             const float* weights, int64_t tokens, int32_t choices, int64_t cols, void* out,
                             int64_t out_stride, void* stream);
 
-/* Backward pass of zs_expert_combine, for each row p with choice s = slot[p] of token t:
- *   dy[p] = weights[s] * dout[t], zeros where p holds no expert's choice;
- *   dweights[s] = sum over columns of dout[t] * y[p], in fp32; 0 for a choice without expert.
+/* Backward pass of zs_expert_combine, for each token t and its choice j in row p = place[t][j]:
+ *   dy[p] = weights[t][j] * dout[t];  dweights[t][j] = sum over columns of dout[t] * y[p], in fp32.
+ * A choice whose place is not within 0 .. tokens * choices - 1 has the weight gradient 0; a row p with
+ * slot[p] < 0 gets zeros.  (With zs_route's slot and place every row of dy is written; a place that
+ * two choices share, which no route has, gets one of the two.)
  *   dy: NULL or a matrix like y.  dweights: NULL or tokens x choices fp32; needs y, which may be
  *   NULL otherwise.  dy may be y itself (same stride).
  * Errors: as zs_expert_gather, and ZS_EINVAL when neither output is given or dy is in y's place at
  * another stride. */
 zs_status zs_expert_combine_backward(const void* dout, int64_t dout_stride, const void* y, int64_t y_stride,
-                                     zs_dtype dtype, const int32_t* slot, const float* weights, int64_t tokens,
-                                     int32_t choices, int64_t cols, void* dy, int64_t dy_stride, float* dweights,
-                                     void* stream);
+                                     zs_dtype dtype, const int32_t* slot, const int32_t* place,
+                                     const float* weights, int64_t tokens, int32_t choices, int64_t cols, void* dy,
+                                     int64_t dy_stride, float* dweights, void* stream);
 
 #ifdef __cplusplus
 }

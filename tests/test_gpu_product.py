@@ -388,7 +388,13 @@ def test_gather_and_combine_bounds(Z):
     Z.expert_combine(y, r, got)
     want, size = PO.combine(y, r.place)
     _assert_within(got, want, 2 * choices * U * size + _last_rounding(want, BF16), "combine")
-    dy, dweights = torch.empty_like(y), torch.full((tokens, choices), 7.0, device="cuda")
+    # by places; rows whose slot is below 0 are cleared, rows that neither names stay
+    dy, dweights = torch.full_like(y, 7.0), torch.full((tokens, choices), 7.0, device="cuda")
     Z.expert_combine_backward(x, y, r, None, dy, dweights)
-    dy_want, _, _ = PO.combine_backward(x, y, bad, choices)
-    assert torch.equal(dy.cpu().double(), dy_want)
+    want, dots = torch.full((8, cols), 7.0, dtype=BF16), torch.zeros(tokens, choices)
+    want[4:7] = 0
+    for t, j, p in ((0, 0, 0), (1, 1, 3), (3, 1, 7)):
+        want[p] = x[t].cpu()
+        dots[t, j] = (x[t].double() @ y[p].double()).cpu()
+    assert torch.equal(dy.cpu(), want)
+    _assert_within(dweights, dots.double(), 2 * (cols + 8) * U * dots.double().abs() + 64 * U, "dweights")

@@ -123,8 +123,8 @@ _SIGS = {
     "zs_expert_gather": [c_void_p, c_int64, c_int32, c_void_p, c_int64, c_int32, c_int64, c_void_p, c_int64, c_void_p],
     "zs_expert_combine": [c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_int64, c_int32, c_int64, c_void_p, c_int64,
                           c_void_p],
-    "zs_expert_combine_backward": [c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_int64, c_int32,
-                                   c_int64, c_void_p, c_int64, c_void_p, c_void_p],
+    "zs_expert_combine_backward": [c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_int64,
+                                   c_int32, c_int64, c_void_p, c_int64, c_void_p, c_void_p],
     "zs_offload_adamw_step": [c_void_p, c_void_p, c_int32, c_void_p, POINTER(AdamwHParams), c_void_p, c_void_p,
                               c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p],
 }
@@ -593,10 +593,10 @@ def zs_expert_combine(y, y_stride, dtype, place, weights, tokens, choices, cols,
                                    _stream(stream)), w)
 
 
-def zs_expert_combine_backward(dout, dout_stride, y, y_stride, dtype, slot, weights, tokens, choices, cols, dy=None,
-                               dy_stride=0, dweights=None, stream=None):
+def zs_expert_combine_backward(dout, dout_stride, y, y_stride, dtype, slot, place, weights, tokens, choices, cols,
+                               dy=None, dy_stride=0, dweights=None, stream=None):
     w = "zs_expert_combine_backward"
     _check(lib().zs_expert_combine_backward(_dptr(dout, "dout", w), dout_stride, _dptr(y, "y", w), y_stride,
-                                            dtype_code(dtype), _dptr(slot, "slot", w), _dptr(weights, "weights", w),
-                                            tokens, choices, cols, _dptr(dy, "dy", w), dy_stride,
-                                            _dptr(dweights, "dweights", w), _stream(stream)), w)
+                                            dtype_code(dtype), _dptr(slot, "slot", w), _dptr(place, "place", w),
+                                            _dptr(weights, "weights", w), tokens, choices, cols, _dptr(dy, "dy", w),
+                                            dy_stride, _dptr(dweights, "dweights", w), _stream(stream)), w)

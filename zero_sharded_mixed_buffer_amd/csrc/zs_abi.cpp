@@ -1479,9 +1479,9 @@ extern "C" zs_status zs_expert_combine(const void* y, int64_t y_stride, zs_dtype
 }
 
 extern "C" zs_status zs_expert_combine_backward(const void* dout, int64_t dout_stride, const void* y, int64_t y_stride,
-                                                zs_dtype dtype, const int32_t* slot, const float* weights, int64_t tokens,
-                                                int32_t choices, int64_t cols, void* dy, int64_t dy_stride,
-                                                float* dweights, void* stream) {
+                                                zs_dtype dtype, const int32_t* slot, const int32_t* place,
+                                                const float* weights, int64_t tokens, int32_t choices, int64_t cols,
+                                                void* dy, int64_t dy_stride, float* dweights, void* stream) {
   const TraceRange trace("zs_expert_combine_backward");
   zs_status st = check_routing(tokens, choices, cols, dtype);
   const int64_t rows = st == ZS_OK ? tokens * choices : 0;
@@ -1490,6 +1490,7 @@ extern "C" zs_status zs_expert_combine_backward(const void* dout, int64_t dout_s
   st = check_matrix(dout, dout_stride, dtype, tokens, cols, "dout");
   if (st == ZS_OK && dweights != nullptr) st = check_matrix(y, y_stride, dtype, rows, cols, "y");
   if (st == ZS_OK) st = check_words(slot, rows, "slot");
+  if (st == ZS_OK) st = check_words(place, rows, "place");
   if (st == ZS_OK) st = check_words(weights, 0, "weights");
   if (st == ZS_OK) st = check_words(dweights, 0, "dweights");
   if (st == ZS_OK && dy != nullptr) st = check_matrix(dy, dy_stride, dtype, rows, cols, "dy");
@@ -1500,6 +1501,7 @@ extern "C" zs_status zs_expert_combine_backward(const void* dout, int64_t dout_s
   a.dout = dout;
   a.y = y;
   a.slot = slot;
+  a.place = place;
   a.weights = weights;
   a.dy = dy;
   a.dweights = dweights;

@@ -199,8 +199,12 @@ struct Piece {
   }
 };
 
+// A lane's next kAhead pieces of a row, loaded together: a load's latency, not its bytes, is what a
+// row costs.
+constexpr int kAhead = 2;
+
 // out[p] = x[slot[p] / choices], zeros where the slot names no choice of an expert.  A workgroup
-// takes kRowsPer rows, 256 / kRowsPer lanes to each.
+// takes 1 << rows_log2 rows, as many lanes to each.
 template <int SIZE>
 __global__ __launch_bounds__(256) void k_gather(RowsArgs g) {
   constexpr int kElems = 16 / SIZE;
@@ -211,10 +215,17 @@ __global__ __launch_bounds__(256) void k_gather(RowsArgs g) {
   const bool any = slot >= 0 && slot < g.rows;
   const char* src = static_cast<const char*>(g.x) + (any ? int64_t(slot / g.choices) * g.x_stride * SIZE : 0);
   char* dst = static_cast<char*>(g.out) + p * g.out_stride * SIZE;
-  for (int64_t c = int64_t(threadIdx.x % per) * kElems; c < g.cols; c += int64_t(per) * kElems) {
-    v4u w = {0u, 0u, 0u, 0u};
-    if (any) w = load_piece<SIZE>(src + c * SIZE, g.cols - c);
-    store_piece<SIZE>(dst + c * SIZE, w, g.cols - c);
+  const int64_t step = int64_t(per) * kElems;
+  for (int64_t c = int64_t(threadIdx.x % per) * kElems; c < g.cols; c += kAhead * step) {
+    v4u w[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      w[u] = v4u{0u, 0u, 0u, 0u};
+      if (any && c + u * step < g.cols) w[u] = load_piece<SIZE>(src + (c + u * step) * SIZE, g.cols - c - u * step);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (c + u * step < g.cols) store_piece<SIZE>(dst + (c + u * step) * SIZE, w[u], g.cols - c - u * step);
   }
 }
 
@@ -227,72 +238,107 @@ __global__ __launch_bounds__(256) void k_combine(RowsArgs g) {
   if (t >= g.rows / g.choices) return;
   const int32_t* place = g.place + t * g.choices;
   const float* weights = g.weights != nullptr ? g.weights + t * g.choices : nullptr;
-  for (int64_t c = int64_t(threadIdx.x % per) * P::kElems; c < g.cols; c += int64_t(per) * P::kElems) {
-    float sum[P::kElems];
+  const int64_t step = int64_t(per) * P::kElems;
+  for (int64_t c = int64_t(threadIdx.x % per) * P::kElems; c < g.cols; c += kAhead * step) {
+    float sum[kAhead][P::kElems];
 #pragma unroll
-    for (int i = 0; i < P::kElems; ++i) sum[i] = 0.0f;
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int i = 0; i < P::kElems; ++i) sum[u][i] = 0.0f;
+#pragma unroll 2
     for (int j = 0; j < g.choices; ++j) {
       const int p = place[j];
       if (p < 0 || p >= g.rows) continue;
       const float w = weights != nullptr ? weights[j] : 1.0f;
-      float f[P::kElems];
-      P::widen(load_piece<P::kSize>(static_cast<const char*>(g.x) + (int64_t(p) * g.x_stride + c) * P::kSize, g.cols - c), f);
+      const char* y = static_cast<const char*>(g.x) + (int64_t(p) * g.x_stride + c) * P::kSize;
+      v4u v[kAhead];
 #pragma unroll
-      for (int i = 0; i < P::kElems; ++i) sum[i] += w * f[i];
+      for (int u = 0; u < kAhead; ++u) {
+        v[u] = v4u{0u, 0u, 0u, 0u};
+        if (c + u * step < g.cols) v[u] = load_piece<P::kSize>(y + u * step * P::kSize, g.cols - c - u * step);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        float f[P::kElems];
+        P::widen(v[u], f);
+#pragma unroll
+        for (int i = 0; i < P::kElems; ++i) sum[u][i] += w * f[i];
+      }
     }
-    store_piece<P::kSize>(static_cast<char*>(g.out) + (t * g.out_stride + c) * P::kSize, P::narrow(sum), g.cols - c);
+    char* out = static_cast<char*>(g.out) + (t * g.out_stride + c) * P::kSize;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (c + u * step < g.cols) store_piece<P::kSize>(out + u * step * P::kSize, P::narrow(sum[u]), g.cols - c - u * step);
   }
 }
 
-// For each row p with choice s of token t: dy[p] = weights[s] * dout[t], dweights[s] = sum over
-// columns of dout[t] * y[p].  A row that belongs to no expert has zeros.
+// For each token t and its choice j in row p = place[t][j]: dy[p] = weights[t][j] * dout[t],
+// dweights[t][j] = sum over columns of dout[t] * y[p].  By tokens, so that dout is read from memory
+// once and from the caches for the other choices; the token also clears those of its choices' worth
+// of rows that hold no expert's choice.
 template <int DT>
 __global__ __launch_bounds__(256) void k_combine_backward(CombineBackwardArgs g) {
   using P = Piece<DT>;
   const int per = 256 >> g.rows_log2;
-  const int64_t p = (int64_t(blockIdx.x) << g.rows_log2) + threadIdx.x / per;
+  const int64_t t = (int64_t(blockIdx.x) << g.rows_log2) + threadIdx.x / per;
   const int in_row = threadIdx.x % per;
   __shared__ float sums[4];
-  const bool here = p < g.rows;
-  int slot = here ? g.slot[p] : -1;
-  const bool any = slot >= 0 && slot < g.rows;
-  if (!any) slot = -1 - slot;  // the choice without an expert, whose weight's gradient is 0
-  const bool known = here && slot >= 0 && slot < g.rows;
-  float dot = 0.0f;
-  if (here) {
-    const int64_t t = any ? slot / g.choices : 0;
-    const float w = any && g.weights != nullptr ? g.weights[slot] : any ? 1.0f : 0.0f;
-    const char* dout = static_cast<const char*>(g.dout) + t * g.dout_stride * P::kSize;
-    const char* y = static_cast<const char*>(g.y) + p * g.y_stride * P::kSize;
-    char* dy = g.dy != nullptr ? static_cast<char*>(g.dy) + p * g.dy_stride * P::kSize : nullptr;
-    for (int64_t c = int64_t(in_row) * P::kElems; c < g.cols; c += int64_t(per) * P::kElems) {
-      v4u out = {0u, 0u, 0u, 0u};
-      if (any) {
-        float d[P::kElems], f[P::kElems];
-        P::widen(load_piece<P::kSize>(dout + c * P::kSize, g.cols - c), d);
-        if (g.dweights != nullptr) {
-          P::widen(load_piece<P::kSize>(y + c * P::kSize, g.cols - c), f);
+  const bool here = t * g.choices < g.rows;
+  const int64_t step = int64_t(per) * P::kElems;
+  const char* dout = static_cast<const char*>(g.dout) + (here ? t : 0) * g.dout_stride * P::kSize;
+  for (int j = 0; j < g.choices; ++j) {
+    const int64_t s = t * g.choices + j;
+    int p = here ? g.place[s] : -1;
+    const bool any = p >= 0 && p < g.rows;
+    const float w = any && g.weights != nullptr ? g.weights[s] : 1.0f;
+    float dot = 0.0f;
+    if (any) {
+      const char* y = static_cast<const char*>(g.y) + int64_t(p) * g.y_stride * P::kSize;
+      char* dy = g.dy != nullptr ? static_cast<char*>(g.dy) + int64_t(p) * g.dy_stride * P::kSize : nullptr;
+      for (int64_t c = int64_t(in_row) * P::kElems; c < g.cols; c += kAhead * step) {
+        v4u a[kAhead], b[kAhead];
 #pragma unroll
-          for (int i = 0; i < P::kElems; ++i) dot += d[i] * f[i];
+        for (int u = 0; u < kAhead; ++u) {
+          a[u] = b[u] = v4u{0u, 0u, 0u, 0u};
+          const int64_t at = c + u * step;
+          if (at < g.cols) {
+            a[u] = load_piece<P::kSize>(dout + at * P::kSize, g.cols - at);
+            if (g.dweights != nullptr) b[u] = load_piece<P::kSize>(y + at * P::kSize, g.cols - at);
+          }
         }
 #pragma unroll
-        for (int i = 0; i < P::kElems; ++i) d[i] *= w;
-        out = P::narrow(d);
+        for (int u = 0; u < kAhead; ++u) {
+          const int64_t at = c + u * step;
+          float d[P::kElems], f[P::kElems];
+          P::widen(a[u], d);
+          P::widen(b[u], f);
+#pragma unroll
+          for (int i = 0; i < P::kElems; ++i) {
+            dot += d[i] * f[i];
+            d[i] *= w;
+          }
+          if (dy != nullptr && at < g.cols) store_piece<P::kSize>(dy + at * P::kSize, P::narrow(d), g.cols - at);
+        }
       }
-      if (dy != nullptr) store_piece<P::kSize>(dy + c * P::kSize, out, g.cols - c);
     }
+    if (g.dy != nullptr && here && g.slot[s] < 0) {
+      char* dy = static_cast<char*>(g.dy) + s * g.dy_stride * P::kSize;
+      for (int64_t c = int64_t(in_row) * P::kElems; c < g.cols; c += step)
+        store_piece<P::kSize>(dy + c * P::kSize, v4u{0u, 0u, 0u, 0u}, g.cols - c);
+    }
+    if (g.dweights == nullptr) continue;
+    // a row's lanes are a power of two: within a wave, or whole waves of one row
+    for (int d = (per < 64 ? per : 64) / 2; d > 0; d >>= 1) dot += __shfl_xor(dot, d);
+    if (per > 64) {
+      __syncthreads();
+      if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = dot;
+      __syncthreads();
+      const int w0 = threadIdx.x / per * (per / 64);
+      dot = sums[w0];
+      for (int v = 1; v < per / 64; ++v) dot += sums[w0 + v];
+    }
+    if (in_row == 0 && here) g.dweights[s] = dot;
   }
-  if (g.dweights == nullptr) return;
-  // a row's lanes are a power of two: within a wave, or whole waves of one row
-  for (int d = (per < 64 ? per : 64) / 2; d > 0; d >>= 1) dot += __shfl_xor(dot, d);
-  if (per > 64) {
-    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = dot;
-    __syncthreads();
-    const int w0 = threadIdx.x / per * (per / 64);
-    dot = sums[w0];
-    for (int w = 1; w < per / 64; ++w) dot += sums[w0 + w];
-  }
-  if (in_row == 0 && known) g.dweights[slot] = any ? dot : 0.0f;
 }
 
 // Rows to a workgroup: as many lanes to a row as it has pieces, within 16 .. 256.
@@ -355,7 +401,7 @@ hipError_t launch_expert_combine(RowsArgs a, int dt, hipStream_t s) {
 hipError_t launch_expert_combine_backward(CombineBackwardArgs a, int dt, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
   a.rows_log2 = rows_log2(a.cols, dt == ZS_FP32 ? 4 : 8);
-  const dim3 grid(static_cast<unsigned>(row_blocks(a.rows, a.rows_log2)));
+  const dim3 grid(static_cast<unsigned>(row_blocks(a.rows / a.choices, a.rows_log2)));
   if (dt == ZS_BF16) hipLaunchKernelGGL((k_combine_backward<ZS_BF16>), grid, dim3(256), 0, s, a);
   else if (dt == ZS_FP16) hipLaunchKernelGGL((k_combine_backward<ZS_FP16>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((k_combine_backward<ZS_FP32>), grid, dim3(256), 0, s, a);

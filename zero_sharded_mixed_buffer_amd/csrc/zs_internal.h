@@ -251,6 +251,7 @@ struct CombineBackwardArgs {
   const void* dout;
   const void* y;         // or null: no dweights
   const int32_t* slot;
+  const int32_t* place;
   const float* weights;  // or null: ones
   void* dy;              // or null
   float* dweights;       // or null

@@ -693,14 +693,14 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
 // ------------------------------------------------------------------ few rows
 
 // Products of 16 * MF rows of a at a time, where reading b is most of it: a workgroup takes 16 * NF
-// rows of b, its eight waves every eighth piece of 128 bytes of k, and the waves' sums meet in
+// rows of b, each of its waves every WAVES-th piece of 128 bytes of k, and the waves' sums meet in
 // LDS.  Operands go from memory into the matrix instructions' registers without LDS: a lane's row is
 // lane % 16, and the order of k within a piece is free as long as both operands have the same, so
 // that a lane takes 32 consecutive bytes (16-bit operands; for 8-bit ones the instruction's scales
 // fix which).  Any alignment will do.
-template <int KIND, int MF, int NF>
-__global__ __launch_bounds__(512) void k_few(ProductArgs g) {
-  constexpr int kSize = KIND == kEight ? 1 : 2, kDepth = 128 / kSize, kWaves = 8, kAhead = MF * NF == 1 ? 4 : 2, kTileM = 16 * MF;
+template <int KIND, int MF, int NF, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void k_few(ProductArgs g) {
+  constexpr int kSize = KIND == kEight ? 1 : 2, kDepth = 128 / kSize, kWaves = WAVES, kAhead = MF * NF == 1 ? 4 : 2, kTileM = 16 * MF;
   __shared__ __attribute__((aligned(16))) v4f sums[kWaves][MF * NF][64];
   const int tiles_n = static_cast<int>((g.n + 16 * NF - 1) / (16 * NF));
   Span s{0, 0, 0};
@@ -851,8 +851,9 @@ template <int KIND, int MF>
 hipError_t launch_few_rows(const ProductArgs& a, hipStream_t s) {
   const bool wide = product_units(a, false, 16 * MF, 32) >= 512;
   const int64_t units = product_units(a, false, 16 * MF, wide ? 32 : 16);
-  auto kernel = wide ? &k_few<KIND, MF, 2> : &k_few<KIND, MF, 1>;
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(launch_units(units, kXcdWhole))), dim3(512), 0, s, a);
+  constexpr int kWaves = 8;
+  auto kernel = wide ? &k_few<KIND, MF, 2, kWaves> : &k_few<KIND, MF, 1, kWaves>;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(launch_units(units, kXcdWhole))), dim3(kWaves * 64), 0, s, a);
   return hipGetLastError();
 }
 

@@ -256,14 +256,18 @@ def route(ids, experts, workspace=None):
     device = ids.device
     _need_gpu(device)
     experts, slots = int(experts), ids.numel()
+    own = workspace is None
     workspace, size = _workspace(workspace, A.zs_route_workspace(slots, experts), device)
     ends = torch.empty(experts, dtype=torch.int32, device=device)
     slot = torch.empty(slots, dtype=torch.int32, device=device)
     place = torch.empty(ids.shape, dtype=torch.int32, device=device)
     _enqueue("zs_route", device, ids.data_ptr(), ids.element_size(), slots, experts, ends.data_ptr(), slot.data_ptr(),
              place.data_ptr(), workspace.data_ptr(), size)
-    _wrote((workspace,))
-    return Route(ends, slot, place)
+    if not own:
+        _wrote((workspace,))
+    out = Route.__new__(Route)  # nothing to check
+    out.ends, out.slot, out.place = ends, slot, place
+    return out
 
 
 def _routed(route, device):
@@ -325,8 +329,8 @@ def expert_combine_backward(dout, y, route, weights=None, dy=None, dweights=None
     if dy is not None:
         dys = _matrix(dy, "dy", dout.dtype, route.rows, cols, dev)
     _enqueue("zs_expert_combine_backward", dev, dout.data_ptr(), ds, _at(y) if dweights is not None else None, ys,
-             _DTYPES[dout.dtype], route.slot.data_ptr(), _at(weights), tokens, route.choices, cols, _at(dy), dys,
-             _at(dweights))
+             _DTYPES[dout.dtype], route.slot.data_ptr(), route.place.data_ptr(), _at(weights), tokens, route.choices, cols,
+             _at(dy), dys, _at(dweights))
     _wrote([t for t in (dy, dweights) if t is not None])
 
 
@@ -471,11 +475,20 @@ def experts(x, weight, ends, in_major=False, save=None, grad_into=None):
     return _Experts.apply(_rows(x), weight, ends, bool(in_major), save, grad_into)
 
 
+def _differentiated(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _gathered(x, route):
+    out = torch.empty(route.rows, x.shape[1], dtype=x.dtype, device=x.device)
+    expert_gather(x, route, out)
+    return out
+
+
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, route):
-        out = torch.empty(route.rows, x.shape[1], dtype=x.dtype, device=x.device)
-        expert_gather(x, route, out)
+        out = _gathered(x, route)
         ctx.save_for_backward(route.ends, route.slot, route.place)
         return out
 
@@ -492,14 +505,21 @@ def dispatch(x, route):
     """expert_gather under autograd: the rows of x [..., cols] (tokens in order) in the route's order."""
     if x.dim() < 1 or x.dtype not in _DTYPES or x.shape[-1] < 1:
         raise ValueError("x must be a bf16, fp16 or fp32 tensor with at least one column")
+    if not _differentiated(x):
+        return _gathered(_rows(x), route)
     return _Dispatch.apply(_rows(x), route)
+
+
+def _combined(y, weights, route):
+    out = torch.empty(route.tokens, y.shape[1], dtype=y.dtype, device=y.device)
+    expert_combine(y, route, out, weights)
+    return out
 
 
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, route):
-        out = torch.empty(route.tokens, y.shape[1], dtype=y.dtype, device=y.device)
-        expert_combine(y, route, out, weights)
+        out = _combined(y, weights, route)
         kept = y if weights is not None and ctx.needs_input_grad[1] else None
         ctx.save_for_backward(route.ends, route.slot, route.place, weights, kept)
         return out
@@ -524,4 +544,7 @@ def combine(y, route, weights=None):
     weights: fp32 [tokens, choices] (the router's), or None for ones."""
     if y.dim() != 2 or y.dtype not in _DTYPES or y.shape[1] < 1:
         raise ValueError("y must be a bf16, fp16 or fp32 matrix with at least one column")
-    return _Combine.apply(_rows(y), weights.contiguous() if weights is not None else None, route)
+    weights = weights.contiguous() if weights is not None else None
+    if not _differentiated(y, weights):
+        return _combined(_rows(y), weights, route)
+    return _Combine.apply(_rows(y), weights, route)
