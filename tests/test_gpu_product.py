@@ -314,7 +314,8 @@ def test_experts_keep_to_their_rows(Z):
 
 # ------------------------------------------------------------------------------ routing
 
-ROUTES = [(0, 1, 4), (1, 1, 1), (3, 2, 4), (64, 1, 3), (65, 2, 16), (300, 8, 64), (1024, 1, 2), (1025, 2, 257), (5000, 3, 1024), (2048, 4, 7)]
+ROUTES = [(0, 1, 4), (1, 1, 1), (3, 2, 4), (64, 1, 3), (65, 2, 16), (300, 8, 64), (1024, 1, 2), (1025, 2, 257), (5000, 3, 1024), (2048, 4, 7),
+          (1300, 3, 600), (40000, 2, 16), (24000, 3, 300)]
 
 
 @pytest.mark.parametrize("int_type", [torch.int32, torch.int64])

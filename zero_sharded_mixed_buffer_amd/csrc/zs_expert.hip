@@ -13,21 +13,29 @@ using namespace act;
 
 // ------------------------------------------------------------------ order by expert
 
-// A counting sort that keeps the order of equal keys.  A workgroup takes kRouteChunk consecutive
-// choices, each of its four waves a quarter, 64 at a time in order.  A choice's place is the number
-// of choices of smaller experts, plus those of its own expert in workgroups, waves and rounds
-// before it, plus the lanes before it in its round: no atomics.  Choices that name no expert count as
-// expert E.
-constexpr int kWaveChunk = kRouteChunk / 4;
+// A counting sort that keeps the order of equal keys.  A wave takes kWaveChunk consecutive choices,
+// 64 at a time in order.  A choice's place is the number of choices of smaller experts, plus those of
+// its own expert in workgroups, waves and rounds before it, plus the lanes before it in its round: no
+// atomics.  Choices that name no expert count as expert E.
+constexpr int kWaveChunk = 256, kRounds = kWaveChunk / 64;
 
 __device__ __forceinline__ int expert_of(const void* ids, int id_bytes, int64_t i, int experts) {
   const int64_t v = id_bytes == 8 ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
   return v >= 0 && v < experts ? static_cast<int>(v) : experts;
 }
 
-// Lanes with the same key, among those that take part.
-__device__ __forceinline__ uint64_t same_key(int key, int bits, bool part) {
-  uint64_t mask = __ballot(part);
+// A lane's keys in the wave's rounds, -1 behind the last choice.
+__device__ __forceinline__ void load_keys(const RouteArgs& g, int64_t first, int (&key)[kRounds]) {
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int64_t at = first + i * 64 + (threadIdx.x & 63);
+    key[i] = at < g.slots ? expert_of(g.ids, g.id_bytes, at, g.experts) : -1;
+  }
+}
+
+// Lanes with the same key, among those that have one.
+__device__ __forceinline__ uint64_t same_key(int key, int bits) {
+  uint64_t mask = __ballot(key >= 0);
   for (int b = 0; b < bits; ++b) {
     const uint64_t set = __ballot((key >> b) & 1);
     mask &= (key >> b) & 1 ? set : ~set;
@@ -35,26 +43,30 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits, bool part) {
   return mask;
 }
 
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // counts[e] += this wave's choices of each expert.
-__device__ __forceinline__ void count_wave(const RouteArgs& g, int64_t first, int* counts) {
+__device__ __forceinline__ void count_wave(const RouteArgs& g, const int (&key)[kRounds], int* counts) {
   const int lane = threadIdx.x & 63;
-  for (int i = 0; i < kWaveChunk; i += 64) {
-    const int64_t at = first + i + lane;
-    const bool part = at < g.slots;
-    const int key = part ? expert_of(g.ids, g.id_bytes, at, g.experts) : 0;
-    const uint64_t mask = same_key(key, g.bits, part);
-    if (part && (mask >> lane) == 1) counts[key] += __popcll(mask);  // the last lane of a key
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const uint64_t mask = same_key(key[i], g.bits);
+    if (key[i] >= 0 && (mask >> lane) == 1) counts[key[i]] += __popcll(mask);  // the last lane of a key
+    wave_fence();
   }
 }
 
 __global__ __launch_bounds__(256) void k_route_count(RouteArgs g) {
   extern __shared__ int counts[];  // four waves of experts + 1
   const int keys = g.experts + 1, wave = threadIdx.x >> 6;
+  int key[kRounds];
+  load_keys(g, int64_t(blockIdx.x) * kRouteChunk + wave * kWaveChunk, key);
   for (int i = threadIdx.x; i < 4 * keys; i += 256) counts[i] = 0;
   __syncthreads();
-  count_wave(g, int64_t(blockIdx.x) * kRouteChunk + wave * kWaveChunk, counts + wave * keys);
+  count_wave(g, key, counts + wave * keys);
   __syncthreads();
   for (int e = threadIdx.x; e < keys; e += 256)
     g.counts[int64_t(blockIdx.x) * keys + e] = counts[e] + counts[keys + e] + counts[2 * keys + e] + counts[3 * keys + e];
@@ -85,23 +97,48 @@ __global__ __launch_bounds__(256) void k_route_scan(RouteArgs g) {
   if (threadIdx.x == 0) g.totals[blockIdx.x] = before;
 }
 
-// ONE: the only workgroup, which counts for itself.
-template <bool ONE>
-__global__ __launch_bounds__(256) void k_route_place(RouteArgs g) {
-  extern __shared__ int counts[];  // four waves of experts + 1, then the experts' first places
+// Where the counts of the workgroups before this one come from: there is none (kAlone), from all
+// workgroups' counts, which each adds up for itself (kFew), or from k_route_scan (kMany).
+enum RouteWay { kAlone, kFew, kMany };
+constexpr int64_t kFewChunks = 64;  // 65536 choices; what kFew adds up for itself then costs as much as the launch of a scan
+
+template <RouteWay WAY, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void k_route_place(RouteArgs g) {
+  extern __shared__ int counts[];  // waves of experts + 1, then the experts' first places, then the choices before this workgroup
   const int keys = g.experts + 1, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int* starts = counts + 4 * keys;
-  const int64_t first = int64_t(blockIdx.x) * kRouteChunk + wave * kWaveChunk;
-  for (int i = threadIdx.x; i < 4 * keys; i += 256) counts[i] = 0;
+  int* starts = counts + WAVES * keys;
+  int* fronts = starts + keys;
+  const int64_t first = int64_t(blockIdx.x) * (WAVES * kWaveChunk) + wave * kWaveChunk;
+  int key[kRounds];
+  load_keys(g, first, key);
+  for (int i = threadIdx.x; i < WAVES * keys; i += WAVES * 64) counts[i] = 0;
   __syncthreads();
-  count_wave(g, first, counts + wave * keys);
+  count_wave(g, key, counts + wave * keys);
+  __syncthreads();
+  for (int e = threadIdx.x; e < keys; e += WAVES * 64) {  // this expert's choices in all, and before this workgroup
+    int all = 0, front = 0;
+    if constexpr (WAY == kAlone) {
+      for (int w = 0; w < WAVES; ++w) all += counts[w * keys + e];
+    } else if constexpr (WAY == kFew) {
+#pragma unroll 8
+      for (int c = 0; c < static_cast<int>(g.chunks); ++c) {
+        const int n = g.counts[c * keys + e];
+        all += n;
+        if (c < static_cast<int>(blockIdx.x)) front += n;
+      }
+    } else {
+      all = g.totals[e];
+      front = g.counts[int64_t(blockIdx.x) * keys + e];
+    }
+    starts[e] = all;
+    fronts[e] = front;
+  }
   __syncthreads();
   if (wave == 0) {  // places before each expert
     int before = 0;
     for (int c = 0; c < keys; c += 64) {
       const int e = c + lane;
-      int n = 0;
-      if (e < keys) n = ONE ? counts[e] + counts[keys + e] + counts[2 * keys + e] + counts[3 * keys + e] : g.totals[e];
+      const int n = e < keys ? starts[e] : 0;
       int sum = n;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
@@ -114,9 +151,9 @@ __global__ __launch_bounds__(256) void k_route_place(RouteArgs g) {
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < keys; e += 256) {
-    int at = starts[e] + (ONE ? 0 : g.counts[int64_t(blockIdx.x) * keys + e]);
-    for (int w = 0; w < 4; ++w) {
+  for (int e = threadIdx.x; e < keys; e += WAVES * 64) {
+    int at = starts[e] + fronts[e];
+    for (int w = 0; w < WAVES; ++w) {
       const int n = counts[w * keys + e];
       counts[w * keys + e] = at;
       at += n;
@@ -124,21 +161,19 @@ __global__ __launch_bounds__(256) void k_route_place(RouteArgs g) {
   }
   __syncthreads();
   int* next = counts + wave * keys;
-  for (int i = 0; i < kWaveChunk; i += 64) {
-    const int64_t at = first + i + lane;
-    const bool part = at < g.slots;
-    const int key = part ? expert_of(g.ids, g.id_bytes, at, g.experts) : 0;
-    const uint64_t mask = same_key(key, g.bits, part);
-    const int place = part ? next[key] + __popcll(mask & ((uint64_t(1) << lane) - 1)) : 0;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (part && (mask >> lane) == 1) next[key] = place + 1;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int64_t at = first + i * 64 + lane;
+    const bool part = key[i] >= 0;
+    const uint64_t mask = same_key(key[i], g.bits);
+    const int place = part ? next[key[i]] + __popcll(mask & ((uint64_t(1) << lane) - 1)) : 0;
+    wave_fence();
+    if (part && (mask >> lane) == 1) next[key[i]] = place + 1;
+    wave_fence();
     if (part) {
       const int slot = static_cast<int>(at);
-      g.place[at] = key < g.experts ? place : -1;
-      g.slot[place] = key < g.experts ? slot : -1 - slot;
+      g.place[at] = key[i] < g.experts ? place : -1;
+      g.slot[place] = key[i] < g.experts ? slot : -1 - slot;
     }
   }
 }
@@ -162,7 +197,7 @@ template <int SIZE>
 __device__ __forceinline__ void store_piece(char* p, const v4u& w, int64_t left) {
   constexpr int kElems = 16 / SIZE;
   if (left >= kElems) {
-    *reinterpret_cast<v4u_a2*>(p) = w;
+    __builtin_nontemporal_store(w, reinterpret_cast<v4u_a2*>(p));
     return;
   }
   if constexpr (SIZE == 2) {
@@ -366,15 +401,23 @@ hipError_t launch_route(RouteArgs a, void* workspace, hipStream_t s) {
   while ((1 << a.bits) < keys) ++a.bits;
   a.totals = static_cast<int32_t*>(workspace);
   a.counts = a.totals + keys;
-  const size_t lds = 5 * size_t(keys) * sizeof(int);
+  auto lds = [&](int waves) { return size_t(waves + 2) * keys * sizeof(int); };
   if (a.chunks <= 1) {
-    hipLaunchKernelGGL((k_route_place<true>), dim3(1), dim3(256), lds, s, a);
+    hipLaunchKernelGGL((k_route_place<kAlone, 4>), dim3(1), dim3(256), lds(4), s, a);
+    return hipGetLastError();
+  }
+  if (a.slots <= 16 * kWaveChunk && keys <= 512) {  // 36 KB of LDS
+    hipLaunchKernelGGL((k_route_place<kAlone, 16>), dim3(1), dim3(1024), lds(16), s, a);
     return hipGetLastError();
   }
   const unsigned chunks = static_cast<unsigned>(a.chunks);
-  hipLaunchKernelGGL(k_route_count, dim3(chunks), dim3(256), lds, s, a);
+  hipLaunchKernelGGL(k_route_count, dim3(chunks), dim3(256), lds(4), s, a);
+  if (a.chunks <= kFewChunks) {
+    hipLaunchKernelGGL((k_route_place<kFew, 4>), dim3(chunks), dim3(256), lds(4), s, a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(k_route_scan, dim3(static_cast<unsigned>(keys)), dim3(256), 0, s, a);
-  hipLaunchKernelGGL((k_route_place<false>), dim3(chunks), dim3(256), lds, s, a);
+  hipLaunchKernelGGL((k_route_place<kMany, 4>), dim3(chunks), dim3(256), lds(4), s, a);
   return hipGetLastError();
 }
 

@@ -979,7 +979,7 @@ __global__ __launch_bounds__(256) void k_weight8(const void* src, int64_t stride
           for (int j = 0; j < 8; ++j) f[h][r][j] = j < n ? p[j] : 0.0f;
         }
       } else {
-        widen8<DT>(load8h(static_cast<const uint16_t*>(src) + row * stride + col, n), f[h][r]);
+        widen8<DT>(load8h_nt(static_cast<const uint16_t*>(src) + row * stride + col, n), f[h][r]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = __builtin_elementwise_maximum(top, fabsf(f[h][r][j]));  // a NaN wins
@@ -1003,7 +1003,7 @@ __global__ __launch_bounds__(256) void k_weight8(const void* src, int64_t stride
     for (int r = 0; r < 4; ++r) {
       c[r] = encode8<ZS_E4M3>(f[h][r], b);
       const int64_t row = bo * 128 + h * 64 + patch_r * 4 + r;
-      if (row < outs) *reinterpret_cast<v2u*>(codes + row * pc + col) = c[r];
+      if (row < outs) __builtin_nontemporal_store(c[r], reinterpret_cast<v2u*>(codes + row * pc + col));
     }
     if (codes_t != nullptr) {
 #pragma unroll
@@ -1021,7 +1021,9 @@ __global__ __launch_bounds__(256) void k_weight8(const void* src, int64_t stride
   for (int q = 0; q < 4; ++q) {
     const int id = q * 256 + threadIdx.x, row = id / 8, at = id % 8;
     const int64_t c = bc * 128 + row;
-    if (c < cols) *reinterpret_cast<v4u*>(codes_t + c * pr + bo * 128 + at * 16) = *reinterpret_cast<const v4u*>(turned + row * 36 + at * 4);
+    if (c < cols)
+      __builtin_nontemporal_store(*reinterpret_cast<const v4u*>(turned + row * 36 + at * 4),
+                                  reinterpret_cast<v4u*>(codes_t + c * pr + bo * 128 + at * 16));
   }
 }
 
