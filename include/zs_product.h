@@ -48,7 +48,7 @@ typedef struct {
 } zs_weight8;
 
 /* Bytes of the arrays of an outs x cols weight.  Host only.
- * Errors: ZS_EINVAL on a NULL output, outs or cols < 1 or sizes past one launch. */
+ * Errors: ZS_EINVAL on a NULL output, outs or cols outside 1 .. 2^23 or sizes past one launch. */
 zs_status zs_weight8_size(int64_t outs, int64_t cols, int64_t* codes_bytes, int64_t* codes_t_bytes,
                           int64_t* scales_bytes);
 

@@ -1191,8 +1191,9 @@ zs_status check_weight8_sizes(int64_t outs, int64_t cols) {
   zs_status st = check_sizes(outs, cols);
   if (st != ZS_OK) return st;
   if (outs < 1) return fail(ZS_EINVAL, "outs must be positive");
-  if (outs > (int64_t(1) << 30) || cols > (int64_t(1) << 30) ||
-      ((outs + 127) / 128) * ((cols + 127) / 128) > zs::kProductMaxUnits)
+  if (outs > zs::kWeight8MaxSide || cols > zs::kWeight8MaxSide)
+    return fail(ZS_EINVAL, "outs and cols are at most %lld", static_cast<long long>(zs::kWeight8MaxSide));
+  if (((outs + 127) / 128) * ((cols + 127) / 128) > zs::kProductMaxUnits)
     return fail(ZS_EINVAL, "outs x cols exceeds one launch");
   return ok();
 }

@@ -217,6 +217,7 @@ hipError_t launch_product8(const ProductArgs& a, hipStream_t s);
 hipError_t launch_expert_product(const ProductArgs& a, int dt, bool in_major, hipStream_t s);
 hipError_t launch_expert_wgrad(const ProductArgs& a, int dt, hipStream_t s);
 constexpr int64_t kWeightBlock = 128;
+constexpr int64_t kWeight8MaxSide = int64_t(1) << 23;  // 256 rows of codes within 32-bit offsets
 hipError_t launch_weight8(const void* src, int dt, int64_t stride, int64_t outs, int64_t cols, uint8_t* codes, uint8_t* codes_t,
                           uint8_t* scales, hipStream_t s);
 

@@ -336,6 +336,10 @@ def expert_combine_backward(dout, y, route, weights=None, dy=None, dweights=None
 
 # ------------------------------------------------------------------------------ autograd
 
+def _differentiated(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 class _Linear8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, x8, w8, grad_into):
@@ -417,6 +421,10 @@ def linear8(x, weight, w8=None, x8=None, grad_into=None):
             raise ValueError("w8 has no transposed codes, which the gradient of x needs")
         if w8._outlived(weight):
             raise ValueError("the weight has been changed in place since w8 was taken of it")
+    if not _differentiated(x, weight):
+        y = torch.empty(*x.shape[:-1], outs, dtype=x.dtype, device=x.device)
+        product8(x8, w8, y.view(-1, outs))
+        return y
     return _Linear8.apply(x, weight, x8, w8, grad_into)
 
 
@@ -472,11 +480,11 @@ def experts(x, weight, ends, in_major=False, save=None, grad_into=None):
         raise ValueError(f"save is 'e4m3', 'int8' or None, not {save!r}")
     _ends(ends, x.device, weight.shape[0])
     _check_grad_into(grad_into, weight)
+    if not _differentiated(x, weight):
+        y = torch.empty(x.shape[0], weight.shape[2 if in_major else 1], dtype=x.dtype, device=x.device)
+        expert_product(_rows(x), weight, ends, y, in_major=in_major, zero_rest=True)
+        return y
     return _Experts.apply(_rows(x), weight, ends, bool(in_major), save, grad_into)
-
-
-def _differentiated(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 def _gathered(x, route):
