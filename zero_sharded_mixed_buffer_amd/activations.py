@@ -343,7 +343,9 @@ def _rows(t):
     m = t.reshape(-1, t.shape[-1])
     rows, cols = m.shape
     row, col = m.stride()
-    return m if (cols == 1 or col == 1) and (rows <= 1 or row >= cols) else m.contiguous()
+    if (cols == 1 or col == 1) and (rows <= 1 or row >= cols):
+        return m
+    return m.clone(memory_format=torch.contiguous_format)  # an empty one counts as contiguous at any strides
 
 
 def _check_grad_into(grad_into, weight):
