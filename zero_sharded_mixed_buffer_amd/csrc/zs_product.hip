@@ -284,54 +284,55 @@ __device__ __forceinline__ void meet() {
 
 // ------------------------------------------------------------------ the product
 
-// Eight sums of row `row` of c, from column col on, cnt of them inside: added to the base and
-// rounded once.
-__device__ __forceinline__ void write8(const ProductArgs& g, int64_t at, int cnt, float (&f)[8]) {
+// Eight elements of the base from `at` on, cnt of them inside, as they lie in memory.
+struct Base8 {
+  v4u lo, hi;  // hi: of fp32
+};
+__device__ __forceinline__ Base8 load_base8(const ProductArgs& g, int64_t at, int cnt) {
+  Base8 b = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+  if (g.c_dt != ZS_FP32) {
+    b.lo = load8h(static_cast<const uint16_t*>(g.base) + at, cnt);
+    return b;
+  }
+  const uint32_t* p = static_cast<const uint32_t*>(g.base) + at;
+  if (cnt == 8) {
+    b.lo = *reinterpret_cast<const v4u_a4*>(p);
+    b.hi = *reinterpret_cast<const v4u_a4*>(p + 4);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < cnt) (j < 4 ? b.lo : b.hi)[j & 3] = p[j];
+  }
+  return b;
+}
+
+// Eight sums of a row of c, cnt of them inside: added to the base and rounded once.
+__device__ __forceinline__ void write8(const ProductArgs& g, int64_t at, int cnt, const Base8& base, float (&f)[8]) {
   if (g.c_dt == ZS_FP32) {
-    float* p = static_cast<float*>(g.c) + at;
-    const float* base = static_cast<const float*>(g.base);
-    if (base != nullptr) base += at;
+    uint32_t* p = static_cast<uint32_t*>(g.c) + at;
+    v4u lo, hi;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lo[j] = f_bits(f[j] + bits_f(base.lo[j]));
+      hi[j] = f_bits(f[4 + j] + bits_f(base.hi[j]));
+    }
     if (cnt == 8) {
-      v4u lo, hi;
-      if (base != nullptr) {
-        const v4u x = *reinterpret_cast<const v4u_a4*>(base), y = *reinterpret_cast<const v4u_a4*>(base + 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[j] += bits_f(x[j]);
-          f[4 + j] += bits_f(y[j]);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        lo[j] = f_bits(f[j]);
-        hi[j] = f_bits(f[4 + j]);
-      }
       *reinterpret_cast<v4u_a4*>(p) = lo;
       *reinterpret_cast<v4u_a4*>(p + 4) = hi;
     } else {
 #pragma unroll
       for (int j = 0; j < 7; ++j)
-        if (j < cnt) p[j] = f[j] + (base != nullptr ? base[j] : 0.0f);
+        if (j < cnt) p[j] = (j < 4 ? lo : hi)[j & 3];
     }
     return;
   }
   uint16_t* p = static_cast<uint16_t*>(g.c) + at;
-  if (g.base != nullptr) {
-    float x[8];
-    const v4u b = load8h(static_cast<const uint16_t*>(g.base) + at, cnt);
-    if (g.c_dt == ZS_BF16) widen8<ZS_BF16>(b, x);
-    else widen8<ZS_FP16>(b, x);
+  float x[8];
+  if (g.c_dt == ZS_BF16) widen8<ZS_BF16>(base.lo, x);
+  else widen8<ZS_FP16>(base.lo, x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] += x[j];
-  }
-  const v4u w = g.c_dt == ZS_BF16 ? narrow8<ZS_BF16>(f) : narrow8<ZS_FP16>(f);
-  if (cnt >= 8) {
-    *reinterpret_cast<v4u_a2*>(p) = w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (j < cnt) p[j] = static_cast<uint16_t>(w[j >> 1] >> ((j & 1) * 16));
-  }
+  for (int j = 0; j < 8; ++j) f[j] += x[j];
+  store8h(p, g.c_dt == ZS_BF16 ? narrow8<ZS_BF16>(f) : narrow8<ZS_FP16>(f), cnt);
 }
 
 // Unit u of a tiles_m x tiles_n grid in bands of eight rows of tiles, column by column: workgroups
@@ -662,8 +663,20 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
   // + r % 4, column lane % 32.
   float* strip = reinterpret_cast<float*>(lds) + wave * 32 * TL::kStripPitch;
   const int64_t c_at = SUM_GROUPS ? s.group * g.c_group : 0;
+  constexpr int kRounds = TL::FN * 2, kEights = TL::FN * 4;  // eights of columns of a strip's row
 #pragma unroll
   for (int i = 0; i < TL::FM; ++i) {
+    int64_t at[kRounds];
+    int cnt[kRounds];
+    Base8 base[kRounds];
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {  // the base's elements set out together
+      const int q = u * 64 + lane, tm = wm + i * 32 + q / kEights, col = wn + q % kEights * 8, left = left_n - col;
+      at[u] = c_at + (m0 + tm) * g.c_stride + n0 + col;
+      cnt[u] = tm >= left_m || left <= 0 ? 0 : left >= 8 ? 8 : left;
+      base[u] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+      if (g.base != nullptr && cnt[u] > 0) base[u] = load_base8(g, at[u], cnt[u]);
+    }
 #pragma unroll
     for (int j = 0; j < TL::FN; ++j)
 #pragma unroll
@@ -671,19 +684,18 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
         strip[(8 * (r / 4) + 4 * (lane >> 5) + r % 4) * TL::kStripPitch + j * 32 + (lane & 31)] = acc[i][j][r];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    for (int q = lane; q < 32 * TL::FN * 4; q += 64) {
-      const int r = q / (TL::FN * 4), c = q % (TL::FN * 4) * 8;
-      const v4u x = *reinterpret_cast<const v4u*>(strip + r * TL::kStripPitch + c);
-      const v4u y = *reinterpret_cast<const v4u*>(strip + r * TL::kStripPitch + c + 4);
-      const int tm = wm + i * 32 + r, left = left_n - (wn + c);
-      if (tm >= left_m || left <= 0) continue;
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+      const int q = u * 64 + lane;
+      const float* from = strip + q / kEights * TL::kStripPitch + q % kEights * 8;
+      const v4u x = *reinterpret_cast<const v4u*>(from), y = *reinterpret_cast<const v4u*>(from + 4);
       float v[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[j] = bits_f(x[j]);
         v[4 + j] = bits_f(y[j]);
       }
-      write8(g, c_at + (m0 + tm) * g.c_stride + n0 + wn + c, left >= 8 ? 8 : left, v);
+      if (cnt[u] > 0) write8(g, at[u], cnt[u], base[u], v);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
