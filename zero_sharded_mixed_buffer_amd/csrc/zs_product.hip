@@ -54,21 +54,21 @@ struct Tile {
 
 // ------------------------------------------------------------------ groups of rows
 
-__device__ __forceinline__ int wave_max_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d && o > v) v = o;
-  }
-  return v;
+// Running sums or maxima (of numbers that are not negative) over a wave's lanes, through the data-parallel
+// moves within and between rows of sixteen lanes.
+template <bool MAX, int CTRL, int ROWS>
+__device__ __forceinline__ int scan_step(int v) {
+  const int o = __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+  return MAX ? (o > v ? o : v) : v + o;
 }
-__device__ __forceinline__ int wave_sum_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
+template <bool MAX>
+__device__ __forceinline__ int wave_scan(int v) {
+  v = scan_step<MAX, 0x111, 0xF>(v);  // from one, two, four, eight lanes before, in the same row
+  v = scan_step<MAX, 0x112, 0xF>(v);
+  v = scan_step<MAX, 0x114, 0xF>(v);
+  v = scan_step<MAX, 0x118, 0xF>(v);
+  v = scan_step<MAX, 0x142, 0xA>(v);  // a row's last lane to the row behind it
+  return scan_step<MAX, 0x143, 0xC>(v);
 }
 
 // Ends that run backwards or past the rows would lead out of the matrices: an end counts as the
@@ -87,48 +87,66 @@ __device__ __forceinline__ Span group_span(const int32_t* ends, int e, int64_t r
   for (int c = 0; c <= e; c += 64) {
     int v = c + lane <= e ? ends[c + lane] : 0;
     v = v < 0 ? 0 : v > rows ? static_cast<int>(rows) : v;
-    const int all = __shfl(wave_max_scan(v, lane), 63);
-    const int less = __shfl(wave_max_scan(c + lane < e ? v : 0, lane), 63);
+    const int all = __builtin_amdgcn_readlane(wave_scan<true>(v), 63);
+    const int less = __builtin_amdgcn_readlane(wave_scan<true>(c + lane < e ? v : 0), 63);
     before = less > before ? less : before;
     upto = all > upto ? all : upto;
   }
-  before = uniform(before);
-  upto = uniform(upto);
   return {before, upto > before ? upto : before, e};
 }
 
-// Tiles of `tile` rows of all groups, one group after the other, and, where `rest`, of the rows
-// behind the last one as one more group.  Returns how many there are; where 0 <= unit < that, *s
-// is the tile's group with the rows from the tile's first to the group's last.
-__device__ __forceinline__ int find_tile(const int32_t* ends, int groups, bool rest, int64_t rows, int tile, int unit, Span* s) {
-  if (ends == nullptr) {
-    *s = {int64_t(unit) * tile, rows, 0};
-    return static_cast<int>((rows + tile - 1) / tile);
-  }
+// 64 groups' rows from `top` on, one group to a lane: their tiles, and the tiles up to each.
+struct GroupTiles {
+  int start, end, tiles, upto;
+};
+__device__ __forceinline__ GroupTiles group_tiles(const int32_t* ends, int groups, bool rest, int64_t rows, int tile, int c, int top) {
   const int lane = threadIdx.x & 63;
-  int top = 0, tiles = 0;
-  const int all = groups + (rest ? 1 : 0);
-  for (int c = 0; c < all; c += 64) {
-    int v = c + lane < groups ? ends[c + lane] : c + lane == groups && rest ? static_cast<int>(rows) : 0;
-    v = v < 0 ? 0 : v > rows ? static_cast<int>(rows) : v;
-    v = wave_max_scan(v, lane);
-    v = v > top ? v : top;
-    const int prev = __shfl_up(v, 1);
-    const int start = lane == 0 ? top : prev;
-    const int n = (v - start + tile - 1) / tile;
-    const int sum = wave_sum_scan(n, lane);
-    const int mine = unit - tiles - (sum - n);
-    const uint64_t hit = __ballot(mine >= 0 && mine < n);
-    if (hit != 0) {
-      const int at = __ffsll(static_cast<unsigned long long>(hit)) - 1;
-      s->first = __builtin_amdgcn_readlane(start, at) + int64_t(__builtin_amdgcn_readlane(mine, at)) * tile;
-      s->last = __builtin_amdgcn_readlane(v, at);
-      s->group = c + at;
-    }
-    tiles += __builtin_amdgcn_readlane(sum, 63);
-    top = __builtin_amdgcn_readlane(v, 63);
+  int v = c + lane < groups ? ends[c + lane] : c + lane == groups && rest ? static_cast<int>(rows) : 0;
+  v = v < 0 ? 0 : v > rows ? static_cast<int>(rows) : v;
+  v = wave_scan<true>(v);
+  v = v > top ? v : top;
+  const int start = __builtin_amdgcn_update_dpp(top, v, 0x138, 0xF, 0xF, false);  // the end of the lane before
+  const int n = (v - start + tile - 1) / tile;
+  return {start, v, n, wave_scan<false>(n)};
+}
+
+// Tiles of `tile` rows of all groups, one group after the other, and, where `rest`, of the rows behind
+// the last one as one more group.  unit_of(their number) names one of them, or none with a number
+// below 0: *s is its group, with the rows from the tile's first to the group's last.
+template <class UnitOf>
+__device__ __forceinline__ void find_tile(const int32_t* ends, int groups, bool rest, int64_t rows, int tile, UnitOf unit_of, Span* s) {
+  if (ends == nullptr) {
+    const int unit = unit_of(static_cast<int>((rows + tile - 1) / tile));
+    *s = {int64_t(unit) * tile, rows, 0};
+    return;
   }
-  return tiles;
+  auto pick = [&](const GroupTiles& t, int unit, int c) {
+    const int mine = unit - (t.upto - t.tiles);
+    const uint64_t hit = __ballot(mine >= 0 && mine < t.tiles);
+    if (hit == 0) return;
+    const int at = __ffsll(static_cast<unsigned long long>(hit)) - 1;
+    s->first = __builtin_amdgcn_readlane(t.start, at) + int64_t(__builtin_amdgcn_readlane(mine, at)) * tile;
+    s->last = __builtin_amdgcn_readlane(t.end, at);
+    s->group = c + at;
+  };
+  const int all = groups + (rest ? 1 : 0);
+  if (all <= 64) {  // one look at the ends
+    const GroupTiles t = group_tiles(ends, groups, rest, rows, tile, 0, 0);
+    pick(t, unit_of(__builtin_amdgcn_readlane(t.upto, 63)), 0);
+    return;
+  }
+  int tiles = 0, unit = 0;
+  for (int pass = 0; pass < 2; ++pass) {  // count, then look
+    int top = 0, before = 0;
+    for (int c = 0; c < all; c += 64) {
+      const GroupTiles t = group_tiles(ends, groups, rest, rows, tile, c, top);
+      if (pass == 0) tiles += __builtin_amdgcn_readlane(t.upto, 63);
+      else pick(t, unit - before, c);
+      before += __builtin_amdgcn_readlane(t.upto, 63);
+      top = __builtin_amdgcn_readlane(t.end, 63);
+    }
+    if (pass == 0) unit = unit_of(tiles);
+  }
 }
 
 // ------------------------------------------------------------------ operands
@@ -360,36 +378,35 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
   // one contiguous run of units per XCD
   const int tiles_n = static_cast<int>((g.n + TL::kN - 1) / TL::kN);
   Span s{0, 0, 0};
-  int64_t m0, n0, k0 = 0, depth = g.k;
-  {
-    int units, tiles_m = 0;
-    if constexpr (SUM_GROUPS) {
-      tiles_m = static_cast<int>((g.m + TL::kM - 1) / TL::kM);
-      units = tiles_m * tiles_n * g.groups;
-    } else {
-      tiles_m = find_tile(g.ends, g.groups, g.zero_rest, g.m, TL::kM, -1, &s);
-      units = tiles_m * tiles_n;
-    }
-    const int run = (units + kXcds - 1) / kXcds, in_run = blockIdx.x / kXcds;
-    int unit = blockIdx.x % kXcds * run + in_run;
-    if (in_run >= run || unit >= units) return;
-    int tm, tn;
-    if constexpr (SUM_GROUPS) {
-      const int e = unit / (tiles_m * tiles_n);
-      unit -= e * tiles_m * tiles_n;
-      s = group_span(g.ends, e, g.k);
-      banded(unit, tiles_m, tiles_n, &tm, &tn);
-      m0 = int64_t(tm) * TL::kM;
-      k0 = s.first;
-      depth = s.last - s.first;
-    } else {
-      banded(unit, tiles_m, tiles_n, &tm, &tn);
-      find_tile(g.ends, g.groups, g.zero_rest, g.m, TL::kM, tm, &s);
-      m0 = s.first;
-      if (g.ends != nullptr && s.group == g.groups) depth = 0;  // rows behind the last group: zeros
-    }
-    n0 = int64_t(tn) * TL::kN;
+  int64_t m0, k0 = 0, depth = g.k;
+  int tm = -1, tn = 0;
+  auto unit_of = [&](int units) {  // this workgroup's, or -1
+    const int run = (units + kXcds - 1) / kXcds, in_run = blockIdx.x / kXcds, unit = blockIdx.x % kXcds * run + in_run;
+    return in_run < run && unit < units ? unit : -1;
+  };
+  if constexpr (SUM_GROUPS) {
+    const int tiles_m = static_cast<int>((g.m + TL::kM - 1) / TL::kM);
+    const int unit = unit_of(tiles_m * tiles_n * g.groups);
+    if (unit < 0) return;
+    const int e = unit / (tiles_m * tiles_n);
+    s = group_span(g.ends, e, g.k);
+    banded(unit - e * tiles_m * tiles_n, tiles_m, tiles_n, &tm, &tn);
+    m0 = int64_t(tm) * TL::kM;
+    k0 = s.first;
+    depth = s.last - s.first;
+  } else {
+    find_tile(g.ends, g.groups, g.zero_rest, g.m, TL::kM,
+              [&](int tiles_m) {
+                const int unit = unit_of(tiles_m * tiles_n);
+                if (unit >= 0) banded(unit, tiles_m, tiles_n, &tm, &tn);
+                return tm;
+              },
+              &s);
+    if (tm < 0) return;
+    m0 = s.first;
+    if (g.ends != nullptr && s.group == g.groups) depth = 0;  // rows behind the last group: zeros
   }
+  const int64_t n0 = int64_t(tn) * TL::kN;
   const int64_t m_end = SUM_GROUPS ? g.m : s.last;
   const int left_m = static_cast<int>(m_end - m0 < TL::kM ? m_end - m0 : TL::kM);
   const int left_n = static_cast<int>(g.n - n0 < TL::kN ? g.n - n0 : TL::kN);
@@ -716,11 +733,20 @@ __global__ __launch_bounds__(WAVES * 64) void k_few(ProductArgs g) {
   __shared__ __attribute__((aligned(16))) v4f sums[kWaves][MF * NF][64];
   const int tiles_n = static_cast<int>((g.n + 16 * NF - 1) / (16 * NF));
   Span s{0, 0, 0};
-  const int tiles_m = find_tile(g.ends, g.groups, g.zero_rest, g.m, kTileM, -1, &s), units = tiles_m * tiles_n;
-  const int run = (units + kXcds - 1) / kXcds, in_run = blockIdx.x / kXcds, unit = blockIdx.x % kXcds * run + in_run;
-  if (in_run >= run || unit >= units) return;
-  find_tile(g.ends, g.groups, g.zero_rest, g.m, kTileM, unit % tiles_m, &s);  // tiles of one n are neighbours
-  const int64_t m0 = s.first, n0 = int64_t(unit / tiles_m) * (16 * NF);
+  int tm = -1, tn = 0;
+  find_tile(g.ends, g.groups, g.zero_rest, g.m, kTileM,
+            [&](int tiles_m) {
+              const int units = tiles_m * tiles_n, run = (units + kXcds - 1) / kXcds, in_run = blockIdx.x / kXcds;
+              const int unit = blockIdx.x % kXcds * run + in_run;
+              if (in_run < run && unit < units) {  // tiles of one n are neighbours
+                tm = unit % tiles_m;
+                tn = unit / tiles_m;
+              }
+              return tm;
+            },
+            &s);
+  if (tm < 0) return;
+  const int64_t m0 = s.first, n0 = int64_t(tn) * (16 * NF);
   const bool none = g.ends != nullptr && s.group == g.groups;  // rows behind the last group: zeros
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), row = lane & 15, part = lane >> 4;
   const int left_m = static_cast<int>(s.last - m0 < kTileM ? s.last - m0 : kTileM);
