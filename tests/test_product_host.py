@@ -266,3 +266,14 @@ def test_tensor_level_refusals(Z):
         Z.expert_gather(torch.zeros(3, 4), r, torch.zeros(6, 4))
     with pytest.raises(ValueError, match="ids"):
         Z.route(torch.zeros(3, 2), 4)
+
+
+def test_header_is_plain_c(tmp_path):
+    """zs_product.h compiles by itself as C99."""
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "h.c"
+    src.write_text('#include "zs_product.h"\nint main(void) { zs_weight8 w = {0, 0, 0}; return w.codes != 0; }\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-pedantic", "-fsyntax-only", "-I", os.path.join(root, "include"), str(src)],
+                   check=True)
