@@ -22,8 +22,9 @@
  * Conventions as in zs.h and zs_act.h, and:
  *   - rows, cols, outs and experts may be any number within the limits; a matrix of no rows is
  *     written as such.  Matrices at any row stride and alignment of their elements give the same
- *     results; those with a base, row stride and expert stride of a multiple of 16 bytes run
- *     fastest.
+ *     results; those with a base, row stride and expert stride of a multiple of 4 bytes run fastest
+ *     (where rows of a matrix run along the sum, as those of w do with in_major and those of x and
+ *     dy in the weight gradient, with a multiple of 8 columns too).
  *   - ends: device memory, one int32 per expert: the row behind its last; its first row is the one
  *     behind the expert's before it (0 for the first).  The kernels read them when they run.  An
  *     end counts as the largest one up to it, within 0 .. rows, so that no value leads out of the

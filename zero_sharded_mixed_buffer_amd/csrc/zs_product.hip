@@ -236,8 +236,16 @@ struct Operand {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + (u * THREADS + wave * 64) * 16), 16, off[u], 0, 0, 0);
 #endif
   }
-  // a stage into registers, at any alignment, with zeros outside; its addresses are worked out here
+  // A stage into registers, at any alignment, with zeros outside.  OFTEN: one that lies inside takes the
+  // offsets that `direct` has; the addresses of the others are worked out here.
+  template <bool OFTEN = false>
   __device__ __forceinline__ void fetch(int64_t stage, v4u (&r)[kLoads]) const {
+    if (OFTEN && SIZE == 2 && (stage + 1) * kDepth <= depth && stride < (1 << 24) && (!BY_K || left >= (half < 0 ? R : 2 * R))) {
+      const char* p = at(stage);
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) r[u] = *reinterpret_cast<const v4u_a2*>(p + off[u]);
+      return;
+    }
     int id = threadIdx.x;
     asm volatile("" : "+v"(id));
     const int row0 = id / kPerRow, p = piece();
@@ -383,8 +391,8 @@ __device__ __forceinline__ void banded(int u, int tiles_m, int tiles_n, int* m, 
 
 // KIND: ZS_BF16, ZS_FP16 or kEight.  AK, BK: operand a, b lies by k.  SUM_GROUPS: the groups divide
 // k, and each has an output of its own (the weight gradient); otherwise they divide m, and each has
-// a b of its own.  STAGED: stages pass through registers, for operands that are not aligned to 16
-// bytes.
+// a b of its own.  STAGED: stages pass through registers, for operands that are not aligned to
+// whole words.
 template <int KIND, bool AK, bool BK, bool SUM_GROUPS, bool STAGED, class TL>
 __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -559,6 +567,7 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
   // stage i + 1.  Each has a stage and a half of time, with four buffers three and a half.  A wave waits for its own pieces one cluster before they are read;
   // the barrier behind that makes it all waves'.
   constexpr bool kTurns = TL::kThreads == 512;
+  static_assert(!STAGED || KIND != kEight, "8-bit operands are aligned");
   static_assert(!STAGED || kBufs == 2, "a stage in registers, one in LDS beside the present one");
   if (stages > 0) {
     constexpr std::integral_constant<int, 0> kZero{};
@@ -566,7 +575,7 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
     Scales sc;
     int next_b_scale = 0;
     auto none = [] {};
-    auto cluster = [&](int h, auto odd, const char* buf_a, const char* buf_b, auto around) {
+    auto cluster = [&](int h, auto odd, const char* buf_a, const char* buf_b, auto around, auto after) {
       constexpr int kFirst = decltype(odd)::value, kLast = kJoined ? 1 : kFirst;
 #pragma unroll
       for (int q = kFirst; q <= kLast; ++q) {
@@ -588,6 +597,7 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
 #pragma unroll
       for (int q = kFirst; q <= kLast; ++q) multiply(h, q, fa[q - kFirst], sc, odd);
       __builtin_amdgcn_s_setprio(0);
+      after();
       if (kTurns || kLast == 1) meet();
     };
     for (int64_t i = 0; i < kBufs && i < stages; ++i) {
@@ -623,7 +633,7 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
 #pragma unroll
           for (int u = 0; u < kA; ++u) op_a[1].direct(u, p, buffer_a(1, i + kBufs - 1), wave);
         } else if constexpr (STAGED) {
-          if (i + 1 < stages) op_a[1].fetch(i + 1, ra1);
+          if (i + 1 < stages) op_a[1].template fetch<true>(i + 1, ra1);
         } else {
           if (i + kBufs - 1 < stages) begin(op_a[1], i + kBufs - 1, buffer_a(1, i + kBufs - 1));
         }
@@ -633,6 +643,7 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
           if (i > 0 && i + 1 < stages) {
             OpA::leave(ra0, buffer_a(0, i + 1));
             OpB::leave(rb, buffer_b(i + 1));
+            wait_lds();
           }
         }
       };
@@ -646,8 +657,8 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
           for (int u = from; u < to; ++u) op_b.direct(u, pb, b, wave);
         } else if (from == 0 && i + kBufs < stages) {
           if constexpr (STAGED) {
-            op_a[0].fetch(i + kBufs, ra0);
-            op_b.fetch(i + kBufs, rb);
+            op_a[0].template fetch<true>(i + kBufs, ra0);
+            op_b.template fetch<true>(i + kBufs, rb);
           } else {
             begin(op_a[0], i + kBufs, a0);
             begin(op_b, i + kBufs, b);
@@ -656,34 +667,39 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
       };
       auto leave_a1 = [&] {
         if constexpr (STAGED) {
-          if (i + 1 < stages) OpA::leave(ra1, buffer_a(1, i + 1));
+          if (i + 1 < stages) {
+            OpA::leave(ra1, buffer_a(1, i + 1));
+            wait_lds();
+          }
         }
       };
       // how many pieces may be under way behind those that are waited for: the second half of a, then
       // the next stage's first half and b
       if constexpr (kJoined) {
-        cluster(0, kZero, a0, b, [&] {
-          leave_a0_b();
-          wait_loads<kMain ? (kBufs - 1) * (kA + kB) + (kBufs - 2) * kA : 0>();
-          send_a1();
-        });
-        cluster(1, kZero, a1, b, [&] {
-          wait_loads<kMain ? (kBufs - 1) * kA + (kBufs - 2) * (kA + kB) : 0>();
-          send_a0_b(0, kB);
-          leave_a1();
-        });
+        cluster(
+            0, kZero, a0, b,
+            [&] {
+              if constexpr (!STAGED) wait_loads<kMain ? (kBufs - 1) * (kA + kB) + (kBufs - 2) * kA : 0>();
+              send_a1();
+            },
+            leave_a0_b);
+        cluster(
+            1, kZero, a1, b,
+            [&] {
+              if constexpr (!STAGED) wait_loads<kMain ? (kBufs - 1) * kA + (kBufs - 2) * (kA + kB) : 0>();
+              send_a0_b(0, kB);
+            },
+            leave_a1);
       } else {
-        cluster(0, kZero, a0, b, send_a1);
+        cluster(0, kZero, a0, b, send_a1, none);
         cluster(0, kOne, a0, b, [&] {
-          leave_a0_b();
           wait_loads<kMain ? (kBufs - 1) * (kA + kB) + (kBufs - 1) * kA : 0>();
-        });
-        cluster(1, kZero, a1, b, [&] { send_a0_b(0, kB / 2); });
+        }, none);
+        cluster(1, kZero, a1, b, [&] { send_a0_b(0, kB / 2); }, none);
         cluster(1, kOne, a1, b, [&] {
-          leave_a1();
           wait_loads<kMain ? kBufs * kA + kB / 2 + (kBufs - 2) * (kA + kB) : 0>();
           send_a0_b(kB / 2, kB);
-        });
+        }, none);
       }
     };
     int64_t i = 0;
@@ -939,12 +955,11 @@ hipError_t launch_tile(const ProductArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// Whether an operand's stages can go straight to LDS: 16-byte pieces at 16-byte addresses, offsets
-// within a tile of 32 bits; by k also whole pieces at a row's end.
+// Whether an operand's stages can go straight to LDS: pieces at addresses of whole words, which such a
+// load takes (7811 x 3156 -> 4096 over 18 experts 306 us, 520 through registers), offsets within a tile
+// of 32 bits; by k also whole pieces at a row's end.
 bool direct_rows(const void* p, int64_t stride, int64_t group) {
-  return aligned16(p) && stride % 8 == 0 && group % 8 == 0 && stride < (1 << 22);
+  return (reinterpret_cast<uintptr_t>(p) & 3) == 0 && stride % 2 == 0 && group % 2 == 0 && stride < (1 << 22);
 }
 
 template <int KIND, bool AK, bool BK, bool SUM_GROUPS>
