@@ -179,7 +179,6 @@ __device__ __forceinline__ v4u load8_row(const uint16_t* row, int64_t k, int64_t
 }
 
 constexpr int64_t kFewUnits = 512;  // see few_rows
-constexpr int64_t kCus = 256;
 constexpr int kEight = 3;  // the operands' type beside ZS_BF16 and ZS_FP16: e4m3 codes
 
 // One operand of a workgroup, or half of one: R rows of m or n, k from 0 to `depth` (elements).
@@ -564,7 +563,7 @@ __global__ __launch_bounds__(TL::kThreads, 2) void k_product(ProductArgs g) {
   // stage are left out.)
   // A half of a, and b, are free once their clusters have been read, and a later stage goes there, i + 2
   // with two buffers: b and the first half from cluster 2 of stage i on, the second half in cluster 0 of
-  // stage i + 1.  Each has a stage and a half of time, with four buffers three and a half.  A wave waits for its own pieces one cluster before they are read;
+  // stage i + 1.  Each has a stage and a half of time.  A wave waits for its own pieces one cluster before they are read;
   // the barrier behind that makes it all waves'.
   constexpr bool kTurns = TL::kThreads == 512;
   static_assert(!STAGED || KIND != kEight, "8-bit operands are aligned");
@@ -937,8 +936,12 @@ hipError_t launch_few(const ProductArgs& a, hipStream_t s) {
 bool few_rows(const ProductArgs& a) { return product_units(a, false, 32, 32) <= kFewUnits; }
 
 using SmallTile = Tile<2, 2, 2, 2, 2>;  // 128 x 128, two workgroups to a CU
-using DeepTile = Tile<2, 2, 2, 2, 4>;   // the same for launches that have a CU for each workgroup
-using LargeTile = Tile<2, 4, 4, 2, 2>;  // 256 x 256
+using LargeTile = Tile<2, 4, 4, 2, 2>;  // 256 x 256, one workgroup to a CU
+
+// From how many large tiles on they are taken: below, too many CUs have none.  4096 -> 4096, 8 bits, us
+// with large and with small tiles: 2048 rows (128 large tiles) 52 and 38, 3000 rows (192) 56 and 62,
+// 4096 rows (256) 62 and 73; weight gradients 2048 rows of 1024 x 4096 (64) 43 and 33.
+constexpr int64_t kLargeUnits = 192;
 
 // ------------------------------------------------------------------ launch choices
 
@@ -971,10 +974,8 @@ hipError_t launch_sizes(const ProductArgs& a, hipStream_t s) {
                       (!BK || a.n % 8 == 0);
   if (!direct) return launch_tile<KIND, AK, BK, SUM_GROUPS, true, SmallTile>(a, s);
   const int64_t per_group = SUM_GROUPS ? a.m : a.m / std::max(1, a.groups);
-  if (per_group >= 192 && a.n >= 192 && product_units(a, SUM_GROUPS, LargeTile::kM, LargeTile::kN) >= 200)
+  if (per_group >= 192 && a.n >= 192 && product_units(a, SUM_GROUPS, LargeTile::kM, LargeTile::kN) >= kLargeUnits)
     return launch_tile<KIND, AK, BK, SUM_GROUPS, false, LargeTile>(a, s);
-  if (product_units(a, SUM_GROUPS, DeepTile::kM, DeepTile::kN) <= kCus)
-    return launch_tile<KIND, AK, BK, SUM_GROUPS, false, DeepTile>(a, s);
   return launch_tile<KIND, AK, BK, SUM_GROUPS, false, SmallTile>(a, s);
 }
 
@@ -989,10 +990,8 @@ int64_t product_units(const ProductArgs& a, bool sum_groups, int64_t tile_m, int
 
 hipError_t launch_product8(const ProductArgs& a, hipStream_t s) {
   if (few_rows(a)) return launch_few<kEight>(a, s);
-  if (product_units(a, false, LargeTile::kM, LargeTile::kN) >= 200)
+  if (product_units(a, false, LargeTile::kM, LargeTile::kN) >= kLargeUnits)
     return launch_tile<kEight, false, false, false, false, LargeTile>(a, s);
-  if (product_units(a, false, DeepTile::kM, DeepTile::kN) <= kCus)
-    return launch_tile<kEight, false, false, false, false, DeepTile>(a, s);
   return launch_tile<kEight, false, false, false, false, SmallTile>(a, s);
 }
 
