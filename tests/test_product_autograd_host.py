@@ -1,0 +1,98 @@
+"""CPU tests of what the products' layers tell autograd: the layers run on host tensors with the launch
+itself replaced, so that no kernel runs."""
+
+import pytest
+import torch
+import torch.autograd.forward_ad as fwd
+
+BF16 = torch.bfloat16
+pytestmark = pytest.mark.filterwarnings("ignore::torch.jit.TracerWarning")
+
+
+@pytest.fixture
+def Z(monkeypatch):
+    import zero_sharded_mixed_buffer_amd as Z
+    for module in (Z.activations, Z.products):
+        monkeypatch.setattr(module, "_need_gpu", lambda device: None)
+        monkeypatch.setattr(module, "_enqueue", lambda name, device, *args: None)
+    Z.lib()
+    return Z
+
+
+def _randn(*shape, seed=0, dtype=BF16):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+def _route(Z):
+    as_int = dict(dtype=torch.int32)
+    return Z.Route(torch.tensor([3, 6], **as_int), torch.arange(6, **as_int), torch.arange(6, **as_int).view(3, 2))
+
+
+# each layer as a function of one of its inputs, and that input
+LAYERS = {
+    "linear8 of x": lambda Z: (lambda x: Z.linear8(x, _randn(5, 8)), _randn(6, 8)),
+    "linear8 of the weight": lambda Z: (lambda w: Z.linear8(_randn(6, 8), w), _randn(5, 8)),
+    "experts of x": lambda Z: (lambda x: Z.experts(x, _randn(2, 5, 8), _route(Z).ends), _randn(6, 8)),
+    "experts of the weight": lambda Z: (lambda w: Z.experts(_randn(6, 8), w, _route(Z).ends), _randn(2, 5, 8)),
+    "dispatch": lambda Z: (lambda x: Z.dispatch(x, _route(Z)), _randn(3, 8)),
+    "combine of y": lambda Z: (lambda y: Z.combine(y, _route(Z), torch.ones(3, 2)), _randn(6, 8)),
+    "combine of the weights": lambda Z: (lambda w: Z.combine(_randn(6, 8), _route(Z), w), _randn(3, 2, dtype=torch.float32)),
+}
+
+
+# ------------------------------------------------------------------------------ other derivatives, traces
+
+@pytest.mark.parametrize("layer", LAYERS)
+@pytest.mark.parametrize("requires_grad", [False, True])
+def test_forward_mode_is_refused(Z, layer, requires_grad):
+    """No layer has a forward-mode derivative: a dual input is refused, as by torch's own functions
+    without one, and its tangent does not get lost."""
+    f, leaf = LAYERS[layer](Z)
+    f(leaf)  # an ordinary one passes
+    with fwd.dual_level():
+        f(leaf)
+        with pytest.raises(NotImplementedError, match="jvp"):
+            f(fwd.make_dual(leaf.clone().requires_grad_(requires_grad), torch.ones_like(leaf)))
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(f, (leaf,), (torch.ones_like(leaf),))
+
+
+@pytest.mark.parametrize("layer", LAYERS)
+@pytest.mark.parametrize("requires_grad", [False, True])
+def test_a_trace_holds_the_layer(Z, monkeypatch, layer, requires_grad):
+    """What a trace records is the layer's function, and not the allocation of its output alone: each call
+    of it enqueues what a call of the layer does."""
+    calls = []
+    for module in (Z.activations, Z.products):
+        monkeypatch.setattr(module, "_enqueue", lambda name, device, *args: calls.append(name))
+    f, leaf = LAYERS[layer](Z)
+    f(leaf)
+    want, calls[:] = list(calls), []
+    traced = torch.jit.trace(f, (leaf.requires_grad_(requires_grad),), check_trace=False)
+    assert calls == want
+    calls.clear()
+    traced(leaf.detach())
+    assert calls == want
+
+
+def test_a_trace_routes_anew(Z, monkeypatch):
+    """A traced function's route is the one of its present choices, for the layers behind it too."""
+    def enqueue(name, device, *args):
+        if name == "zs_route":
+            routed.append(args[0])  # the choices' address
+        elif name == "zs_expert_gather":
+            gathered.append(args[3])  # the slots' address
+
+    routed, gathered = [], []
+    monkeypatch.setattr(Z.products, "_enqueue", enqueue)
+
+    def f(x, ids):
+        r = Z.route(ids, 2)
+        return r.slot, Z.dispatch(x, r)
+
+    x = _randn(3, 8)
+    traced = torch.jit.trace(f, (x, torch.zeros(3, 2, dtype=torch.int64)), check_trace=False)
+    for leaf in (x, x.clone().requires_grad_()):
+        ids = torch.ones(3, 2, dtype=torch.int64)
+        slot, out = traced(leaf, ids)
+        assert routed[-1] == ids.data_ptr() and gathered[-1] == slot.data_ptr() and out.shape == (6, 8)

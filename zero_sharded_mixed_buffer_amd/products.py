@@ -20,11 +20,12 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _abi as A
 from .activations import (_DTYPES, CODES, HALF, Act8, _add_in_turn, _at, _check_grad_into, _checkpoint, _enqueue, _fills,
-                          _has_own_version, _input, _matrix, _need_gpu, _rows, _workspace, _wrote, act_pack, act_wgrad)
+                          _has_own_version, _input, _matrix, _need_gpu, _rows, _workspace, _wrote, act_wgrad)
 
 BLOCK = 128
 
@@ -253,9 +254,14 @@ def route(ids, experts, workspace=None):
         raise ValueError(f"ids must be [tokens, choices], got shape {tuple(ids.shape)}")
     if ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
         raise ValueError("ids must be int32 or int64 and contiguous")
-    device = ids.device
-    _need_gpu(device)
-    experts, slots = int(experts), ids.numel()
+    _need_gpu(ids.device)
+    if _traced():
+        return _route_of(*_Routed.apply(ids, int(experts), workspace))
+    return _route_of(*_route(ids, int(experts), workspace))
+
+
+def _route(ids, experts, workspace):
+    device, slots = ids.device, ids.numel()
     own = workspace is None
     workspace, size = _workspace(workspace, A.zs_route_workspace(slots, experts), device)
     ends = torch.empty(experts, dtype=torch.int32, device=device)
@@ -265,9 +271,28 @@ def route(ids, experts, workspace=None):
              place.data_ptr(), workspace.data_ptr(), size)
     if not own:
         _wrote((workspace,))
-    out = Route.__new__(Route)  # nothing to check
+    return ends, slot, place
+
+
+def _route_of(ends, slot, place):
+    """A Route of arrays that need no checks."""
+    out = Route.__new__(Route)
     out.ends, out.slot, out.place = ends, slot, place
     return out
+
+
+class _Routed(torch.autograd.Function):
+    """route as one operation of a trace."""
+
+    @staticmethod
+    def forward(ctx, ids, experts, workspace):
+        out = _route(ids, experts, workspace)
+        ctx.mark_non_differentiable(*out)
+        return out
+
+    @staticmethod
+    def backward(ctx, *grads):
+        return None, None, None
 
 
 def _routed(route, device):
@@ -337,12 +362,26 @@ def expert_combine_backward(dout, y, route, weights=None, dy=None, dweights=None
 # ------------------------------------------------------------------------------ autograd
 
 def _differentiated(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    """Whether a layer has to go through its autograd function.  Without a gradient that costs host time
+    for nothing, but forward-mode derivatives and function transforms are refused there, and a trace
+    records the function (outside of it, the output's allocation alone)."""
+    return (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+            or forward_ad._current_level >= 0 or torch._C._are_functorch_transforms_active() or _traced())
+
+
+def _traced():
+    return torch._C._get_tracing_state() is not None
+
+
+def _eights(x, weight, x8, w8, turned):
+    """The 8-bit forms of a layer's operands that are not given."""
+    return (Act8.of(_rows(x)) if x8 is None else x8), (Weight8.of(weight, turned) if w8 is None else w8)
 
 
 class _Linear8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, x8, w8, grad_into):
+        x8, w8 = _eights(x, weight, x8, w8, ctx.needs_input_grad[0])
         y = torch.empty(*x.shape[:-1], w8.outs, dtype=x.dtype, device=x.device)
         product8(x8, w8, y.view(-1, w8.outs))
         ctx.shape, ctx.grad_into = x.shape, grad_into
@@ -403,18 +442,13 @@ def linear8(x, weight, w8=None, x8=None, grad_into=None):
     _check_grad_into(grad_into, weight)
     rows = x.numel() // cols
     turned = x.requires_grad and torch.is_grad_enabled()
-    if x8 is None:
-        x8 = Act8.empty(rows, cols, "e4m3", x.device)
-        act_pack(_rows(x.detach()), x8)
-    else:
+    if x8 is not None:
         if x8.code != "e4m3":
             raise ValueError("x8 must hold e4m3 codes")
         _checkpoint(x8, "x8", rows, cols, x.device)
         if x8._outlived(x):
             raise ValueError("x has been changed in place since x8 was taken of it")
-    if w8 is None:
-        w8 = Weight8.of(weight.detach(), transposed=turned)
-    else:
+    if w8 is not None:
         if (w8.outs, w8.cols) != (outs, cols) or w8.device != x.device:
             raise ValueError(f"w8 is a weight of {w8.outs} x {w8.cols} on {w8.device}, not of {outs} x {cols} on {x.device}")
         if turned and w8.codes_t is None:
@@ -422,6 +456,7 @@ def linear8(x, weight, w8=None, x8=None, grad_into=None):
         if w8._outlived(weight):
             raise ValueError("the weight has been changed in place since w8 was taken of it")
     if not _differentiated(x, weight):
+        x8, w8 = _eights(x, weight, x8, w8, False)
         y = torch.empty(*x.shape[:-1], outs, dtype=x.dtype, device=x.device)
         product8(x8, w8, y.view(-1, outs))
         return y
@@ -495,18 +530,18 @@ def _gathered(x, route):
 
 class _Dispatch(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, route):
-        out = _gathered(x, route)
-        ctx.save_for_backward(route.ends, route.slot, route.place)
+    def forward(ctx, x, *places):
+        out = _gathered(x, _route_of(*places))
+        ctx.save_for_backward(*places)
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        route = Route(*ctx.saved_tensors)
+        route = _route_of(*ctx.saved_tensors)
         dx = torch.empty(route.tokens, dout.shape[1], dtype=dout.dtype, device=dout.device)
         expert_combine(_rows(dout), route, dx)
-        return dx, None
+        return dx, None, None, None
 
 
 def dispatch(x, route):
@@ -515,7 +550,7 @@ def dispatch(x, route):
         raise ValueError("x must be a bf16, fp16 or fp32 tensor with at least one column")
     if not _differentiated(x):
         return _gathered(_rows(x), route)
-    return _Dispatch.apply(_rows(x), route)
+    return _Dispatch.apply(_rows(x), route.ends, route.slot, route.place)
 
 
 def _combined(y, weights, route):
@@ -526,17 +561,17 @@ def _combined(y, weights, route):
 
 class _Combine(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, y, weights, route):
-        out = _combined(y, weights, route)
+    def forward(ctx, y, weights, *places):
+        out = _combined(y, weights, _route_of(*places))
         kept = y if weights is not None and ctx.needs_input_grad[1] else None
-        ctx.save_for_backward(route.ends, route.slot, route.place, weights, kept)
+        ctx.save_for_backward(*places, weights, kept)
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
         *places, weights, y = ctx.saved_tensors
-        route = Route(*places)
+        route = _route_of(*places)
         dout = _rows(dout)
         dy = dweights = None
         if ctx.needs_input_grad[0]:
@@ -544,7 +579,7 @@ class _Combine(torch.autograd.Function):
         if y is not None:
             dweights = torch.empty_like(weights)
         expert_combine_backward(dout, y, route, weights, dy, dweights)
-        return dy, dweights, None
+        return dy, dweights, None, None, None
 
 
 def combine(y, route, weights=None):
@@ -555,4 +590,4 @@ def combine(y, route, weights=None):
     weights = weights.contiguous() if weights is not None else None
     if not _differentiated(y, weights):
         return _combined(_rows(y), weights, route)
-    return _Combine.apply(_rows(y), weights, route)
+    return _Combine.apply(_rows(y), weights, route.ends, route.slot, route.place)
