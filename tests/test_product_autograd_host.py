@@ -40,6 +40,23 @@ LAYERS = {
 }
 
 
+# ------------------------------------------------------------------------------ what is kept
+
+def test_experts_keep_the_weight_for_the_inputs_gradient_alone(Z):
+    """A weight may change before a backward pass that reads nothing of it, and not before another."""
+    x, w = _randn(6, 8), _randn(2, 5, 8).requires_grad_()
+    y = Z.experts(x, w, _route(Z).ends)
+    with torch.no_grad():
+        w.mul_(2)
+    y.sum().backward()
+    assert w.grad.shape == w.shape and w.grad.dtype == w.dtype
+    y = Z.experts(x.requires_grad_(), w, _route(Z).ends)
+    with torch.no_grad():
+        w.mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
 # ------------------------------------------------------------------------------ other derivatives, traces
 
 @pytest.mark.parametrize("layer", LAYERS)

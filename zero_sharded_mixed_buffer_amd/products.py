@@ -477,7 +477,8 @@ class _Experts(torch.autograd.Function):
                 kept = [x8.codes, x8.scales]
             else:
                 kept = [x]
-        ctx.save_for_backward(ends, weight, *kept)
+        ctx.save_for_backward(ends, weight if ctx.needs_input_grad[0] else None, *kept)
+        ctx.like = weight.shape, weight.dtype
         return y
 
     @staticmethod
@@ -493,7 +494,8 @@ class _Experts(torch.autograd.Function):
             into = ctx.grad_into
             x = kept[0] if ctx.save is None else Act8(kept[0], kept[1], ctx.cols, ctx.save).unpack(dy.dtype)
             if into is None:
-                dw = torch.empty(weight.shape, dtype=weight.dtype, device=weight.device)
+                shape, dtype = ctx.like
+                dw = torch.empty(shape, dtype=dtype, device=dy.device)
                 expert_wgrad(x, dy2, ends, dw, in_major=ctx.in_major)
             else:
                 _add_in_turn(into, lambda: expert_wgrad(x, dy2, ends, into, base=into, in_major=ctx.in_major))
