@@ -57,6 +57,20 @@ def test_experts_keep_the_weight_for_the_inputs_gradient_alone(Z):
         y.sum().backward()
 
 
+def test_combine_keeps_the_weights_for_the_rows_gradient_alone(Z):
+    y, weights = _randn(6, 8), torch.ones(3, 2).requires_grad_()
+    out = Z.combine(y, _route(Z), weights)
+    with torch.no_grad():
+        weights.mul_(2)
+    out.sum().backward()
+    assert weights.grad.shape == (3, 2)
+    out = Z.combine(y.requires_grad_(), _route(Z), weights)
+    with torch.no_grad():
+        weights.mul_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+
+
 # ------------------------------------------------------------------------------ other derivatives, traces
 
 @pytest.mark.parametrize("layer", LAYERS)

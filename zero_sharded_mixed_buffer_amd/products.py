@@ -565,8 +565,8 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, *places):
         out = _combined(y, weights, _route_of(*places))
-        kept = y if weights is not None and ctx.needs_input_grad[1] else None
-        ctx.save_for_backward(*places, weights, kept)
+        turn_y, turn_weights = ctx.needs_input_grad[0], weights is not None and ctx.needs_input_grad[1]
+        ctx.save_for_backward(*places, weights if turn_y else None, y if turn_weights else None)
         return out
 
     @staticmethod
@@ -579,7 +579,7 @@ class _Combine(torch.autograd.Function):
         if ctx.needs_input_grad[0]:
             dy = torch.empty(route.rows, dout.shape[1], dtype=dout.dtype, device=dout.device)
         if y is not None:
-            dweights = torch.empty_like(weights)
+            dweights = torch.empty(route.tokens, route.choices, dtype=torch.float32, device=dout.device)
         expert_combine_backward(dout, y, route, weights, dy, dweights)
         return dy, dweights, None, None, None
 
