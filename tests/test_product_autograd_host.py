@@ -127,3 +127,22 @@ def test_a_trace_routes_anew(Z, monkeypatch):
         ids = torch.ones(3, 2, dtype=torch.int64)
         slot, out = traced(leaf, ids)
         assert routed[-1] == ids.data_ptr() and gathered[-1] == slot.data_ptr() and out.shape == (6, 8)
+
+
+# ------------------------------------------------------------------------------ strides that mean nothing
+
+def test_base_of_the_experts_gradients_has_the_strides_that_count(Z):
+    """With one expert the stride between experts means nothing, with one row that between rows."""
+    ends = torch.tensor([6], dtype=torch.int32)
+    x, dy = _randn(6, 8), _randn(6, 5)
+    dw = torch.empty(1, 5, 8, dtype=BF16)
+    Z.expert_wgrad(x, dy, ends, dw, base=torch.empty(4, 5, 8, dtype=BF16)[:1].as_strided((1, 5, 8), (999, 8, 1)))
+    one = _randn(6, 1)
+    Z.expert_wgrad(x, one, ends, torch.empty(1, 1, 8, dtype=BF16), base=torch.empty(1, 1, 20, dtype=BF16)[:, :, :8])
+    two = torch.tensor([2, 6], dtype=torch.int32)
+    dw = torch.empty(2, 1, 8, dtype=BF16)
+    Z.expert_wgrad(x, one, two, dw, base=torch.empty(2 * 8, dtype=BF16).as_strided((2, 1, 8), (8, 77, 1)))
+    with pytest.raises(ValueError, match="same strides"):
+        Z.expert_wgrad(x, one, two, dw, base=torch.empty(2, 2, 8, dtype=BF16)[:, :1])
+    with pytest.raises(ValueError, match="same strides"):
+        Z.expert_wgrad(x, dy, ends, torch.empty(1, 5, 8, dtype=BF16), base=torch.empty(1, 5, 9, dtype=BF16)[:, :, :8])

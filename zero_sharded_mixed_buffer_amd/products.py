@@ -200,7 +200,8 @@ def expert_wgrad(x, dy, ends, dw, base=None, in_major=False):
     shape = (cols, outs) if in_major else (outs, cols)
     dws, apart = _expert_matrices(dw, "dw", (x.dtype, torch.float32), experts, *shape, dev)
     if base is not None and base is not dw:
-        if _expert_matrices(base, "base", (dw.dtype,), experts, *shape, dev) != (dws, apart):
+        row, far = _expert_matrices(base, "base", (dw.dtype,), experts, *shape, dev)
+        if (row != dws and shape[0] > 1) or (far != apart and experts > 1):
             raise ValueError("base and dw must have the same strides")
     _enqueue("zs_expert_wgrad", dev, x.data_ptr(), xs, dy.data_ptr(), dys, _DTYPES[x.dtype], ends.data_ptr(), experts, rows,
              cols, outs, dw.data_ptr(), _DTYPES[dw.dtype], dws, apart, 1 if in_major else 0, _at(base))
