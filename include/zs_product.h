@@ -120,7 +120,10 @@ zs_status zs_route(const void* ids, int32_t id_bytes, int64_t slots, int32_t exp
 /* Rows in the order of their experts: out[p] = x[slot[p] / choices], zeros where slot[p] is not
  * within 0 .. tokens * choices - 1.
  *   x: tokens x cols, out: tokens * choices x cols, of dtype bf16, fp16 or fp32.
- * Errors: ZS_EINVAL on a NULL pointer, a bad dtype, size, stride or alignment. */
+ * tokens * choices is at most 2^31 - 4096, and the rows of out, at 16 lanes to a row of up to 256 bytes
+ * and twice as many up to each power of two, but 256 at most, have fewer than 2^32 lanes: that is
+ * below 2^28 rows of up to 256 bytes and 2^24 of more than 2048.
+ * Errors: ZS_EINVAL on a NULL pointer, a bad dtype, size, stride or alignment, or sizes past one launch. */
 zs_status zs_expert_gather(const void* x, int64_t x_stride, zs_dtype dtype, const int32_t* slot, int64_t tokens,
                            int32_t choices, int64_t cols, void* out, int64_t out_stride, void* stream);
 
@@ -128,7 +131,7 @@ zs_status zs_expert_gather(const void* x, int64_t x_stride, zs_dtype dtype, cons
  * fp32, rounded once.  Choices whose place is not within 0 .. tokens * choices - 1 count nothing.
  *   y: tokens * choices x cols, out: tokens x cols, of dtype bf16, fp16 or fp32.
  *   weights: NULL (ones) or tokens x choices fp32, consecutive.
- * Errors: as zs_expert_gather. */
+ * Errors: as zs_expert_gather, whose limits hold for the tokens here. */
 zs_status zs_expert_combine(const void* y, int64_t y_stride, zs_dtype dtype, const int32_t* place,
                             const float* weights, int64_t tokens, int32_t choices, int64_t cols, void* out,
                             int64_t out_stride, void* stream);
@@ -140,7 +143,7 @@ zs_status zs_expert_combine(const void* y, int64_t y_stride, zs_dtype dtype, con
  * two choices share, which no route has, gets one of the two.)
  *   dy: NULL or a matrix like y.  dweights: NULL or tokens x choices fp32; needs y, which may be
  *   NULL otherwise.  dy may be y itself (same stride).
- * Errors: as zs_expert_gather, and ZS_EINVAL when neither output is given or dy is in y's place at
+ * Errors: as zs_expert_combine, and ZS_EINVAL when neither output is given or dy is in y's place at
  * another stride. */
 zs_status zs_expert_combine_backward(const void* dout, int64_t dout_stride, const void* y, int64_t y_stride,
                                      zs_dtype dtype, const int32_t* slot, const int32_t* place,

@@ -1232,15 +1232,15 @@ zs_status check_expert_matrices(const void* p, int64_t stride, int64_t apart, in
   return ok();
 }
 
-zs_status check_routing(int64_t tokens, int32_t choices, int64_t cols, int dt) {
+// by_rows: the launch is over the routed rows, otherwise over the tokens.
+zs_status check_routing(int64_t tokens, int32_t choices, int64_t cols, int dt, bool by_rows) {
   if (!is_grad_dtype(dt)) return fail(ZS_EINVAL, "dtype must be bf16, fp16 or fp32");
   if (choices < 1) return fail(ZS_EINVAL, "choices must be positive");
   zs_status st = check_sizes(tokens, cols);
   if (st != ZS_OK) return st;
   if (tokens > zs::kMaxSlots / choices) return fail(ZS_EINVAL, "tokens x choices exceeds 2^31 - 4096");
-  // a launch holds fewer than 2^32 threads, up to 256 for a row
-  if (tokens * choices > zs::kProductMaxUnits * 2 && cols > 64)
-    return fail(ZS_EINVAL, "tokens x choices exceeds one launch");
+  if (zs::expert_row_blocks(by_rows ? tokens * choices : tokens, cols, dt) > zs::kExpertMaxBlocks)
+    return fail(ZS_EINVAL, by_rows ? "tokens x choices exceeds one launch" : "tokens exceeds one launch");
   return check_sizes(tokens * choices, cols);
 }
 
@@ -1435,7 +1435,7 @@ extern "C" zs_status zs_route(const void* ids, int32_t id_bytes, int64_t slots, 
 extern "C" zs_status zs_expert_gather(const void* x, int64_t x_stride, zs_dtype dtype, const int32_t* slot, int64_t tokens,
                                       int32_t choices, int64_t cols, void* out, int64_t out_stride, void* stream) {
   const TraceRange trace("zs_expert_gather");
-  zs_status st = check_routing(tokens, choices, cols, dtype);
+  zs_status st = check_routing(tokens, choices, cols, dtype, true);
   const int64_t rows = st == ZS_OK ? tokens * choices : 0;
   if (st == ZS_OK) st = check_matrix(x, x_stride, dtype, tokens, cols, "x");
   if (st == ZS_OK) st = check_words(slot, rows, "slot");
@@ -1458,7 +1458,7 @@ extern "C" zs_status zs_expert_combine(const void* y, int64_t y_stride, zs_dtype
                                        const float* weights, int64_t tokens, int32_t choices, int64_t cols, void* out,
                                        int64_t out_stride, void* stream) {
   const TraceRange trace("zs_expert_combine");
-  zs_status st = check_routing(tokens, choices, cols, dtype);
+  zs_status st = check_routing(tokens, choices, cols, dtype, false);
   const int64_t rows = st == ZS_OK ? tokens * choices : 0;
   if (st == ZS_OK) st = check_matrix(y, y_stride, dtype, rows, cols, "y");
   if (st == ZS_OK) st = check_words(place, rows, "place");
@@ -1484,7 +1484,7 @@ extern "C" zs_status zs_expert_combine_backward(const void* dout, int64_t dout_s
                                                 const float* weights, int64_t tokens, int32_t choices, int64_t cols,
                                                 void* dy, int64_t dy_stride, float* dweights, void* stream) {
   const TraceRange trace("zs_expert_combine_backward");
-  zs_status st = check_routing(tokens, choices, cols, dtype);
+  zs_status st = check_routing(tokens, choices, cols, dtype, false);
   const int64_t rows = st == ZS_OK ? tokens * choices : 0;
   if (st != ZS_OK) return st;
   if (rows > 0 && dy == nullptr && dweights == nullptr) return fail(ZS_EINVAL, "no output is given");

@@ -394,6 +394,8 @@ int64_t row_blocks(int64_t rows, int lg) { return (rows + (int64_t(1) << lg) - 1
 
 }  // namespace
 
+int64_t expert_row_blocks(int64_t rows, int64_t cols, int dt) { return row_blocks(rows, rows_log2(cols, dt == ZS_FP32 ? 4 : 8)); }
+
 int64_t route_workspace(int64_t slots, int experts) {
   const int64_t chunks = (slots + kRouteChunk - 1) / kRouteChunk;
   if (chunks <= 1) return 16;

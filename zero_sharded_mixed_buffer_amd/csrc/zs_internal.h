@@ -246,6 +246,9 @@ struct RowsArgs {
   int64_t rows, cols, x_stride, out_stride;  // rows: tokens * choices
   int32_t choices, rows_log2;
 };
+// Workgroups of the gather's launch over rows, or the combination's over tokens.
+int64_t expert_row_blocks(int64_t rows, int64_t cols, int dt);
+constexpr int64_t kExpertMaxBlocks = (int64_t(1) << 24) - 1;  // of 256 threads: a launch holds fewer than 2^32
 hipError_t launch_expert_gather(RowsArgs a, int dt, hipStream_t s);
 hipError_t launch_expert_combine(RowsArgs a, int dt, hipStream_t s);
 struct CombineBackwardArgs {
