@@ -25,6 +25,8 @@
  *     results; those with a base, row stride and expert stride of a multiple of 4 bytes run fastest
  *     (where rows of a matrix run along the sum, as those of w do with in_major and those of x and
  *     dy in the weight gradient, with a multiple of 8 columns too).
+ *   - an output may not lie in an input's memory, but where a call says so; one that begins where an
+ *     input does is refused.
  *   - ends: device memory, one int32 per expert: the row behind its last; its first row is the one
  *     behind the expert's before it (0 for the first).  The kernels read them when they run.  An
  *     end counts as the largest one up to it, within 0 .. rows, so that no value leads out of the

@@ -46,3 +46,32 @@ def test_rows_of_one_launch(Z, cols, dtype):
         Z.zs_expert_gather(None, tokens=most // 7, **{**gather, "choices": 7})
     with pytest.raises(Z.ZsInvalidArgument, match="one launch"):
         Z.zs_expert_gather(None, tokens=most // 7 + 1, **{**gather, "choices": 7})
+
+
+def test_outputs_in_an_inputs_place_are_refused(Z):
+    """Rows are written while others still read them: an output that begins where an input does is
+    refused, but for those that the calls name."""
+    def refused(fn, good, **bad):
+        with pytest.raises(Z.ZsInvalidArgument, match="same memory|in place of"):
+            fn(**{**good, **bad}, stream=0)
+
+    x, w, y = P, 2 * P, 3 * P
+    product = dict(x=x, x_stride=64, weight=w, w_stride=64, w_expert_stride=64 * 64, dtype=BF16, ends=P, experts=2, rows=9, cols=64,
+                   outs=64, in_major=False, y=y, y_stride=64)
+    for in_major in (False, True):
+        refused(Z.zs_expert_product, product, y=x, in_major=in_major)
+        refused(Z.zs_expert_product, product, y=w, in_major=in_major)
+    wgrad = dict(x=x, x_stride=64, dy=w, dy_stride=64, dtype=BF16, ends=P, experts=2, rows=9, cols=64, outs=64, dw=y, dw_dtype=BF16,
+                 dw_stride=64, dw_expert_stride=64 * 64)
+    refused(Z.zs_expert_wgrad, wgrad, dw=x)
+    refused(Z.zs_expert_wgrad, wgrad, dw=w)
+    gather = dict(x=x, x_stride=64, dtype=BF16, slot=P, tokens=5, choices=1, cols=64, out=x, out_stride=64)
+    refused(Z.zs_expert_gather, gather)
+    combine = dict(y=x, y_stride=64, dtype=BF16, place=P, weights=None, tokens=5, choices=1, cols=64, out=x, out_stride=64)
+    refused(Z.zs_expert_combine, combine)
+    backward = dict(dout=x, dout_stride=64, y=y, y_stride=64, dtype=BF16, slot=P, place=P, weights=P, tokens=5, choices=1, cols=64,
+                    dy=x, dy_stride=64)
+    refused(Z.zs_expert_combine_backward, backward)
+    refused(Z.zs_weight8_pack, dict(src=x, src_dtype=BF16, src_stride=64, outs=48, cols=64, w8=Z.Weight8Arrays(w, w, y)))
+    refused(Z.zs_product8, dict(x8=Z.ActArrays(x, w, 0, 0), rows=4, w8=Z.Weight8Arrays(y, None, 4 * P), outs=48, cols=64,
+                                transposed=False, y=x, y_dtype=BF16, y_stride=64))

@@ -1187,6 +1187,12 @@ extern "C" zs_status zs_act_wgrad(const zs_act* x8, int64_t rows, int64_t cols, 
 
 namespace {
 
+// An output whose rows other workgroups' inputs may lie under: `out` may not begin where `in` does.
+zs_status check_apart(const void* out, const char* out_name, const void* in, const char* in_name) {
+  if (out != nullptr && out == in) return fail(ZS_EINVAL, "%s and %s are the same memory", out_name, in_name);
+  return ok();
+}
+
 zs_status check_weight8_sizes(int64_t outs, int64_t cols) {
   zs_status st = check_sizes(outs, cols);
   if (st != ZS_OK) return st;
@@ -1272,6 +1278,7 @@ extern "C" zs_status zs_weight8_pack(const void* src, zs_dtype src_dtype, int64_
   zs_status st = check_weight8_sizes(outs, cols);
   if (st == ZS_OK) st = check_matrix(src, src_stride, src_dtype, outs, cols, "src");
   if (st == ZS_OK) st = check_weight8(w8, false);
+  if (st == ZS_OK) st = check_apart(w8->codes_t, "w8: the transposed codes", w8->codes, "the codes");
   if (st != ZS_OK) return st;
   hipError_t e = zs::launch_weight8(src, src_dtype, src_stride, outs, cols, static_cast<uint8_t*>(w8->codes),
                                     static_cast<uint8_t*>(w8->codes_t), static_cast<uint8_t*>(w8->scales), as_stream(stream));
@@ -1310,6 +1317,9 @@ extern "C" zs_status zs_product8(const zs_act* x8, int64_t rows, const zs_weight
   if (rows > zs::kMaxSlots || zs::product_units(a, false, zs::kProductTile, zs::kProductTile) > zs::kProductMaxUnits)
     return fail(ZS_EINVAL, "rows x outs exceeds one launch");
   if (rows == 0) return ok();
+  st = check_apart(y, "y", a.a, "x8's codes");
+  if (st == ZS_OK) st = check_apart(y, "y", a.b, "w8's codes");
+  if (st != ZS_OK) return st;
   hipError_t e = zs::launch_product8(a, as_stream(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "launching the 8-bit product");
 }
@@ -1345,6 +1355,9 @@ extern "C" zs_status zs_expert_product(const void* x, int64_t x_stride, const vo
   if (zs::product_units(a, false, zs::kProductTile, zs::kProductTile) > zs::kProductMaxUnits)
     return fail(ZS_EINVAL, "rows x outs exceeds one launch");
   if (rows == 0) return ok();
+  st = check_apart(y, "y", x, "x");
+  if (st == ZS_OK) st = check_apart(y, "y", w, "w");
+  if (st != ZS_OK) return st;
   hipError_t e = zs::launch_expert_product(a, dtype, in_major != 0, as_stream(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "launching the experts' products");
 }
@@ -1384,6 +1397,9 @@ extern "C" zs_status zs_expert_wgrad(const void* x, int64_t x_stride, const void
   if (dw_rows == 0) return ok();
   if (zs::product_units(a, true, zs::kProductTile, zs::kProductTile) > zs::kProductMaxUnits)
     return fail(ZS_EINVAL, "experts x outs x cols exceeds one launch");
+  if (rows > 0) st = check_apart(dw, "dw", x, "x");
+  if (st == ZS_OK && rows > 0) st = check_apart(dw, "dw", dy, "dy");
+  if (st != ZS_OK) return st;
   hipError_t e = zs::launch_expert_wgrad(a, dtype, as_stream(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "launching the experts' weight gradients");
 }
@@ -1440,6 +1456,7 @@ extern "C" zs_status zs_expert_gather(const void* x, int64_t x_stride, zs_dtype 
   if (st == ZS_OK) st = check_matrix(x, x_stride, dtype, tokens, cols, "x");
   if (st == ZS_OK) st = check_words(slot, rows, "slot");
   if (st == ZS_OK) st = check_matrix(out, out_stride, dtype, rows, cols, "out");
+  if (st == ZS_OK && rows > 0) st = check_apart(out, "out", x, "x");
   if (st != ZS_OK) return st;
   zs::RowsArgs a{};
   a.x = x;
@@ -1464,6 +1481,7 @@ extern "C" zs_status zs_expert_combine(const void* y, int64_t y_stride, zs_dtype
   if (st == ZS_OK) st = check_words(place, rows, "place");
   if (st == ZS_OK) st = check_words(weights, 0, "weights");
   if (st == ZS_OK) st = check_matrix(out, out_stride, dtype, tokens, cols, "out");
+  if (st == ZS_OK && rows > 0) st = check_apart(out, "out", y, "y");
   if (st != ZS_OK) return st;
   zs::RowsArgs a{};
   a.x = y;
@@ -1498,6 +1516,8 @@ extern "C" zs_status zs_expert_combine_backward(const void* dout, int64_t dout_s
   if (st != ZS_OK) return st;
   if (dweights != nullptr && moved(dy, dy_stride, y, y_stride, rows))
     return fail(ZS_EINVAL, "dy is in place of y at another stride");
+  if (rows > 0) st = check_apart(dy, "dy", dout, "dout");
+  if (st != ZS_OK) return st;
   zs::CombineBackwardArgs a{};
   a.dout = dout;
   a.y = y;
