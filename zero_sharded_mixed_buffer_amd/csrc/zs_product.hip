@@ -1,7 +1,12 @@
 // gfx950 kernels of the matrix products: a layer's products with an 8-bit weight (zs_product8), and
 // the experts' products over groups of rows (zs_expert_product, zs_expert_wgrad):
 //   c[m][n] = sum over k of a[m][k] * b[n][k]
-// on the matrix cores, summed in fp32.
+// on the matrix cores, summed in fp32.  16-bit products are exact in it.  The 8-bit instructions align up to
+// eight consecutive products to the largest and cut off what lies 2^-13 below it before they add the eight to
+// the fp32 sum: up to 7 * 2^-13 of the largest for each eight, and measured over whole sums about 2^-15.6 of
+// the result, where rounding it to fp16 takes 2^-12.2 (777 x 1003 -> 517: error against 64 bits 2.083e-4 of the
+// norm, 2.074e-4 for the exact sum rounded once).  Without the cut, in bf16, the product runs at the 16-bit
+// rate, at half the speed.
 //
 // An operand lies in memory with consecutive k (rows of m or n, "by rows"), or with consecutive m
 // or n (rows of k, "by k").  A stage of the sum is 128 bytes of every row, a cache line: 64 values of
@@ -929,18 +934,28 @@ hipError_t launch_few(const ProductArgs& a, hipStream_t s) {
   return a.m <= 16 * int64_t(a.groups) ? launch_few_rows<KIND, 1>(a, s) : launch_few_rows<KIND, 2>(a, s);
 }
 
-// Whether k_few is the better way: a unit of it takes k times 1.07 ns per 128 bytes (8 KB of operands),
-// a workgroup of the tiles below about 0.75 us for the same k as long as there are no more of them than
-// CUs.  Measured in 8 bits, k_few and tiles: 128 x 4096 -> 4096 (512 units) 22 and 26 us, 256 rows 40 and 26;
-// 512 x 1003 -> 517 (272 units) 8 and 12; 32 x 4096 -> 14336 (448 units) 34 and 36.
+// Whether k_few is the better way: past some 512 units its time goes with their number, while the tiles' time
+// stays that of one tile's stages (0.65 us each) as long as there are no more tiles than CUs.  Both go with k
+// alike, so the rule asks for the units alone.  Measured, us of k_few
+// and of tiles: 8 bits 64 x 4096 -> 4096 (256 units) 18 and 22, 128 rows (512) 22 and 22, 256 (1024) 39 and 23;
+// 128 x 14336 -> 4096 (512) 72 and 80, 256 (1024) 137 and 80; 512 x 1003 -> 517 (272) 8 and 12, 1024 (544) 11 and
+// 12; 512 x 512 -> 2048 (1024) 9 and 9.  16 bits: one expert 64 x 4096 -> 4096 (384) 26 and 37, 128 (640) 34 and
+// 38, 256 (1152) 63 and 39; 16 experts 512 x 4096 -> 448 (448) 29 and 37, 1024 (672) 41 and 38; 128 x 448 -> 4096
+// (2560) 18 and 13; 256 x 1024 -> 1024 (768) 10 and 13, 1024 (1536) 21 and 15.  So it is off by up to 40 % between
+// 512 and 1200 units of few stages or with many experts of few rows, which add a unit each.
 bool few_rows(const ProductArgs& a) { return product_units(a, false, 32, 32) <= kFewUnits; }
 
 using SmallTile = Tile<2, 2, 2, 2, 2>;  // 128 x 128, two workgroups to a CU
 using LargeTile = Tile<2, 4, 4, 2, 2>;  // 256 x 256, one workgroup to a CU
 
-// From how many large tiles on they are taken: below, too many CUs have none.  4096 -> 4096, 8 bits, us
-// with large and with small tiles: 2048 rows (128 large tiles) 52 and 38, 3000 rows (192) 56 and 62,
-// 4096 rows (256) 62 and 73; weight gradients 2048 rows of 1024 x 4096 (64) 43 and 33.
+// From how many large tiles on they are taken: below, too many CUs have none.  Measured, us with large and
+// with small tiles, at any length of the sum alike.  8 bits, 2048, 3000 and 4096 rows (128, 192, 256 large tiles):
+// 1024 -> 4096 22 and 15, 23 and 24, 23 and 27; 4096 -> 4096 52 and 39, 54 and 63, 60 and 72; 14336 -> 4096 146 and
+// 109, 156 and 184, 178 and 215.  16 bits, one expert, the same rows: 448 -> 4096 19 and 13, 19 and 21, 21 and 25;
+// 4096 -> 4096 71 and 64, 84 and 101, 102 and 125.  16384 rows over 16 experts of 4096 x 448: y (160) 74 and 64, dx
+// (1280) 78 and 92, dw (512) 64 and 83; 8 of 1024 x 1024: y (288) 33 and 40, dw (128) 41 and 38; 7811 over 18 of
+// 3200 x 4096: y (784) 226 and 263.  An expert's last tile counts as a whole one though half of it may be empty:
+// 16384 rows over 64 experts of 1024 x 512 (256) take 27 and 22.
 constexpr int64_t kLargeUnits = 192;
 
 // ------------------------------------------------------------------ launch choices

@@ -12,7 +12,8 @@
 As in the activation operators, the functions work on the current stream of their tensors' device,
 write into the tensors they are given, never wait for the GPU, and refuse a wrong type, shape,
 stride or device with a ValueError before anything is enqueued.  What a call writes counts as
-changed in place for autograd.
+changed in place for autograd.  The layers have a backward pass and no forward-mode derivative; a
+trace records them, and route, as one operation each.
 """
 
 from __future__ import annotations
