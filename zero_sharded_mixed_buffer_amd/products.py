@@ -29,6 +29,7 @@ from .activations import (_DTYPES, CODES, HALF, Act8, _add_in_turn, _at, _check_
                           _has_own_version, _input, _matrix, _need_gpu, _rows, _workspace, _wrote, act_wgrad)
 
 BLOCK = 128
+_transformed, _traced = torch._C._are_functorch_transforms_active, torch._C._get_tracing_state
 
 
 def _blocks(n):
@@ -257,7 +258,7 @@ def route(ids, experts, workspace=None):
     if ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
         raise ValueError("ids must be int32 or int64 and contiguous")
     _need_gpu(ids.device)
-    if _traced():
+    if _traced() is not None:
         return _route_of(*_Routed.apply(ids, int(experts), workspace))
     return _route_of(*_route(ids, int(experts), workspace))
 
@@ -368,11 +369,7 @@ def _differentiated(*tensors):
     for nothing, but forward-mode derivatives and function transforms are refused there, and a trace
     records the function (outside of it, the output's allocation alone)."""
     return (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
-            or forward_ad._current_level >= 0 or torch._C._are_functorch_transforms_active() or _traced())
-
-
-def _traced():
-    return torch._C._get_tracing_state() is not None
+            or forward_ad._current_level >= 0 or _transformed() or _traced() is not None)
 
 
 def _eights(x, weight, x8, w8, turned):
