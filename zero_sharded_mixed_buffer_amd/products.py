@@ -29,7 +29,7 @@ from .activations import (_DTYPES, CODES, HALF, Act8, _add_in_turn, _at, _check_
                           _has_own_version, _input, _matrix, _need_gpu, _rows, _workspace, _wrote, act_wgrad)
 
 BLOCK = 128
-_transformed, _traced = torch._C._are_functorch_transforms_active, torch._C._get_tracing_state
+_transformed, _traced = torch._C._are_functorch_transforms_active, torch._C._is_tracing
 
 
 def _blocks(n):
@@ -258,9 +258,9 @@ def route(ids, experts, workspace=None):
     if ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
         raise ValueError("ids must be int32 or int64 and contiguous")
     _need_gpu(ids.device)
-    if _traced() is not None:
+    if _traced():
         return _route_of(*_Routed.apply(ids, int(experts), workspace))
-    return _route_of(*_route(ids, int(experts), workspace))
+    return _route(ids, int(experts), workspace)
 
 
 def _route(ids, experts, workspace):
@@ -274,7 +274,7 @@ def _route(ids, experts, workspace):
              place.data_ptr(), workspace.data_ptr(), size)
     if not own:
         _wrote((workspace,))
-    return ends, slot, place
+    return _route_of(ends, slot, place)
 
 
 def _route_of(ends, slot, place):
@@ -289,9 +289,9 @@ class _Routed(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, ids, experts, workspace):
-        out = _route(ids, experts, workspace)
-        ctx.mark_non_differentiable(*out)
-        return out
+        r = _route(ids, experts, workspace)
+        ctx.mark_non_differentiable(r.ends, r.slot, r.place)
+        return r.ends, r.slot, r.place
 
     @staticmethod
     def backward(ctx, *grads):
@@ -299,9 +299,10 @@ class _Routed(torch.autograd.Function):
 
 
 def _routed(route, device):
-    if route.place.device != device:
-        raise ValueError(f"the route lives on {route.place.device}, not on {device}")
-    return route.tokens, route.choices
+    place = route.place
+    if place.device != device:
+        raise ValueError(f"the route lives on {place.device}, not on {device}")
+    return place.shape
 
 
 def _choice_weights(t, what, tokens, choices, device):
@@ -315,10 +316,11 @@ def expert_gather(x, route, out):
     """out[p] = the row of x [tokens, cols] (bf16, fp16 or fp32) whose choice lies at row p of the route;
     zeros in the rows of choices without expert."""
     tokens, cols, dev, xs = _input(x, "x", _DTYPES)
-    if _routed(route, dev)[0] != tokens:
-        raise ValueError(f"x has {tokens} rows, the route {route.tokens} tokens")
-    outs = _matrix(out, "out", x.dtype, route.rows, cols, dev)
-    _enqueue("zs_expert_gather", dev, x.data_ptr(), xs, _DTYPES[x.dtype], route.slot.data_ptr(), tokens, route.choices, cols,
+    routed, choices = _routed(route, dev)
+    if routed != tokens:
+        raise ValueError(f"x has {tokens} rows, the route {routed} tokens")
+    outs = _matrix(out, "out", x.dtype, tokens * choices, cols, dev)
+    _enqueue("zs_expert_gather", dev, x.data_ptr(), xs, _DTYPES[x.dtype], route.slot.data_ptr(), tokens, choices, cols,
              out.data_ptr(), outs)
     _wrote((out,))
 
@@ -327,13 +329,14 @@ def expert_combine(y, route, out, weights=None):
     """out[t] = the sum over token t's choices of weights[t][j] * the row of y that holds it, in fp32 and
     in the choices' order; weights: fp32 [tokens, choices], or None for ones."""
     tokens, cols, dev, outs = _input(out, "out", _DTYPES)
-    if _routed(route, dev)[0] != tokens:
-        raise ValueError(f"out has {tokens} rows, the route {route.tokens} tokens")
-    ys = _matrix(y, "y", out.dtype, route.rows, cols, dev)
+    routed, choices = _routed(route, dev)
+    if routed != tokens:
+        raise ValueError(f"out has {tokens} rows, the route {routed} tokens")
+    ys = _matrix(y, "y", out.dtype, tokens * choices, cols, dev)
     if weights is not None:
-        _choice_weights(weights, "weights", tokens, route.choices, dev)
+        _choice_weights(weights, "weights", tokens, choices, dev)
     _enqueue("zs_expert_combine", dev, y.data_ptr(), ys, _DTYPES[y.dtype], route.place.data_ptr(), _at(weights), tokens,
-             route.choices, cols, out.data_ptr(), outs)
+             choices, cols, out.data_ptr(), outs)
     _wrote((out,))
 
 
@@ -342,22 +345,23 @@ def expert_combine_backward(dout, y, route, weights=None, dy=None, dweights=None
     choices' dot products of dout and y (fp32 [tokens, choices]); each is written if it is given.  y
     is needed for dweights only."""
     tokens, cols, dev, ds = _input(dout, "dout", _DTYPES)
-    if _routed(route, dev)[0] != tokens:
-        raise ValueError(f"dout has {tokens} rows, the route {route.tokens} tokens")
+    routed, choices = _routed(route, dev)
+    if routed != tokens:
+        raise ValueError(f"dout has {tokens} rows, the route {routed} tokens")
     if dy is None and dweights is None:
         raise ValueError("neither dy nor dweights is given")
     ys = dys = 0
     if dweights is not None:
-        _choice_weights(dweights, "dweights", tokens, route.choices, dev)
+        _choice_weights(dweights, "dweights", tokens, choices, dev)
         if y is None:
             raise ValueError("dweights needs y")
-        ys = _matrix(y, "y", dout.dtype, route.rows, cols, dev)
+        ys = _matrix(y, "y", dout.dtype, tokens * choices, cols, dev)
     if weights is not None:
-        _choice_weights(weights, "weights", tokens, route.choices, dev)
+        _choice_weights(weights, "weights", tokens, choices, dev)
     if dy is not None:
-        dys = _matrix(dy, "dy", dout.dtype, route.rows, cols, dev)
+        dys = _matrix(dy, "dy", dout.dtype, tokens * choices, cols, dev)
     _enqueue("zs_expert_combine_backward", dev, dout.data_ptr(), ds, _at(y) if dweights is not None else None, ys,
-             _DTYPES[dout.dtype], route.slot.data_ptr(), route.place.data_ptr(), _at(weights), tokens, route.choices, cols,
+             _DTYPES[dout.dtype], route.slot.data_ptr(), route.place.data_ptr(), _at(weights), tokens, choices, cols,
              _at(dy), dys, _at(dweights))
     _wrote([t for t in (dy, dweights) if t is not None])
 
@@ -369,7 +373,7 @@ def _differentiated(*tensors):
     for nothing, but forward-mode derivatives and function transforms are refused there, and a trace
     records the function (outside of it, the output's allocation alone)."""
     return (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
-            or forward_ad._current_level >= 0 or _transformed() or _traced() is not None)
+            or forward_ad._current_level >= 0 or _transformed() or _traced())
 
 
 def _eights(x, weight, x8, w8, turned):
